@@ -27,7 +27,9 @@ EXPORTS = ("gemm_plan_create", "gemm_plan_create_config", "gemm_plan_create_ex",
            "gemm_run_host", "gemm_plan_destroy", "gemm_plan_status", "gemm_plan_describe", "gemm_last_error",
            "gemm_selftest_bounded_wait", "gemm_select_config", "gemm_run_noalloc", "gemm_selftest_device_call",
            "gemm_device_prepare",
-           "rowop_softmax", "rowop_rmsnorm", "rowop_layernorm")
+           "rowop_softmax", "rowop_rmsnorm", "rowop_layernorm",
+           "rowop_block_norm", "rowop_block_norm_workspace", "rowop_block_norm_backward",
+           "rowop_distill", "rowop_distill_backward", "rowop_verify", "rowop_verify_workspace")
 
 _lock = threading.Lock()
 _lib = None
@@ -81,6 +83,15 @@ def lib() -> ctypes.CDLL:
             L.rowop_rmsnorm.restype = i32
             L.rowop_layernorm.argtypes = [vp, i64, vp, vp, vp, i64, i64, i64, f32, vp]
             L.rowop_layernorm.restype = i32
+            for fn in (L.rowop_block_norm, L.rowop_distill, L.rowop_distill_backward, L.rowop_verify):
+                fn.argtypes = [vp, vp]
+                fn.restype = i32
+            L.rowop_block_norm_backward.argtypes = [vp, vp, vp]
+            L.rowop_block_norm_backward.restype = i32
+            L.rowop_block_norm_workspace.argtypes = [vp]
+            L.rowop_block_norm_workspace.restype = i64
+            L.rowop_verify_workspace.argtypes = [i64, i64, i64]
+            L.rowop_verify_workspace.restype = i64
             L.gemm_run_noalloc.restype = i32
             L.gemm_select_config.argtypes = [i64, i64, i64, i32, i32, i32, ctypes.c_char_p, i32]
             L.gemm_select_config.restype = i32
@@ -176,6 +187,106 @@ def rowop_rmsnorm(X, ldx: int, gamma, Y, ldy: int, rows: int, width: int, eps: f
 def rowop_layernorm(X, ldx: int, gamma, beta, Y, ldy: int, rows: int, width: int, eps: float = 1e-5,
                     stream=None) -> int:
     return lib().rowop_layernorm(_p(X), ldx, _p(gamma), _p(beta), _p(Y), ldy, rows, width, eps, _p(stream))
+
+
+# ---- row operators of language models (include/rowops.h) ----------------------
+
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+
+
+class _Args(ctypes.Structure):
+    """An argument struct of include/rowops.h, filled by keyword.
+
+    Pointers may be given as tensors (kept alive by the struct) or addresses,
+    element types and norms by name; fields not given are 0 or NULL. Fill it
+    once and pass it to any number of calls.
+    """
+
+    def __init__(self, **fields):
+        super().__init__()
+        self._keep = {}
+        for name, value in fields.items():
+            setattr(self, name, value)
+
+    def __setattr__(self, name, value):
+        kind = self._kinds.get(name)
+        if kind is None and name != "_keep":
+            raise AttributeError(f"{type(self).__name__} has no field {name}")
+        if kind is ctypes.c_void_p:
+            self._keep[name] = value
+            value = _p(value)
+        elif isinstance(value, str):
+            value = (NORMS if name.endswith("_norm") else C_TYPES)[value]
+        super().__setattr__(name, value)
+
+    @property
+    def address(self) -> int:
+        return ctypes.addressof(self)
+
+
+def _struct(name: str, layout: str, doc: str):
+    """The _Args class of a struct given as "type field field ...; type ..."."""
+    types = {"i64": ctypes.c_int64, "i32": ctypes.c_int32, "f32": ctypes.c_float, "ptr": ctypes.c_void_p}
+    fields = [(f, types[part.split()[0]]) for part in layout.split(";") for f in part.split()[1:]]
+    return type(name, (_Args,), {"_fields_": fields, "_kinds": dict(fields), "__doc__": doc})
+
+
+BlockNormArgs = _struct("BlockNormArgs", "i64 rows width; i32 block_type stream_type gate_type post_norm pre_norm;"
+                        "f32 post_eps pre_eps residual_scale branch_scale; ptr x; i64 ldx; ptr y; i64 ldy;"
+                        "ptr post_gamma post_beta pre_gamma pre_beta gate; i64 ldg rows_per_gate; ptr h; i64 ldh; ptr z;"
+                        "i64 ldz; ptr post_stats pre_stats", "rowop_block_norm_args")
+BlockNormGrads = _struct("BlockNormGrads", "ptr dh; i64 lddh; ptr dz; i64 lddz; ptr dx; i64 lddx; ptr dy; i64 lddy;"
+                         "ptr dgate; i64 lddg; ptr dpost_gamma dpost_beta dpre_gamma dpre_beta workspace;"
+                         "i64 workspace_bytes", "rowop_block_norm_grads")
+DistillArgs = _struct("DistillArgs", "i64 rows vocab k; i32 logits_type teacher_type; f32 temperature; ptr logits;"
+                      "i64 ldl; ptr ids; i64 ldi; ptr teacher; i64 ldt; ptr teacher_lse weight loss lse dloss dlogits;"
+                      "i64 ldd", "rowop_distill_args")
+VerifyArgs = _struct("VerifyArgs", "i64 batch drafts vocab; i32 logits_type; f32 temperature draft_temperature;"
+                     "ptr target; i64 ldt; ptr draft; i64 ldq; ptr tokens lengths uniforms noise; i64 ldn;"
+                     "ptr accepted out logprobs workspace; i64 workspace_bytes", "rowop_verify_args")
+
+
+def _a(args: _Args | None) -> int | None:
+    return None if args is None else args.address
+
+
+def rowop_block_norm(args: BlockNormArgs, stream=None) -> int:
+    """Norm after a block, gate, residual, norm before the next block (see include/rowops.h)."""
+    return lib().rowop_block_norm(_a(args), _p(stream))
+
+
+def rowop_block_norm_workspace(args: BlockNormArgs) -> int:
+    """Scratch bytes of rowop_block_norm_backward."""
+    return _size(lib().rowop_block_norm_workspace(_a(args)))
+
+
+def rowop_block_norm_backward(args: BlockNormArgs, grads: BlockNormGrads, stream=None) -> int:
+    return lib().rowop_block_norm_backward(_a(args), _a(grads), _p(stream))
+
+
+def rowop_distill(args: DistillArgs, stream=None) -> int:
+    """Loss against a teacher's top logits, and its gradient where dlogits is given (see include/rowops.h)."""
+    return lib().rowop_distill(_a(args), _p(stream))
+
+
+def rowop_distill_backward(args: DistillArgs, stream=None) -> int:
+    return lib().rowop_distill_backward(_a(args), _p(stream))
+
+
+def rowop_verify(args: VerifyArgs, stream=None) -> int:
+    """Accept or refuse drafted tokens and draw the next one (see include/rowops.h)."""
+    return lib().rowop_verify(_a(args), _p(stream))
+
+
+def rowop_verify_workspace(batch: int, drafts: int, vocab: int) -> int:
+    """Scratch bytes of rowop_verify."""
+    return _size(lib().rowop_verify_workspace(batch, drafts, vocab))
+
+
+def _size(n: int) -> int:
+    if n < 0:
+        raise GemmError(n, gemm_last_error())
+    return n
 
 
 def gemm_plan_destroy(plan: int) -> None:

@@ -26,7 +26,9 @@ STAMP = os.path.join(LIB_DIR, "libsatgemm.stamp")
 # The kernel variants come as three translation units per dtype (they take
 # most of the build); the longest units are listed first.
 SOURCES = [f"kernels_{dt}{grp}.cu" for grp in ("", "_alt", "_trans") for dt in ("tf32", "bf16", "fp16")] + [
-    "device_call.cu", "api.cu", "aux_kernels.cu", "dispatch.cpp", "tensor_map.cpp", "noalloc.cu", "rowops.cu"]
+    "device_call.cu", "api.cu", "aux_kernels.cu", "dispatch.cpp", "tensor_map.cpp", "noalloc.cu", "rowops.cu", "blocknorm.cu", "blocknorm_f32.cu",
+    "blocknorm_bf16.cu", "blocknorm_f16.cu",
+    "distill.cu", "verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 # The GEMM kernel units: an explicit register ceiling (the launch bounds of
@@ -71,7 +73,8 @@ def source_hash() -> str:
 
 
 # Sources of the row operators only: no GEMM kernel includes or calls them.
-_ROWOP_ONLY = ("rowops.cu", "rowops.h")
+_ROWOP_ONLY = ("rowops.cu", "rowops.h", "rows.cuh", "blocknorm.h", "blocknorm.cuh", "blocknorm.cu", "blocknorm_f32.cu",
+                "blocknorm_bf16.cu", "blocknorm_f16.cu", "distill.cu", "verify.cu")
 
 
 def gemm_source_hash() -> str:

@@ -1,0 +1,218 @@
+// What the row operators of language models share: element types, loads and
+// stores of eight elements, reductions over a CTA, and checks of arguments.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "registry.h"
+#include "rowops.h"
+
+namespace sat {
+namespace rows {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v)
+{
+    if constexpr (std::is_same_v<T, float>)
+        return v;
+    else if constexpr (std::is_same_v<T, __half>)
+        return __float2half_rn(v);
+    else
+        return __float2bfloat16_rn(v);
+}
+
+// Eight consecutive elements as they lie in memory, 16 or 32 bytes, moved by
+// one instruction (256-bit global loads and stores for fp32). The address is
+// aligned to the eight elements.
+template <typename T>
+struct Pack {
+    uint32_t w[2 * sizeof(T)];
+};
+
+template <typename T>
+__device__ __forceinline__ Pack<T> load_pack(const T* p)
+{
+    Pack<T> v;
+    if constexpr (sizeof(T) == 4)
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]),
+                       "=r"(v.w[6]), "=r"(v.w[7])
+                     : "l"(p));
+    else
+        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3])
+                     : "l"(p));
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_pack(T* p, const Pack<T>& v)
+{
+    if constexpr (sizeof(T) == 4)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v.w[0]), "r"(v.w[1]),
+                     "r"(v.w[2]), "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]), "r"(v.w[7])
+                     : "memory");
+    else
+        asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.w[0]), "r"(v.w[1]), "r"(v.w[2]),
+                     "r"(v.w[3])
+                     : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(const Pack<T>& v, float (&out)[8])
+{
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            out[e] = __uint_as_float(v.w[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint16_t bits = static_cast<uint16_t>(v.w[e / 2] >> (16 * (e % 2)));
+            if constexpr (std::is_same_v<T, __half>)
+                out[e] = __half2float(__ushort_as_half(bits));
+            else
+                out[e] = __bfloat162float(__ushort_as_bfloat16(bits));
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ Pack<T> pack(const float (&in)[8])
+{
+    Pack<T> v;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v.w[e] = __float_as_uint(in[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (std::is_same_v<T, __half>) {
+                const __half2 h = __floats2half2_rn(in[2 * e], in[2 * e + 1]);
+                v.w[e] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(in[2 * e], in[2 * e + 1]);
+                v.w[e] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+    }
+    return v;
+}
+
+// Sums of N values over the NT threads that share a row, returned to each of
+// them, in a fixed order: lanes by shuffles, then (NT > 32) warps through
+// `scratch`, 2 x N x NT / 32 floats. Consecutive reductions alternate between
+// its halves, so one barrier each suffices: a half is rewritten two
+// reductions later, after a barrier that every thread passed after reading it.
+template <int NT, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float* scratch, int& turn)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if constexpr (NT > 32) {
+        constexpr int W = NT / 32;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        float* half = scratch + turn * (N * W);
+        turn ^= 1;
+        if (lane == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                half[i * W + warp] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = lane < W ? half[i * W + lane] : 0.0f;
+#pragma unroll
+        for (int o = W / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        if constexpr (W < 32)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[i] = __shfl_sync(0xffffffffu, v[i], 0);
+    }
+}
+
+// The running maximum and sum of exponentials of a softmax: sum is of
+// exp2((v - max) scale) over the values seen, with max -inf for none.
+struct Softmax {
+    float max = -INFINITY, sum = 0.0f;
+
+    __device__ __forceinline__ void add(float v, float scale)
+    {
+        if (v > max) {
+            sum = sum * exp2f((max - v) * scale) + 1.0f;
+            max = v;
+        } else if (v != -INFINITY) {  // a NaN comes here and stays in the sum
+            sum += exp2f((v - max) * scale);
+        }
+    }
+
+    __device__ __forceinline__ void add(const Softmax& o, float scale)
+    {
+        const float m = fmaxf(max, o.max);
+        // A side that has seen nothing but -inf keeps its sum of 0 (or NaN).
+        sum = (max == m ? sum : sum * exp2f((max - m) * scale)) + (o.max == m ? o.sum : o.sum * exp2f((o.max - m) * scale));
+        max = m;
+    }
+};
+
+// The softmax over what the NT threads of a CTA have seen, returned to each of
+// them, in a fixed order. `scratch` holds NT / 32 of them; free after a barrier.
+template <int NT>
+__device__ __forceinline__ Softmax cta_softmax(Softmax s, float scale, Softmax* scratch)
+{
+    auto step = [&](int o) {
+        Softmax u;
+        u.max = __shfl_xor_sync(0xffffffffu, s.max, o);
+        u.sum = __shfl_xor_sync(0xffffffffu, s.sum, o);
+        // Both lanes of a pair add in the same order and get the same bits.
+        if (threadIdx.x & o) {
+            u.add(s, scale);
+            s = u;
+        } else {
+            s.add(u, scale);
+        }
+    };
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        step(o);
+    if ((threadIdx.x & 31) == 0)
+        scratch[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = Softmax();
+    if ((threadIdx.x & 31) < NT / 32)
+        s = scratch[threadIdx.x & 31];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        step(o);
+    return s;
+}
+
+// ---- host: argument checks ------------------------------------------------------
+
+inline bool type_ok(int t) { return t == GEMM_C_F32 || t == GEMM_C_BF16 || t == GEMM_C_F16; }
+inline int type_bytes(int t) { return t == GEMM_C_F32 ? 4 : 2; }
+inline bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Whether all rows start on a boundary of eight elements (a matrix that is not there does).
+inline bool packs(const void* p, int64_t ld, int type) { return !p || (aligned(p, 8 * type_bytes(type)) && ld % 8 == 0); }
+
+}  // namespace rows
+}  // namespace sat
