@@ -228,12 +228,6 @@ cudaError_t choose_forward(const rowop_block_norm_args& a, cudaStream_t s)
 
 // ---- backward ----------------------------------------------------------------------
 
-// Stores to shared memory of any CTA of the cluster.
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
-{
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
 // The NT threads of CTA `rank` of a cluster of `ctas` take columns
 // [rank NT 8, (rank + 1) NT 8) of a row, eight each, and go through one part's
 // rows in order, with the sums over rows of their own columns in registers.
@@ -283,6 +277,9 @@ __global__ void __launch_bounds__(NT == 32 ? 128 : NT)
     const float* post_gamma = post && a.post_gamma ? a.post_gamma + off : nullptr;
     const float* pre_gamma = pre && a.pre_gamma ? a.pre_gamma + off : nullptr;
     float acc[kBeta ? kSums : kPreBeta][8] = {};
+    if constexpr (NT == 512)
+        if (ctas > 1)
+            cluster_sync();  // the others have started, and may be written to
     int64_t first, end;
     split.range(part, a.rows, first, end);
     int64_t flush = split.direct ? min((first / a.rows_per_gate + 1) * a.rows_per_gate, end) : end;

@@ -1,4 +1,15 @@
 // Distillation from a teacher's top logits and its gradient (include/rowops.h).
+//
+// A row's logits are cut into slices that lie in shared memory while a CTA
+// works on them: fetched by bulk copies (all of a slice in flight at once),
+// reduced to a maximum and a sum of exponentials chunk by chunk as they
+// land, and, for the gradient, read a second time from there. The CTAs of a
+// cluster take a row's slices and put their maxima and sums together through
+// distributed shared memory, so a row that no SM could hold is read from
+// memory once and its gradient written once: 4 bytes a token in 16-bit
+// types, which HBM bandwidth bounds. Slices are cut on 16-byte boundaries of
+// memory, wherever the row starts; the ragged ends move by plain loads.
+#include "ptx.cuh"
 #include "rows.cuh"
 
 namespace {
@@ -6,7 +17,20 @@ namespace {
 using namespace sat;
 using namespace sat::rows;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kChunk = 16384;       // bytes of a bulk copy with its own barrier
+constexpr int kMaxSlice = 65536;    // so that three CTAs' slices fit an SM
+constexpr int kMaxChunks = kMaxSlice / kChunk;
+constexpr int kMaxCluster = 16;
+constexpr int kWaitLimit = 1 << 22;  // polls of a barrier, each of which the hardware suspends for a while
+
+enum Mode { kLoss, kBoth, kGrad };
+
+// A row's slices, `bytes` each from the 16-byte boundary at or before its
+// start. CTA `rank` of the row's `ctas` takes slices rank, rank + ctas, ...
+struct Slices {
+    int bytes, ctas, per_row;
+};
 
 template <typename T>
 __device__ __forceinline__ float teacher_at(const void* p, int64_t i)
@@ -21,99 +45,250 @@ __device__ __forceinline__ float teacher_logit(const rowop_distill_args& a, int6
                                            : teacher_at<__half>(a.teacher, i);
 }
 
-// One CTA a row: the teacher's entries into shared memory, the student's
-// softmax in one pass over its logits, the gradient in a second.
-template <typename T, bool kForward>
-__global__ void __launch_bounds__(kThreads) sat_distill_kernel(const __grid_constant__ rowop_distill_args a)
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
 {
-    __shared__ Softmax scratch[kThreads / 32];
-    __shared__ float sums[2 * 2 * (kThreads / 32)];
-    __shared__ int id[ROWOP_DISTILL_MAX_K];    // -1 for an absent entry
-    __shared__ float p[ROWOP_DISTILL_MAX_K];   // the teacher's probability
-    __shared__ float at[ROWOP_DISTILL_MAX_K];  // the student's logit
-    int turn = 0;
-    const int k = static_cast<int>(a.k);
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kThreads)
+    sat_distill_kernel(const __grid_constant__ rowop_distill_args a, const Slices cut)
+{
+    constexpr int N = kPer16<T>;
+    extern __shared__ __align__(128) unsigned char slice[];
+    float* p = reinterpret_cast<float*>(slice + cut.bytes);  // the teacher's probabilities
+    float* log_p = p + a.k;                                  // its logits, then log probabilities
+    float* at_id = log_p + a.k;                              // the student's logits there (for the loss)
+    int* id = reinterpret_cast<int*>(at_id + a.k);           // -1 for an absent entry
+    __shared__ __align__(8) uint64_t bars[kMaxChunks];
+    __shared__ Softmax scratch[2][kWarps];
+    __shared__ float sums[2 * kWarps];
+    __shared__ Softmax across[kMaxCluster];
+    const int rank = blockIdx.x % cut.ctas, k = static_cast<int>(a.k);
+    const int64_t r = blockIdx.x / cut.ctas;
+    const float weight = a.weight ? a.weight[r] : 1.0f;
     const float scale = kLog2e / a.temperature, inv_t = 1.0f / a.temperature;
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        __syncthreads();  // the previous row's entries are no longer read
-        const T* s = static_cast<const T*>(a.logits) + r * a.ldl;
-        T* d = a.dlogits ? static_cast<T*>(a.dlogits) + r * a.ldd : nullptr;
-        const float weight = a.weight ? a.weight[r] : 1.0f;
-        Softmax t;
+    const T* row = static_cast<const T*>(a.logits) + r * a.ldl;
+    T* out = a.dlogits ? static_cast<T*>(a.dlogits) + r * a.ldd : nullptr;
+    // The row, and the slices, as addresses.
+    const uint64_t start = reinterpret_cast<uint64_t>(row), base = start & ~15ull, stop = start + a.vocab * sizeof(T);
+    int phase = 0, packs = 0;
+    int64_t first = 0;  // the element that the slice's first pack starts with (negative where that is before the row)
+
+    // Starts the copies of slice i; every thread then knows its first element and number of packs.
+    auto fetch = [&](int i) {
+        const uint64_t at = base + static_cast<uint64_t>(i) * cut.bytes;
+        const uint64_t lo = at > start ? at : start;
+        uint64_t hi = at + cut.bytes < stop ? at + cut.bytes : stop;
+        hi = hi > at ? hi : at;  // the last slice may have nothing, as the row may start on any byte of its first 16
+        const uint64_t lo16 = (lo + 15) & ~15ull, hi16 = hi & ~15ull;
+        first = (static_cast<int64_t>(at) - static_cast<int64_t>(start)) / static_cast<int64_t>(sizeof(T));
+        packs = static_cast<int>((hi - at + 15) / 16);
+        if (threadIdx.x == 0) {
+            for (int c = 0; c < kMaxChunks; ++c) {
+                const uint64_t from = at + c * kChunk;
+                const uint64_t b = from > lo16 ? from : lo16, e = from + kChunk < hi16 ? from + kChunk : hi16;
+                const uint32_t bytes = b < e ? static_cast<uint32_t>(e - b) : 0;
+                mbar_arrive_expect_tx(smem_u32(&bars[c]), bytes);
+                if (bytes)
+                    bulk_load(smem_u32(slice) + static_cast<uint32_t>(b - at), reinterpret_cast<const void*>(b), bytes,
+                              smem_u32(&bars[c]));
+            }
+        }
+        // The ends: elements of the packs that are not whole; -inf where there is none.
+        if (threadIdx.x >= 32 && threadIdx.x < 32 + 2 * N) {
+            const int e = (threadIdx.x - 32) % N;
+            const uint64_t pack = threadIdx.x - 32 < N ? lo & ~15ull : hi & ~15ull;
+            const uint64_t x = pack + e * sizeof(T);
+            const bool whole = pack >= lo && pack + 16 <= hi;
+            if (!whole && pack < at + cut.bytes && (threadIdx.x - 32 < N || pack != (lo & ~15ull)))
+                *reinterpret_cast<T*>(slice + (x - at)) =
+                    x >= lo && x < hi ? *reinterpret_cast<const T*>(x) : from_f32<T>(-INFINITY);
+        }
+    };
+    // Into a slice that has been read, and had its ends written, by ordinary instructions.
+    auto refetch = [&](int i) {
+        fence_proxy_async_smem();
+        __syncthreads();
+        fetch(i);
+    };
+    bool failed = false;
+    auto wait = [&](int c) {
+        int n = 0;
+        while (!mbar_try_wait<false>(smem_u32(&bars[c]), phase))
+            if (++n > kWaitLimit) {
+                failed = true;
+                break;
+            }
+    };
+    // Writes f(logit) for the elements of the slice, pack by pack.
+    auto write = [&](auto f) {
+        const bool aligned16 = ((reinterpret_cast<uint64_t>(out) ^ start) & 15) == 0;
+        for (int i = threadIdx.x; i < packs; i += kThreads) {
+            float v[N];
+            unpack16<T>(reinterpret_cast<const uint4*>(slice)[i], v);
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                v[e] = f(v[e]);
+            const int64_t j = first + static_cast<int64_t>(i) * N;
+            if (aligned16 && j >= 0 && j + N <= a.vocab) {
+                *reinterpret_cast<uint4*>(out + j) = pack16<T>(v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    if (j + e >= 0 && j + e < a.vocab)
+                        out[j + e] = from_f32<T>(v[e]);
+            }
+        }
+    };
+    auto write_zeros = [&] {
+        for (int64_t j = rank * static_cast<int64_t>(kThreads) + threadIdx.x; j < a.vocab; j += cut.ctas * kThreads)
+            out[j] = from_f32<T>(0.0f);
+    };
+
+    if (weight == 0.0f) {  // alike for all CTAs of the cluster
+        if (MODE != kGrad && rank == 0 && threadIdx.x == 0) {
+            a.loss[r] = 0.0f;
+            if (a.lse)
+                a.lse[r] = 0.0f;
+        }
+        if (MODE != kLoss)
+            write_zeros();
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int c = 0; c < kMaxChunks; ++c)
+            mbar_init(smem_u32(&bars[c]), 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    const bool any = rank < cut.per_row;
+    if (any)
+        fetch(rank);
+    __syncwarp();
+    if (MODE != kGrad && cut.ctas > 1)
+        cluster_arrive();  // waited for before the first store to another CTA, which has to have started by then
+
+    // The teacher's entries, while the first slice is on its way.
+    bool empty = false;
+    float sum[1] = {0.0f};
+    int turn = 0;
+    if (MODE != kLoss || rank == 0) {
+        Softmax t = Softmax::none();
         for (int i = threadIdx.x; i < k; i += kThreads) {
             const int token = a.ids[r * a.ldi + i];
-            const float v = teacher_logit(a, r * a.ldt + i);
-            const bool there = token >= 0 && token < a.vocab && v != -INFINITY;
+            const float v[1] = {teacher_logit(a, r * a.ldt + i)};
+            const bool there = token >= 0 && token < a.vocab && v[0] != -INFINITY;
             id[i] = there ? token : -1;
-            p[i] = v;
+            log_p[i] = v[0];
+            // Before any CTA of the cluster writes its part of the gradient, which may be in the logits' place.
+            if (MODE != kGrad && rank == 0)
+                at_id[i] = there ? to_f32(row[token]) : 0.0f;
             if (there)
                 t.add(v, scale);
         }
-        t = cta_softmax<kThreads>(t, scale, scratch);
-        if (weight == 0.0f || t.max == -INFINITY) {
-            if (kForward && threadIdx.x == 0) {
-                a.loss[r] = 0.0f;
-                if (a.lse)
-                    a.lse[r] = 0.0f;
-            }
-            if (d)
-                for (int j = threadIdx.x; j < a.vocab; j += kThreads)
-                    d[j] = from_f32<T>(0.0f);
-            continue;
-        }
-        Softmax q;
-        if (kForward) {
-            for (int j = threadIdx.x; j < a.vocab; j += kThreads)
-                q.add(to_f32(s[j]), scale);
-            __syncthreads();  // scratch has been read
-            q = cta_softmax<kThreads>(q, scale, scratch);
-        } else {
-            q.max = a.lse[r] * a.temperature;
-            q.sum = 1.0f;
-        }
-        // log p_i = (T_i - L') / t with L' the largest of T, and so on.
-        const float top = a.teacher_lse ? a.teacher_lse[r] : t.max * inv_t + logf(t.sum);
-        const float log_sum = logf(q.sum);
-        float sum[2] = {0.0f, 0.0f};  // of p, and of p (log p - log q)
+        t = cta_softmax<kThreads>(t, scale, scratch[0]);
+        empty = t.max == -INFINITY;
+        const float top = a.teacher_lse ? 0.0f : t.max, rest = a.teacher_lse ? a.teacher_lse[r] : logf(t.sum);
         for (int i = threadIdx.x; i < k; i += kThreads) {
-            float pi = 0.0f;
-            if (id[i] >= 0) {
-                const float log_p = a.teacher_lse ? fmaf(p[i], inv_t, -top) : (p[i] - t.max) * inv_t - logf(t.sum);
-                pi = expf(log_p);
-                at[i] = to_f32(s[id[i]]);
-                if (pi > 0.0f)
-                    sum[1] += pi * (log_p - ((at[i] - q.max) * inv_t - log_sum));
-                sum[0] += pi;
-            }
-            p[i] = pi;
+            log_p[i] = (log_p[i] - top) * inv_t - rest;
+            p[i] = id[i] >= 0 ? expf(log_p[i]) : 0.0f;
+            sum[0] += p[i];
         }
         row_sums<kThreads>(sum, sums, turn);
-        if (kForward && threadIdx.x == 0) {
-            a.loss[r] = weight * a.temperature * a.temperature * sum[1];
-            if (a.lse)
-                a.lse[r] = q.max * inv_t + log_sum;
-        }
-        if (!d)
-            continue;
-        const float c = (a.dloss ? a.dloss[r] : 1.0f) * weight * a.temperature;
-        const float log2_sum = log_sum * kLog2e;
-        auto whole = [&](float v) { return sum[0] * exp2f(fmaf(v - q.max, scale, -log2_sum)); };
-        for (int j = threadIdx.x; j < a.vocab; j += kThreads)
-            d[j] = from_f32<T>(c * whole(to_f32(s[j])));
-        __syncthreads();
-        // The teacher's tokens, each once: by the first of the entries that name it.
-        for (int i = threadIdx.x; i < k; i += kThreads) {
-            if (id[i] < 0)
-                continue;
-            bool first = true;
-            float pi = 0.0f;
-            for (int l = 0; l < k; ++l)
-                if (id[l] == id[i]) {
-                    first = first && l >= i;
-                    pi += p[l];
+    }
+
+    Softmax q = Softmax::none();
+    if (MODE != kGrad) {
+        for (int i = rank; i < cut.per_row; i += cut.ctas) {
+            if (i != rank)
+                refetch(i);
+            __syncthreads();  // the ends are written
+            for (int c = 0; c < kMaxChunks; ++c) {
+                wait(c);
+                const int end = min(packs, (c + 1) * (kChunk / 16));
+                for (int j = c * (kChunk / 16) + threadIdx.x; j < end; j += kThreads) {
+                    float v[N];
+                    unpack16<T>(reinterpret_cast<const uint4*>(slice)[j], v);
+                    q.add(v, scale);
                 }
-            if (first)
-                d[id[i]] = from_f32<T>(c * (whole(at[i]) - pi));
+            }
+            phase ^= 1;
+        }
+        if (failed)
+            q.sum = NAN;
+        q = cta_softmax<kThreads>(q, scale, scratch[1]);
+        if (cut.ctas > 1) {
+            cluster_wait();
+            if (threadIdx.x < cut.ctas) {
+                const uint32_t at = map_to_cta(smem_u32(&across[rank]), threadIdx.x);
+                st_cluster_f32(at, q.max);
+                st_cluster_f32(at + 4, q.sum);
+            }
+            __syncwarp();
+            cluster_sync();
+            q = across[0];
+            for (int c = 1; c < cut.ctas; ++c)
+                q.add(across[c], scale);
+        }
+        const float log_sum = logf(q.sum);
+        if (rank == 0) {
+            float loss[1] = {0.0f};
+            for (int i = threadIdx.x; i < k; i += kThreads)
+                if (p[i] > 0.0f)
+                    loss[0] += p[i] * (log_p[i] - ((at_id[i] - q.max) * inv_t - log_sum));
+            row_sums<kThreads>(loss, sums, turn);
+            if (threadIdx.x == 0) {
+                a.loss[r] = empty ? 0.0f : weight * a.temperature * a.temperature * loss[0];
+                if (a.lse)
+                    a.lse[r] = empty ? 0.0f : q.max * inv_t + log_sum;
+            }
+        }
+    }
+    if (MODE == kLoss)
+        return;
+    if (empty) {
+        if (MODE == kGrad && any)  // the copies have to land before the CTA ends
+            for (int c = 0; c < kMaxChunks; ++c)
+                wait(c);
+        write_zeros();
+        return;
+    }
+    const float c = (a.dloss ? a.dloss[r] : 1.0f) * weight * a.temperature;
+    const float lse = MODE == kGrad ? a.lse[r] : 0.0f, share = MODE == kGrad ? c * sum[0] : c * sum[0] / q.sum;
+    auto whole = [&](float v) {
+        return share * (MODE == kGrad ? ex2(fmaf(v, inv_t, -lse) * kLog2e) : ex2((v - q.max) * scale));
+    };
+    const bool resident = MODE == kBoth && cut.per_row <= cut.ctas;
+    for (int i = rank; i < cut.per_row; i += cut.ctas) {
+        if (!resident) {
+            if (MODE == kBoth || i != rank)
+                refetch(i);
+            __syncthreads();
+            for (int n = 0; n < kMaxChunks; ++n)
+                wait(n);
+            phase ^= 1;
+            if (failed)
+                return;
+        }
+        write(whole);
+        __syncthreads();
+        // The teacher's tokens within the slice, each once: by the first of the entries that name it.
+        const int64_t last = min(first + static_cast<int64_t>(packs) * N, a.vocab);
+        for (int n = threadIdx.x; n < k; n += kThreads) {
+            if (id[n] < max(first, int64_t{0}) || id[n] >= last)
+                continue;
+            bool lowest = true;
+            float pn = 0.0f;
+            for (int l = 0; l < k; ++l)
+                if (id[l] == id[n]) {
+                    lowest = lowest && l >= n;
+                    pn += p[l];
+                }
+            if (lowest)
+                out[id[n]] = from_f32<T>(whole(to_f32(reinterpret_cast<const T*>(slice)[id[n] - first])) - c * pn);
         }
     }
 }
@@ -126,6 +301,8 @@ int check(const rowop_distill_args* a, bool forward)
         return fail_with(GEMM_ERR_ARG, "negative size");
     if (a->rows == 0)
         return GEMM_OK;
+    if (a->rows > (1 << 26))
+        return fail_with(GEMM_ERR_ARG, "rows %lld is above 2^26", (long long)a->rows);
     if (a->vocab < 1 || a->vocab > (INT64_C(1) << 30))
         return fail_with(GEMM_ERR_ARG, "vocab %lld is not within 1 .. 2^30", (long long)a->vocab);
     if (a->k > ROWOP_DISTILL_MAX_K)
@@ -147,22 +324,47 @@ int check(const rowop_distill_args* a, bool forward)
     return GEMM_OK;
 }
 
-template <bool kForward>
-int run(const rowop_distill_args* a, void* stream)
+template <typename T, int MODE>
+cudaError_t launch(const rowop_distill_args& a, cudaStream_t s)
 {
-    set_last_error("");
-    const int rc = check(a, kForward);
-    if (rc || a->rows == 0)
-        return rc;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned grid = static_cast<unsigned>(a->rows < (1 << 20) ? a->rows : (1 << 20));
-    if (a->logits_type == GEMM_C_F32)
-        sat_distill_kernel<float, kForward><<<grid, kThreads, 0, s>>>(*a);
-    else if (a->logits_type == GEMM_C_BF16)
-        sat_distill_kernel<__nv_bfloat16, kForward><<<grid, kThreads, 0, s>>>(*a);
-    else
-        sat_distill_kernel<__half, kForward><<<grid, kThreads, 0, s>>>(*a);
-    const cudaError_t e = cudaGetLastError();
+    const int64_t bytes = a.vocab * static_cast<int64_t>(sizeof(T)) + 15;
+    // Slices of a cluster's CTAs: of 64 KB at most, so that three CTAs share an
+    // SM and one's copies overlap another's arithmetic; smaller, down to 4 KB,
+    // where there are too few rows to fill the GPU with two CTAs per SM.
+    Slices cut;
+    cut.ctas = 1;
+    while (cut.ctas < kMaxCluster && (bytes > static_cast<int64_t>(cut.ctas) * kMaxSlice ||
+                                      (a.rows * cut.ctas < 304 && bytes > static_cast<int64_t>(cut.ctas) * 4096)))
+        cut.ctas *= 2;
+    const int64_t each = (bytes + cut.ctas - 1) / cut.ctas;
+    cut.bytes = static_cast<int>(each < kMaxSlice ? (each + 127) / 128 * 128 : kMaxSlice);
+    cut.per_row = static_cast<int>((bytes + cut.bytes - 1) / cut.bytes);
+    const int smem = cut.bytes + static_cast<int>(a.k) * 16;
+    auto kernel = sat_distill_kernel<T, MODE>;
+    static Prepared prepared;
+    const cudaError_t e = prepared.once(reinterpret_cast<const void*>(kernel), kMaxSlice + ROWOP_DISTILL_MAX_K * 16);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = MODE == kGrad ? 1 : static_cast<unsigned>(cut.ctas);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(a.rows * cut.ctas));
+    return cudaLaunchKernelEx(&cfg, kernel, a, cut);
+}
+
+template <int MODE>
+int run(const rowop_distill_args& a, cudaStream_t s)
+{
+    const cudaError_t e = a.logits_type == GEMM_C_F32    ? launch<float, MODE>(a, s)
+                          : a.logits_type == GEMM_C_BF16 ? launch<__nv_bfloat16, MODE>(a, s)
+                                                         : launch<__half, MODE>(a, s);
     return e == cudaSuccess ? GEMM_OK
                             : fail_with(GEMM_ERR_LAUNCH, "launching the distillation kernel: %s", cudaGetErrorString(e));
 }
@@ -171,8 +373,23 @@ int run(const rowop_distill_args* a, void* stream)
 
 extern "C" {
 
-int rowop_distill(const rowop_distill_args* args, void* stream) { return run<true>(args, stream); }
+int rowop_distill(const rowop_distill_args* args, void* stream)
+{
+    set_last_error("");
+    const int rc = check(args, true);
+    if (rc || args->rows == 0)
+        return rc;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return args->dlogits ? run<kBoth>(*args, s) : run<kLoss>(*args, s);
+}
 
-int rowop_distill_backward(const rowop_distill_args* args, void* stream) { return run<false>(args, stream); }
+int rowop_distill_backward(const rowop_distill_args* args, void* stream)
+{
+    set_last_error("");
+    const int rc = check(args, false);
+    if (rc || args->rows == 0)
+        return rc;
+    return run<kGrad>(*args, static_cast<cudaStream_t>(stream));
+}
 
 }  // extern "C"

@@ -6,9 +6,11 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
+#include "ptx.cuh"
 #include "registry.h"
 #include "rowops.h"
 
@@ -111,6 +113,35 @@ __device__ __forceinline__ Pack<T> pack(const float (&in)[8])
     return v;
 }
 
+// Sixteen bytes as they lie in memory, and their elements.
+template <typename T>
+constexpr int kPer16 = 16 / sizeof(T);
+
+template <typename T>
+__device__ __forceinline__ void unpack16(const uint4& w, float (&out)[kPer16<T>])
+{
+    if constexpr (sizeof(T) == 4) {
+        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            out[e] = __uint_as_float(words[e]);
+    } else {
+        Pack<T> v = {{w.x, w.y, w.z, w.w}};
+        unpack(v, out);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack16(const float (&in)[kPer16<T>])
+{
+    if constexpr (sizeof(T) == 4) {
+        return make_uint4(__float_as_uint(in[0]), __float_as_uint(in[1]), __float_as_uint(in[2]), __float_as_uint(in[3]));
+    } else {
+        const Pack<T> v = pack<T>(in);
+        return make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    }
+}
+
 // Sums of N values over the NT threads that share a row, returned to each of
 // them, in a fixed order: lanes by shuffles, then (NT > 32) warps through
 // `scratch`, 2 x N x NT / 32 floats. Consecutive reductions alternate between
@@ -149,26 +180,48 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* scratch, int& tur
     }
 }
 
+// 2^x, flushing what is below the smallest normal number to 0 (relative error
+// about 2^-22; one instruction, where exp2f adds the care for subnormals).
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // The running maximum and sum of exponentials of a softmax: sum is of
 // exp2((v - max) scale) over the values seen, with max -inf for none.
 struct Softmax {
-    float max = -INFINITY, sum = 0.0f;
+    float max, sum;
 
-    __device__ __forceinline__ void add(float v, float scale)
+    static __device__ __forceinline__ Softmax none() { return {-INFINITY, 0.0f}; }
+
+    // N values at once: one look at the maximum, then N exponentials. A NaN
+    // passes the maximum by and stays in the sum.
+    template <int N>
+    __device__ __forceinline__ void add(const float (&v)[N], float scale)
     {
-        if (v > max) {
-            sum = sum * exp2f((max - v) * scale) + 1.0f;
-            max = v;
-        } else if (v != -INFINITY) {  // a NaN comes here and stays in the sum
-            sum += exp2f((v - max) * scale);
+        float top = v[0];
+#pragma unroll
+        for (int e = 1; e < N; ++e)
+            top = fmaxf(top, v[e]);
+        if (top > max) {
+            sum *= ex2((max - top) * scale);
+            max = top;
         }
+        const float from = max == -INFINITY ? 0.0f : max;  // -inf so far: the exponentials are 0
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            s += ex2((v[e] - from) * scale);
+        sum += s;
     }
 
     __device__ __forceinline__ void add(const Softmax& o, float scale)
     {
         const float m = fmaxf(max, o.max);
         // A side that has seen nothing but -inf keeps its sum of 0 (or NaN).
-        sum = (max == m ? sum : sum * exp2f((max - m) * scale)) + (o.max == m ? o.sum : o.sum * exp2f((o.max - m) * scale));
+        sum = (max == m ? sum : sum * ex2((max - m) * scale)) + (o.max == m ? o.sum : o.sum * ex2((o.max - m) * scale));
         max = m;
     }
 };
@@ -196,7 +249,7 @@ __device__ __forceinline__ Softmax cta_softmax(Softmax s, float scale, Softmax* 
     if ((threadIdx.x & 31) == 0)
         scratch[threadIdx.x >> 5] = s;
     __syncthreads();
-    s = Softmax();
+    s = Softmax::none();
     if ((threadIdx.x & 31) < NT / 32)
         s = scratch[threadIdx.x & 31];
 #pragma unroll
@@ -204,6 +257,41 @@ __device__ __forceinline__ Softmax cta_softmax(Softmax s, float scale, Softmax* 
         step(o);
     return s;
 }
+
+// ---- clusters ----------------------------------------------------------------------
+
+// Stores to shared memory of any CTA of the cluster (which must have started).
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// The halves of cluster_sync().
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// ---- host: kernels' attributes -----------------------------------------------------
+
+// Sets, once per kernel and device, how much dynamic shared memory the kernel
+// may have and that its clusters may have up to 16 CTAs. Zero-initialised
+// statics, safe from several threads.
+struct Prepared {
+    std::atomic<uint64_t> devices[2];
+
+    cudaError_t once(const void* kernel, int smem)
+    {
+        int d = 0;
+        cudaError_t e = cudaGetDevice(&d);
+        if (e != cudaSuccess || (d < 128 && (devices[d / 64].load(std::memory_order_acquire) >> (d % 64) & 1)))
+            return e;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess && d < 128)
+            devices[d / 64].fetch_or(uint64_t{1} << (d % 64), std::memory_order_release);
+        return e;
+    }
+};
 
 // ---- host: argument checks ------------------------------------------------------
 
