@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kThreads)
     constexpr int N = kPer16<T>;
     extern __shared__ __align__(128) unsigned char slice[];
     float* p = reinterpret_cast<float*>(slice + cut.bytes);  // the teacher's probabilities
-    float* log_p = p + a.k;                                  // its logits, then log probabilities
+    float* log_p = p + a.k;                                  // its logits, then log2 of the probabilities
     float* at_id = log_p + a.k;                              // the student's logits there (for the loss)
     int* id = reinterpret_cast<int*>(at_id + a.k);           // -1 for an absent entry
     __shared__ __align__(8) uint64_t bars[kMaxChunks];
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kThreads)
     const int rank = blockIdx.x % cut.ctas, k = static_cast<int>(a.k);
     const int64_t r = blockIdx.x / cut.ctas;
     const float weight = a.weight ? a.weight[r] : 1.0f;
-    const float scale = kLog2e / a.temperature, inv_t = 1.0f / a.temperature;
+    const float scale = kLog2e / a.temperature;
     const T* row = static_cast<const T*>(a.logits) + r * a.ldl;
     T* out = a.dlogits ? static_cast<T*>(a.dlogits) + r * a.ldd : nullptr;
     // The row, and the slices, as addresses.
@@ -123,25 +123,44 @@ __global__ void __launch_bounds__(kThreads)
                 break;
             }
     };
-    // Writes f(logit) for the elements of the slice, pack by pack.
-    auto write = [&](auto f) {
-        const bool aligned16 = ((reinterpret_cast<uint64_t>(out) ^ start) & 15) == 0;
-        for (int i = threadIdx.x; i < packs; i += kThreads) {
-            float v[N];
-            unpack16<T>(reinterpret_cast<const uint4*>(slice)[i], v);
+    // Writes share 2^((v times - from) power) for the logits v of the slice.
+    float share = 0.0f, times = 1.0f, from = 0.0f, power = scale;
+    auto one_of = [&](float v) { return share * ex2(fmaf(v, times, -from) * power); };
+    auto write = [&] {
+        if (packs == 0)
+            return;
+        // The packs that lie wholly in the row, 16 bytes each, where the gradient's row starts on the same
+        // byte of 16 as the logits'; the rest element by element.
+        const bool wide = ((reinterpret_cast<uint64_t>(out) ^ start) & 15) == 0;
+        const int begin = !wide ? packs : first < 0 ? 1 : 0;
+        const int end = wide && first + static_cast<int64_t>(packs) * N > a.vocab ? packs - 1 : packs;
+        const uint64_t times2 = pair(times, times), from2 = pair(-from, -from), power2 = pair(power, power);
+        const uint64_t share2 = pair(share, share);
+        T* to = out + first;
+#pragma unroll 4
+        for (int i = begin + threadIdx.x; i < end; i += kThreads) {
+            uint64_t v[kPairs<T>];
+            unpack_pairs<T>(reinterpret_cast<const uint4*>(slice)[i], v);
+            float o[N];
 #pragma unroll
-            for (int e = 0; e < N; ++e)
-                v[e] = f(v[e]);
-            const int64_t j = first + static_cast<int64_t>(i) * N;
-            if (aligned16 && j >= 0 && j + N <= a.vocab) {
-                *reinterpret_cast<uint4*>(out + j) = pack16<T>(v);
-            } else {
-#pragma unroll
-                for (int e = 0; e < N; ++e)
-                    if (j + e >= 0 && j + e < a.vocab)
-                        out[j + e] = from_f32<T>(v[e]);
+            for (int e = 0; e < kPairs<T>; ++e) {
+                const float2 x = halves(mul2(fma2(v[e], times2, from2), power2));
+                const float2 y = halves(mul2(pair(ex2(x.x), ex2(x.y)), share2));
+                o[2 * e] = y.x, o[2 * e + 1] = y.y;
             }
+            *reinterpret_cast<uint4*>(to + static_cast<int64_t>(i) * N) = pack16<T>(o);
         }
+        auto one = [&](int j) {
+            if (first + j >= 0 && first + j < a.vocab)
+                to[j] = from_f32<T>(one_of(to_f32(reinterpret_cast<const T*>(slice)[j])));
+        };
+        if (!wide)
+            for (int j = threadIdx.x; j < packs * N; j += kThreads)
+                one(j);
+        else if (threadIdx.x < N && begin == 1)
+            one(threadIdx.x);
+        if (wide && threadIdx.x >= 32 && threadIdx.x < 32 + N && end < packs && (end > 0 || begin == 0))
+            one(end * N + threadIdx.x - 32);
     };
     auto write_zeros = [&] {
         for (int64_t j = rank * static_cast<int64_t>(kThreads) + threadIdx.x; j < a.vocab; j += cut.ctas * kThreads)
@@ -179,10 +198,10 @@ __global__ void __launch_bounds__(kThreads)
         Softmax t = Softmax::none();
         for (int i = threadIdx.x; i < k; i += kThreads) {
             const int token = a.ids[r * a.ldi + i];
-            const float v[1] = {teacher_logit(a, r * a.ldt + i)};
-            const bool there = token >= 0 && token < a.vocab && v[0] != -INFINITY;
+            const float v = teacher_logit(a, r * a.ldt + i);
+            const bool there = token >= 0 && token < a.vocab && v != -INFINITY;
             id[i] = there ? token : -1;
-            log_p[i] = v[0];
+            log_p[i] = v;
             // Before any CTA of the cluster writes its part of the gradient, which may be in the logits' place.
             if (MODE != kGrad && rank == 0)
                 at_id[i] = there ? to_f32(row[token]) : 0.0f;
@@ -191,16 +210,17 @@ __global__ void __launch_bounds__(kThreads)
         }
         t = cta_softmax<kThreads>(t, scale, scratch[0]);
         empty = t.max == -INFINITY;
-        const float top = a.teacher_lse ? 0.0f : t.max, rest = a.teacher_lse ? a.teacher_lse[r] : logf(t.sum);
+        const float top = a.teacher_lse ? 0.0f : t.max, rest = a.teacher_lse ? a.teacher_lse[r] * kLog2e : log2f(t.sum);
         for (int i = threadIdx.x; i < k; i += kThreads) {
-            log_p[i] = (log_p[i] - top) * inv_t - rest;
-            p[i] = id[i] >= 0 ? expf(log_p[i]) : 0.0f;
+            log_p[i] = (log_p[i] - top) * scale - rest;
+            p[i] = id[i] >= 0 ? exp2f(log_p[i]) : 0.0f;
             sum[0] += p[i];
         }
         row_sums<kThreads>(sum, sums, turn);
     }
 
     Softmax q = Softmax::none();
+    RunningSoftmax run;
     if (MODE != kGrad) {
         for (int i = rank; i < cut.per_row; i += cut.ctas) {
             if (i != rank)
@@ -209,14 +229,13 @@ __global__ void __launch_bounds__(kThreads)
             for (int c = 0; c < kMaxChunks; ++c) {
                 wait(c);
                 const int end = min(packs, (c + 1) * (kChunk / 16));
-                for (int j = c * (kChunk / 16) + threadIdx.x; j < end; j += kThreads) {
-                    float v[N];
-                    unpack16<T>(reinterpret_cast<const uint4*>(slice)[j], v);
-                    q.add(v, scale);
-                }
+#pragma unroll 4
+                for (int j = c * (kChunk / 16) + threadIdx.x; j < end; j += kThreads)
+                    run.add<T>(reinterpret_cast<const uint4*>(slice)[j], scale);
             }
             phase ^= 1;
         }
+        q = run.whole();
         if (failed)
             q.sum = NAN;
         q = cta_softmax<kThreads>(q, scale, scratch[1]);
@@ -233,17 +252,17 @@ __global__ void __launch_bounds__(kThreads)
             for (int c = 1; c < cut.ctas; ++c)
                 q.add(across[c], scale);
         }
-        const float log_sum = logf(q.sum);
+        const float log_sum = log2f(q.sum);
         if (rank == 0) {
             float loss[1] = {0.0f};
             for (int i = threadIdx.x; i < k; i += kThreads)
                 if (p[i] > 0.0f)
-                    loss[0] += p[i] * (log_p[i] - ((at_id[i] - q.max) * inv_t - log_sum));
+                    loss[0] += p[i] * (log_p[i] - ((at_id[i] - q.max) * scale - log_sum));
             row_sums<kThreads>(loss, sums, turn);
             if (threadIdx.x == 0) {
-                a.loss[r] = empty ? 0.0f : weight * a.temperature * a.temperature * loss[0];
+                a.loss[r] = empty ? 0.0f : weight * a.temperature * a.temperature * kLn2 * loss[0];
                 if (a.lse)
-                    a.lse[r] = empty ? 0.0f : q.max * inv_t + log_sum;
+                    a.lse[r] = empty ? 0.0f : (q.max * scale + log_sum) * kLn2;
             }
         }
     }
@@ -257,10 +276,11 @@ __global__ void __launch_bounds__(kThreads)
         return;
     }
     const float c = (a.dloss ? a.dloss[r] : 1.0f) * weight * a.temperature;
-    const float lse = MODE == kGrad ? a.lse[r] : 0.0f, share = MODE == kGrad ? c * sum[0] : c * sum[0] / q.sum;
-    auto whole = [&](float v) {
-        return share * (MODE == kGrad ? ex2(fmaf(v, inv_t, -lse) * kLog2e) : ex2((v - q.max) * scale));
-    };
+    if (MODE == kGrad) {
+        share = c * sum[0], times = 1.0f / a.temperature, from = a.lse[r], power = kLog2e;
+    } else {
+        share = c * sum[0] / q.sum, from = q.max;
+    }
     const bool resident = MODE == kBoth && cut.per_row <= cut.ctas;
     for (int i = rank; i < cut.per_row; i += cut.ctas) {
         if (!resident) {
@@ -273,7 +293,7 @@ __global__ void __launch_bounds__(kThreads)
             if (failed)
                 return;
         }
-        write(whole);
+        write();
         __syncthreads();
         // The teacher's tokens within the slice, each once: by the first of the entries that name it.
         const int64_t last = min(first + static_cast<int64_t>(packs) * N, a.vocab);
@@ -287,8 +307,10 @@ __global__ void __launch_bounds__(kThreads)
                     lowest = lowest && l >= n;
                     pn += p[l];
                 }
-            if (lowest)
-                out[id[n]] = from_f32<T>(whole(to_f32(reinterpret_cast<const T*>(slice)[id[n] - first])) - c * pn);
+            if (lowest) {
+                const float v = to_f32(reinterpret_cast<const T*>(slice)[id[n] - first]);
+                out[id[n]] = from_f32<T>(one_of(v) - c * pn);
+            }
         }
     }
 }
@@ -327,7 +349,9 @@ int check(const rowop_distill_args* a, bool forward)
 template <typename T, int MODE>
 cudaError_t launch(const rowop_distill_args& a, cudaStream_t s)
 {
-    const int64_t bytes = a.vocab * static_cast<int64_t>(sizeof(T)) + 15;
+    // With what a row may need before its start to reach a 16-byte boundary.
+    const bool even = aligned(a.logits, 16) && a.ldl * sizeof(T) % 16 == 0;
+    const int64_t bytes = a.vocab * static_cast<int64_t>(sizeof(T)) + (even ? 0 : 15);
     // Slices of a cluster's CTAs: of 64 KB at most, so that three CTAs share an
     // SM and one's copies overlap another's arithmetic; smaller, down to 4 KB,
     // where there are too few rows to fill the GPU with two CTAs per SM.

@@ -17,7 +17,7 @@
 namespace sat {
 namespace rows {
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -71,6 +71,16 @@ __device__ __forceinline__ void store_pack(T* p, const Pack<T>& v)
                      : "memory");
 }
 
+// The two 16-bit elements of a word.
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w)
+{
+    if constexpr (std::is_same_v<T, __half>)
+        return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    else
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
 template <typename T>
 __device__ __forceinline__ void unpack(const Pack<T>& v, float (&out)[8])
 {
@@ -80,12 +90,10 @@ __device__ __forceinline__ void unpack(const Pack<T>& v, float (&out)[8])
             out[e] = __uint_as_float(v.w[e]);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint16_t bits = static_cast<uint16_t>(v.w[e / 2] >> (16 * (e % 2)));
-            if constexpr (std::is_same_v<T, __half>)
-                out[e] = __half2float(__ushort_as_half(bits));
-            else
-                out[e] = __bfloat162float(__ushort_as_bfloat16(bits));
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack2<T>(v.w[e]);
+            out[2 * e] = f.x;
+            out[2 * e + 1] = f.y;
         }
     }
 }
@@ -189,32 +197,89 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// The running maximum and sum of exponentials of a softmax: sum is of
-// exp2((v - max) scale) over the values seen, with max -inf for none.
+// Two fp32 values in one 64-bit register, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ float2 halves(uint64_t v)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+
+// Sixteen bytes as pairs of fp32 values, and the largest of them (NaNs aside).
+template <typename T>
+constexpr int kPairs = 8 / sizeof(T);
+
+template <typename T>
+__device__ __forceinline__ void unpack_pairs(const uint4& w, uint64_t (&out)[kPairs<T>])
+{
+    if constexpr (sizeof(T) == 4) {
+        out[0] = pair(__uint_as_float(w.x), __uint_as_float(w.y));
+        out[1] = pair(__uint_as_float(w.z), __uint_as_float(w.w));
+    } else {
+        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack2<T>(words[e]);
+            out[e] = pair(f.x, f.y);
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ float largest(const uint4& w)
+{
+    if constexpr (sizeof(T) == 4) {
+        return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+    } else {
+        using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+        const T2 m = __hmax2(__hmax2(*reinterpret_cast<const T2*>(&w.x), *reinterpret_cast<const T2*>(&w.y)),
+                             __hmax2(*reinterpret_cast<const T2*>(&w.z), *reinterpret_cast<const T2*>(&w.w)));
+        const float2 f = unpack2<T>(*reinterpret_cast<const uint32_t*>(&m));
+        return fmaxf(f.x, f.y);
+    }
+}
+
+// The maximum of a softmax's values and the sum of 2^((v - max) scale) over
+// them, scale being log2 e over the temperature. The difference comes first:
+// it is exact where it matters, so rows far from 0 lose nothing, and it is 0
+// where all values are the type's lowest, whose products overflow.
 struct Softmax {
     float max, sum;
 
     static __device__ __forceinline__ Softmax none() { return {-INFINITY, 0.0f}; }
 
-    // N values at once: one look at the maximum, then N exponentials. A NaN
-    // passes the maximum by and stays in the sum.
-    template <int N>
-    __device__ __forceinline__ void add(const float (&v)[N], float scale)
+    __device__ __forceinline__ void add(float v, float scale)
     {
-        float top = v[0];
-#pragma unroll
-        for (int e = 1; e < N; ++e)
-            top = fmaxf(top, v[e]);
-        if (top > max) {
-            sum *= ex2((max - top) * scale);
-            max = top;
+        if (v > max) {
+            sum *= ex2((max - v) * scale);
+            max = v;
         }
-        const float from = max == -INFINITY ? 0.0f : max;  // -inf so far: the exponentials are 0
-        float s = 0.0f;
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-            s += ex2((v[e] - from) * scale);
-        sum += s;
+        // With nothing but -inf so far 0 is subtracted, so that 2^-inf is 0. A NaN stays in the sum.
+        sum += ex2((v - (max == -INFINITY ? 0.0f : max)) * scale);
     }
 
     __device__ __forceinline__ void add(const Softmax& o, float scale)
@@ -223,6 +288,40 @@ struct Softmax {
         // A side that has seen nothing but -inf keeps its sum of 0 (or NaN).
         sum = (max == m ? sum : sum * ex2((max - m) * scale)) + (o.max == m ? o.sum : o.sum * ex2((o.max - m) * scale));
         max = m;
+    }
+};
+
+// A thread's running softmax over packs of 16 bytes: one look at the maximum
+// a pack, and for each pair of elements three packed instructions and two
+// exponentials.
+struct RunningSoftmax {
+    float max = -INFINITY;
+    uint64_t sums = 0;  // two sums, of even and odd elements
+
+    template <typename T>
+    __device__ __forceinline__ void add(const uint4& w, float scale)
+    {
+        const float top = largest<T>(w);
+        if (top > max) {
+            const float f = ex2((max - top) * scale);
+            sums = mul2(sums, pair(f, f));
+            max = top;
+        }
+        const float from = max == -INFINITY ? 0.0f : -max;
+        const uint64_t scale2 = pair(scale, scale), from2 = pair(from, from);
+        uint64_t v[kPairs<T>];
+        unpack_pairs<T>(w, v);
+#pragma unroll
+        for (int e = 0; e < kPairs<T>; ++e) {
+            const float2 x = halves(mul2(add2(v[e], from2), scale2));
+            sums = add2(sums, pair(ex2(x.x), ex2(x.y)));
+        }
+    }
+
+    __device__ __forceinline__ Softmax whole() const
+    {
+        const float2 s = halves(sums);
+        return {max, s.x + s.y};
     }
 };
 
@@ -235,13 +334,7 @@ __device__ __forceinline__ Softmax cta_softmax(Softmax s, float scale, Softmax* 
         Softmax u;
         u.max = __shfl_xor_sync(0xffffffffu, s.max, o);
         u.sum = __shfl_xor_sync(0xffffffffu, s.sum, o);
-        // Both lanes of a pair add in the same order and get the same bits.
-        if (threadIdx.x & o) {
-            u.add(s, scale);
-            s = u;
-        } else {
-            s.add(u, scale);
-        }
+        s.add(u, scale);  // the same either way round: both lanes of a pair get the same bits
     };
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -249,9 +342,7 @@ __device__ __forceinline__ Softmax cta_softmax(Softmax s, float scale, Softmax* 
     if ((threadIdx.x & 31) == 0)
         scratch[threadIdx.x >> 5] = s;
     __syncthreads();
-    s = Softmax::none();
-    if ((threadIdx.x & 31) < NT / 32)
-        s = scratch[threadIdx.x & 31];
+    s = (threadIdx.x & 31) < NT / 32 ? scratch[threadIdx.x & 31] : Softmax::none();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         step(o);

@@ -131,16 +131,17 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sat_verify_kernel(const __grid_
         const Packs<T> s(i <= len ? target_row(i) : draft_row(i - len - 1), vocab);
         const float by = i <= len ? scale : q_scale;
         RowStats st = {Softmax::none(), -INFINITY, -1};
+        RunningSoftmax run;
         auto add = [&](const uint4& w, int pack) {
-            float v[N];
-            unpack16<T>(w, v);
-            if (kGreedy) {
+            if (kGreedy && largest<T>(w) > st.value) {
+                float v[N];
+                unpack16<T>(w, v);
 #pragma unroll
                 for (int e = 0; e < N; ++e)
                     if (v[e] > st.value)
                         st.value = v[e], st.best = s.element(pack) + e;
             }
-            st.q.add(v, by);
+            run.add<T>(w, by);
         };
         constexpr int U = 4;
         int j = s.inside + rank * NT + threadIdx.x;
@@ -155,13 +156,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sat_verify_kernel(const __grid_
         }
         for (; j < s.end; j += ctas * NT)
             add(s.load(j), j);
+        st.q = run.whole();
         // The ends' elements, a lane each.
         if (rank == 0 && warp == kWarps - 1 && lane < 2 * N) {
             const int c = lane < N ? (s.inside ? lane - s.shift : -1) : s.element(s.end) + lane - N;
             if (c >= 0 && c < vocab) {
-                const float v[1] = {to_f32(s.row[c])};
-                if (kGreedy && v[0] > -INFINITY)
-                    take(st.value, st.best, v[0], c);
+                const float v = to_f32(s.row[c]);
+                if (kGreedy && v > -INFINITY)
+                    take(st.value, st.best, v, c);
                 st.q.add(v, by);
             }
         }
@@ -312,8 +314,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sat_verify_kernel(const __grid_
         if (a.logprobs)
             a.logprobs[b * (drafts + 1) + i] =
                 said < 0 ? 0.0f
-                         : ((i < n ? logit[0][i] : to_f32(target_row(i)[said])) - whole[i].q.max) * (scale / kLog2e) -
-                               logf(whole[i].q.sum);
+                         : (((i < n ? logit[0][i] : to_f32(target_row(i)[said])) - whole[i].q.max) * scale -
+                            log2f(whole[i].q.sum)) * kLn2;
     }
     if (threadIdx.x == 0)
         a.accepted[b] = n;
