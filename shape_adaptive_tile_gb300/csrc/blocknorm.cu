@@ -13,10 +13,6 @@ using sat::rows::packs;
 using sat::rows::type_bytes;
 using sat::rows::type_ok;
 
-// CTAs of the backward pass that fill the GPU: 152 SMs, each with 512 threads
-// of up to 128 registers.
-constexpr int64_t kSMs = 152;
-
 // The sums of all parts, or of a gate row's pieces, in the order of the parts
 // (eight interleaved runs, then those): a warp takes 32 columns of one sum.
 constexpr int kLanes = 8;
@@ -72,9 +68,7 @@ Split split_of(const rowop_block_norm_args& a, bool gate)
     const int threads = backward_threads(a.width);
     s.sums = a.post_norm == ROWOP_NORM_LAYER || a.pre_norm == ROWOP_NORM_LAYER ? kSums : kPreBeta;
     s.stride = (a.width + 7) / 8 * 8;
-    s.ctas = 1;
-    while (s.ctas * 512 * 8 < a.width)
-        s.ctas *= 2;
+    s.ctas = static_cast<int32_t>((a.width + 4095) / 4096);
     const int64_t fill = threads == 32 ? kSMs * 8 : kSMs * 512 / (threads * s.ctas);
     s.group_rows = gate && a.rows_per_gate < a.rows ? a.rows_per_gate : a.rows;
     s.groups = a.rows ? (a.rows + s.group_rows - 1) / s.group_rows : 0;

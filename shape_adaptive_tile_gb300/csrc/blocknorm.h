@@ -10,6 +10,8 @@
 namespace sat {
 namespace blocknorm {
 
+constexpr int64_t kSMs = 152;
+constexpr int kSmemPerSM = 227 * 1024;
 constexpr int kMaxCluster = 4;  // CTAs that share a row in the backward pass
 
 // The backward pass's parts: each is a range of rows that one warp, CTA or

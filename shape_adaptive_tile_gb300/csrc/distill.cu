@@ -220,7 +220,6 @@ __global__ void __launch_bounds__(kThreads)
     }
 
     Softmax q = Softmax::none();
-    RunningSoftmax run;
     if (MODE != kGrad) {
         for (int i = rank; i < cut.per_row; i += cut.ctas) {
             if (i != rank)
@@ -229,13 +228,18 @@ __global__ void __launch_bounds__(kThreads)
             for (int c = 0; c < kMaxChunks; ++c) {
                 wait(c);
                 const int end = min(packs, (c + 1) * (kChunk / 16));
-#pragma unroll 4
-                for (int j = c * (kChunk / 16) + threadIdx.x; j < end; j += kThreads)
-                    run.add<T>(reinterpret_cast<const uint4*>(slice)[j], scale);
+                const int begin = c * (kChunk / 16) + threadIdx.x;
+                constexpr int U = kChunk / 16 / kThreads;
+                if (begin < end) {
+                    uint4 w[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        w[u] = begin + u * kThreads < end ? reinterpret_cast<const uint4*>(slice)[begin + u * kThreads] : nothing<T>();
+                    q.add(softmax_of<T>(w, scale), scale);
+                }
             }
             phase ^= 1;
         }
-        q = run.whole();
         if (failed)
             q.sum = NAN;
         q = cta_softmax<kThreads>(q, scale, scratch[1]);
@@ -248,9 +252,7 @@ __global__ void __launch_bounds__(kThreads)
             }
             __syncwarp();
             cluster_sync();
-            q = across[0];
-            for (int c = 1; c < cut.ctas; ++c)
-                q.add(across[c], scale);
+            q = sum_softmax(across, 1, cut.ctas, scale);
         }
         const float log_sum = log2f(q.sum);
         if (rank == 0) {

@@ -197,6 +197,14 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// 1 / x to about 2^-23, flushing subnormals.
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Two fp32 values in one 64-bit register, and arithmetic on both at once.
 __device__ __forceinline__ uint64_t pair(float a, float b)
 {
@@ -291,62 +299,104 @@ struct Softmax {
     }
 };
 
-// A thread's running softmax over packs of 16 bytes: one look at the maximum
-// a pack, and for each pair of elements three packed instructions and two
-// exponentials.
-struct RunningSoftmax {
-    float max = -INFINITY;
-    uint64_t sums = 0;  // two sums, of even and odd elements
-
-    template <typename T>
-    __device__ __forceinline__ void add(const uint4& w, float scale)
-    {
-        const float top = largest<T>(w);
-        if (top > max) {
-            const float f = ex2((max - top) * scale);
-            sums = mul2(sums, pair(f, f));
-            max = top;
-        }
-        const float from = max == -INFINITY ? 0.0f : -max;
-        const uint64_t scale2 = pair(scale, scale), from2 = pair(from, from);
-        uint64_t v[kPairs<T>];
-        unpack_pairs<T>(w, v);
+// Sums of 2^((v - top) scale) over packs of 16 bytes, `get(i)` for i < n: for
+// each pair of elements a multiply-add, two exponentials and an addition. The
+// multiply-add subtracts top scale as rounded, and what the rounding was goes
+// into the sum as a factor at the end, so rows far from 0 lose nothing. Where
+// that product might overflow (a maximum that is the type's lowest value) the
+// difference is taken first instead, one instruction more.
+template <typename T, typename Get>
+__device__ __forceinline__ float sum_packs(Get get, int n, float top, float scale)
+{
+    const float from = top == -INFINITY ? 0.0f : top;  // of nothing but -inf: 0 is subtracted, and 2^-inf is 0
+    const bool plain = fabsf(from) < 1e30f;
+    const float off = plain ? -from * scale : -from;
+    const uint64_t scale2 = pair(scale, scale), off2 = pair(off, off);
+    uint64_t sums[2] = {0, 0};
+    if (plain) {
 #pragma unroll
-        for (int e = 0; e < kPairs<T>; ++e) {
-            const float2 x = halves(mul2(add2(v[e], from2), scale2));
-            sums = add2(sums, pair(ex2(x.x), ex2(x.y)));
+        for (int i = 0; i < n; ++i) {
+            uint64_t v[kPairs<T>];
+            unpack_pairs<T>(get(i), v);
+#pragma unroll
+            for (int e = 0; e < kPairs<T>; ++e) {
+                const float2 x = halves(fma2(v[e], scale2, off2));
+                sums[e & 1] = add2(sums[e & 1], pair(ex2(x.x), ex2(x.y)));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            uint64_t v[kPairs<T>];
+            unpack_pairs<T>(get(i), v);
+#pragma unroll
+            for (int e = 0; e < kPairs<T>; ++e) {
+                const float2 x = halves(mul2(add2(v[e], off2), scale2));
+                sums[e & 1] = add2(sums[e & 1], pair(ex2(x.x), ex2(x.y)));
+            }
         }
     }
+    const float2 s = halves(add2(sums[0], sums[1]));
+    return (s.x + s.y) * (plain ? ex2(-fmaf(from, scale, off)) : 1.0f);
+}
 
-    __device__ __forceinline__ Softmax whole() const
-    {
-        const float2 s = halves(sums);
-        return {max, s.x + s.y};
-    }
-};
+// A pack of -inf, for where a row has none.
+template <typename T>
+__device__ __forceinline__ uint4 nothing()
+{
+    const uint32_t w = sizeof(T) == 4 ? 0xff800000u : std::is_same_v<T, __half> ? 0xfc00fc00u : 0xff80ff80u;
+    return make_uint4(w, w, w, w);
+}
+
+// The softmax of a thread's packs, all of them in registers: the maximum
+// first, so that no sum is rescaled.
+template <typename T, int U>
+__device__ __forceinline__ Softmax softmax_of(const uint4 (&w)[U], float scale)
+{
+    float top = largest<T>(w[0]);
+#pragma unroll
+    for (int u = 1; u < U; ++u)
+        top = fmaxf(top, largest<T>(w[u]));
+    return {top, sum_packs<T>([&](int i) { return w[i]; }, U, top, scale)};
+}
+
+// The softmax over what a warp's lanes have seen, to each of them: the largest
+// maximum first, so that a lane rescales its sum once.
+__device__ __forceinline__ Softmax warp_softmax(Softmax s, float scale)
+{
+    float m = s.max;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    // A lane that has seen nothing but -inf keeps its sum of 0 (or NaN).
+    float sum = s.max == m ? s.sum : s.sum * ex2((s.max - m) * scale);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return {m, sum};
+}
+
+// The softmax of n shares that lie in memory, in order.
+__device__ __forceinline__ Softmax sum_softmax(const Softmax* s, int stride, int n, float scale)
+{
+    float m = s[0].max, sum = 0.0f;
+    for (int i = 1; i < n; ++i)
+        m = fmaxf(m, s[i * stride].max);
+    for (int i = 0; i < n; ++i)
+        sum += s[i * stride].max == m ? s[i * stride].sum : s[i * stride].sum * ex2((s[i * stride].max - m) * scale);
+    return {m, sum};
+}
 
 // The softmax over what the NT threads of a CTA have seen, returned to each of
 // them, in a fixed order. `scratch` holds NT / 32 of them; free after a barrier.
 template <int NT>
 __device__ __forceinline__ Softmax cta_softmax(Softmax s, float scale, Softmax* scratch)
 {
-    auto step = [&](int o) {
-        Softmax u;
-        u.max = __shfl_xor_sync(0xffffffffu, s.max, o);
-        u.sum = __shfl_xor_sync(0xffffffffu, s.sum, o);
-        s.add(u, scale);  // the same either way round: both lanes of a pair get the same bits
-    };
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        step(o);
+    s = warp_softmax(s, scale);
     if ((threadIdx.x & 31) == 0)
         scratch[threadIdx.x >> 5] = s;
     __syncthreads();
-    s = (threadIdx.x & 31) < NT / 32 ? scratch[threadIdx.x & 31] : Softmax::none();
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        step(o);
-    return s;
+    return warp_softmax((threadIdx.x & 31) < NT / 32 ? scratch[threadIdx.x & 31] : Softmax::none(), scale);
 }
 
 // ---- clusters ----------------------------------------------------------------------
@@ -355,6 +405,13 @@ __device__ __forceinline__ Softmax cta_softmax(Softmax s, float scale, Softmax* 
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
 {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// Stores eight bytes to shared memory of any CTA of the cluster and counts them on a barrier there.
+__device__ __forceinline__ void send_b64(uint32_t addr, uint64_t v, uint32_t bar)
+{
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(addr), "l"(v), "r"(bar)
+                 : "memory");
 }
 
 // The halves of cluster_sync().

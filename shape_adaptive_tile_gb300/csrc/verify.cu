@@ -1,12 +1,13 @@
 // Verification of drafted tokens and the draw of the next one (include/rowops.h).
 //
-// A cluster of CTAs takes a sequence. Its CTAs go through their shares of the
-// sequence's rows (each logit read once, 16 bytes a load, reduced to a
-// maximum and a sum of exponentials), put the rows' softmaxes together
-// through distributed shared memory, decide alike which token is the first
-// refused, and race through their shares of that one row. HBM bandwidth
-// bounds large batches; one sequence is a chain of latencies: the launch, a
-// load, two exchanges and a second load.
+// Two kernels. The first reads every row of every sequence once: each warp
+// takes its share of the rows' parts, 4 KB in 16-bit types and all of them in
+// flight at once, and leaves a part's maximum and sum of exponentials in the
+// workspace; HBM bandwidth bounds it. In the second a cluster of CTAs takes a
+// sequence: each puts the parts together, all decide alike which token is the
+// first refused, and each races through its share of that one row (from L2,
+// mostly, and the noise with it, which the first kernel had fetched there).
+// It starts while the first one's last CTAs run.
 #include "rows.cuh"
 
 namespace {
@@ -14,17 +15,16 @@ namespace {
 using namespace sat;
 using namespace sat::rows;
 
-constexpr int kMaxCluster = 16;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
 constexpr int kMaxRows = 2 * ROWOP_VERIFY_MAX_DRAFTS + 1;
 
-// What is kept of a row (or of a CTA's or warp's share of it): its softmax,
+// What is kept of a row (or of a part or a warp's share of it): its softmax,
 // and for the greedy choice its largest value's lowest token.
 struct __align__(16) RowStats {
     Softmax q;
     float value;
     int best;
-
-    __device__ __forceinline__ void add(const RowStats& o, float scale);
 };
 
 // The larger value, or of equals the lower index; an index of -1 is none.
@@ -32,12 +32,6 @@ __device__ __forceinline__ void take(float& v, int& at, float v2, int at2)
 {
     if (at2 >= 0 && (at < 0 || v2 > v || (v2 == v && at2 < at)))
         v = v2, at = at2;
-}
-
-__device__ __forceinline__ void RowStats::add(const RowStats& o, float scale)
-{
-    q.add(o.q, scale);
-    take(value, best, o.value, o.best);
 }
 
 __device__ __forceinline__ void warp_best(float& v, int& at)
@@ -72,19 +66,46 @@ struct Packs {
     __device__ __forceinline__ uint4 load(int i) const { return *reinterpret_cast<const uint4*>(row + element(i)); }
 };
 
-// Eight (or four) elements of another row of the same tokens, by one or two
-// 16-byte loads where they lie on the boundaries for it.
+// N consecutive elements from row[j] on, of a row of `vocab`: by 16-byte loads
+// from the boundary before them, shifted into place, where all that these
+// touch lies in the row. The shift is the same for all lanes.
 template <int N, typename T>
-__device__ __forceinline__ void load_beside(float (&v)[N], const T* row, int j, bool wide)
+__device__ __forceinline__ void load_window(float (&v)[N], const T* row, int j, int vocab)
 {
-    if (wide) {
+    constexpr int V = N / kPer16<T>, P = kPer16<T>;
+    const int shift = static_cast<int>((reinterpret_cast<uint64_t>(row + j) & 15) / sizeof(T));
+    const int first = j - shift;
+    if (shift == 0 || (first >= 0 && first + (V + 1) * P <= vocab)) {
+        uint32_t w[4 * V + 4];
 #pragma unroll
-        for (int h = 0; h < N / kPer16<T>; ++h) {
-            float u[kPer16<T>];
-            unpack16<T>(*reinterpret_cast<const uint4*>(row + j + h * kPer16<T>), u);
+        for (int h = 0; h <= V; ++h)
+            if (h < V || shift) {
+                const uint4 x = *reinterpret_cast<const uint4*>(row + first + h * P);
+                w[4 * h] = x.x, w[4 * h + 1] = x.y, w[4 * h + 2] = x.z, w[4 * h + 3] = x.w;
+            }
+        const int words = shift * static_cast<int>(sizeof(T)) / 4;
+        if (words & 2)
 #pragma unroll
-            for (int e = 0; e < kPer16<T>; ++e)
-                v[h * kPer16<T> + e] = u[e];
+            for (int k = 0; k < 4 * V + 2; ++k)
+                w[k] = w[k + 2];
+        if (words & 1)
+#pragma unroll
+            for (int k = 0; k < 4 * V + 1; ++k)
+                w[k] = w[k + 1];
+        if constexpr (sizeof(T) == 2) {
+            if (shift & 1)
+#pragma unroll
+                for (int k = 0; k < 4 * V; ++k)
+                    w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+#pragma unroll
+            for (int k = 0; k < N / 2; ++k) {
+                const float2 f = unpack2<T>(w[k]);
+                v[2 * k] = f.x, v[2 * k + 1] = f.y;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                v[k] = __uint_as_float(w[k]);
         }
     } else {
 #pragma unroll
@@ -93,26 +114,210 @@ __device__ __forceinline__ void load_beside(float (&v)[N], const T* row, int j, 
     }
 }
 
-template <typename T, int NT, bool kGreedy>
-__global__ void __launch_bounds__(NT, 1024 / NT) sat_verify_kernel(const __grid_constant__ rowop_verify_args a, int ctas)
+// The rows' parts: `elements` of a row each.
+struct Parts {
+    int elements, per_row;
+};
+
+constexpr int kCtas = 4 * 152;     // of the first kernel: four an SM
+constexpr int kMaxScan = 1024;     // sequences whose lengths its CTAs add up
+
+Parts parts_of(int64_t batch, int64_t drafts, int64_t vocab)
 {
-    constexpr int N = kPer16<T>, kWarps = NT / 32;
-    extern __shared__ RowStats stats[];  // [rows][kWarps], then [rows][ctas]
+    // 2048 elements, 64 a lane; fewer, down to 512, where two warps an SM's
+    // scheduler would not come of it; more where a row would have over 512.
+    const int64_t rows = batch * (2 * drafts + 1);
+    int64_t each = 2048;
+    // A row may start up to 7 elements after a 16-byte boundary.
+    auto count = [&] { return (vocab + 7 + each - 1) / each; };
+    while (each > 512 && rows * count() < 8 * 152)
+        each /= 2;
+    while (count() > 512 || rows * count() > (1 << 30))
+        each *= 2;
+    return {static_cast<int>(each), static_cast<int>(count())};
+}
+
+__device__ __forceinline__ int length_of(const rowop_verify_args& a, int64_t b)
+{
+    const int drafts = static_cast<int>(a.drafts);
+    return a.lengths ? min(max(a.lengths[b], 0), drafts) : drafts;
+}
+
+// Scales of the exponents: a greedy target's log probabilities are at temperature 1.
+template <bool kGreedy>
+__device__ __forceinline__ float target_scale(const rowop_verify_args& a)
+{
+    return kGreedy ? kLog2e : kLog2e / a.temperature;
+}
+
+// All sequences' rows in order (of each the target's 0 .. length, then the
+// draft's 0 .. length - 1) have their parts dealt to the grid's warps in equal
+// runs. The rows before each sequence are counted by every CTA for itself;
+// past kMaxScan sequences, all `drafts` rows are counted and those past the
+// lengths skipped.
+template <typename T, bool kGreedy>
+__global__ void __launch_bounds__(kThreads, 4)
+    sat_verify_rows_kernel(const __grid_constant__ rowop_verify_args a, const Parts parts)
+{
+    constexpr int N = kPer16<T>, U = 8;
+    __shared__ int before[kMaxScan + 1], sums[kWarps];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int drafts = static_cast<int>(a.drafts), vocab = static_cast<int>(a.vocab), batch = static_cast<int>(a.batch);
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const bool point = kGreedy || !a.draft, scan = a.lengths && batch <= kMaxScan;
+    const int most = drafts + 1 + (point ? 0 : drafts);
+    auto rows_for = [&](int len) { return len + 1 + (point ? 0 : len); };
+    int total = batch * most;
+    if (scan) {
+        constexpr int S = kMaxScan / kThreads;
+        int n[S], sum = 0;
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            const int b = threadIdx.x * S + i;
+            n[i] = b < batch ? rows_for(length_of(a, b)) : 0;
+            sum += n[i];
+        }
+        int upto = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            upto += lane >= o ? v : 0;
+        }
+        if (lane == 31)
+            sums[warp] = upto;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w)
+            upto += sums[w];
+        int at = upto - sum;
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            before[threadIdx.x * S + i] = at;
+            at += n[i];
+        }
+        if (threadIdx.x == kThreads - 1)
+            before[kMaxScan] = at;
+        __syncthreads();
+        total = before[kMaxScan];
+    }
+    // This warp's run of parts, and the sequence, row and part that it begins with.
+    const int warps = gridDim.x * kWarps, me = blockIdx.x * kWarps + warp;
+    const int64_t items = static_cast<int64_t>(total) * parts.per_row;
+    int item = static_cast<int>(items * me / warps);
+    const int stop = static_cast<int>(items * (me + 1) / warps);
+    if (item >= stop)
+        return;
+    const int first_row = item / parts.per_row;
+    int part = item - first_row * parts.per_row, b, i;
+    if (scan) {
+        int low = 0, high = batch - 1;  // the last sequence with no more rows before it
+        while (low < high) {
+            const int mid = (low + high + 1) / 2;
+            if (before[mid] <= first_row)
+                low = mid;
+            else
+                high = mid - 1;
+        }
+        b = low, i = first_row - before[b];
+    } else {
+        b = first_row / most, i = first_row - b * most;
+    }
+    int len = length_of(a, b);
+    for (int more; item < stop; item += more, part = 0, ++i) {
+        more = min(parts.per_row - part, stop - item);  // this row's parts of the run, taken as one
+        if (i == (scan ? rows_for(len) : most))
+            i = 0, len = length_of(a, ++b);
+        // Past the scan the target's rows are drafts + 1 always.
+        const int targets = scan ? len + 1 : drafts + 1;
+        const bool target = i < targets;
+        const int r = target ? i : i - targets;
+        if (!scan && (target ? r > len : r >= len))
+            continue;
+        const Packs<T> s(target ? static_cast<const T*>(a.target) + (static_cast<int64_t>(b) * (drafts + 1) + r) * a.ldt
+                                : static_cast<const T*>(a.draft) + (static_cast<int64_t>(b) * drafts + r) * a.ldq, vocab);
+        const float scale = target ? target_scale<kGreedy>(a) : kLog2e / a.draft_temperature;
+        const int first = part * (parts.elements / N), last = min(first + more * (parts.elements / N), s.count);
+        const int begin = max(first, s.inside), end = min(last, s.end);
+        RowStats st = {Softmax::none(), -INFINITY, -1};
+        auto add = [&](const uint4(&w)[U], int j) {
+            const Softmax q = softmax_of<T>(w, scale);
+            if (kGreedy && q.max > st.value) {  // of equals the lower token: later packs are higher
+                st.value = q.max;
+#pragma unroll
+                for (int u = U - 1; u >= 0; --u) {
+                    float v[N];
+                    unpack16<T>(w[u], v);
+#pragma unroll
+                    for (int e = N - 1; e >= 0; --e)
+                        if (v[e] == q.max)
+                            st.best = s.element(j + u * 32) + e;
+                }
+            }
+            st.q.add(q, scale);
+        };
+        int j = begin + lane;
+        for (const uint4* at = reinterpret_cast<const uint4*>(s.row + s.element(j)); j - lane + U * 32 <= end; j += U * 32, at += U * 32) {
+            uint4 w[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                w[u] = at[u * 32];
+            add(w, j);
+        }
+        if (j - lane < end) {
+            uint4 w[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                w[u] = j + u * 32 < end ? s.load(j + u * 32) : nothing<T>();
+            add(w, j);
+        }
+        // The packs at the row's ends, an element a lane.
+        if (lane < 2 * N) {
+            const int c = lane < N ? (s.inside && part == 0 ? lane - s.shift : -1)
+                                   : s.end < last && s.end >= first ? s.element(s.end) + lane - N : -1;
+            if (c >= 0 && c < vocab) {
+                const float v = to_f32(s.row[c]);
+                if (kGreedy && v > -INFINITY)
+                    take(st.value, st.best, v, c);
+                st.q.add(v, scale);
+            }
+        }
+        __syncwarp();
+        st.q = warp_softmax(st.q, scale);
+        if (kGreedy)
+            warp_best(st.value, st.best);
+        // All of the run in the first part's place, nothing in the others'.
+        RowStats* to = static_cast<RowStats*>(a.workspace) +
+                       (static_cast<int64_t>(b) * (2 * drafts + 1) + (target ? r : drafts + 1 + r)) * parts.per_row + part;
+        for (int c = lane; c < more; c += 32)
+            to[c] = c == 0 ? st : RowStats{Softmax::none(), -INFINITY, -1};
+        // The noise that the sequence's draw will want, towards L2.
+        if (!kGreedy && i == 0) {
+            const char* noise = reinterpret_cast<const char*>(a.noise + b * a.ldn);
+            const int64_t to = min((part + more) * static_cast<int64_t>(parts.elements), a.vocab) * 4;
+            for (int64_t at = part * static_cast<int64_t>(parts.elements) * 4 + lane * 128; at < to; at += 32 * 128)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(noise + at));
+        }
+    }
+}
+
+// A cluster of `ctas` a sequence: the decisions, then the draw.
+template <typename T, bool kGreedy>
+__global__ void __launch_bounds__(kThreads, 3)
+    sat_verify_draw_kernel(const __grid_constant__ rowop_verify_args a, const Parts parts, int ctas)
+{
+    constexpr int N = kPer16<T>;
     __shared__ RowStats whole[kMaxRows];  // of the target's rows, then the draft's
     __shared__ float logit[2][ROWOP_VERIFY_MAX_DRAFTS];  // the target's and the draft's at the drafted tokens
-    __shared__ RowStats races[kMaxCluster];
+    __shared__ __align__(16) uint4 races[kMaxCluster];
     __shared__ float values[kWarps];
     __shared__ int where[kWarps];
     __shared__ int refused;
     const int rank = blockIdx.x % ctas, drafts = static_cast<int>(a.drafts), vocab = static_cast<int>(a.vocab);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t b = blockIdx.x / ctas;
-    const int len = a.lengths ? min(max(a.lengths[b], 0), drafts) : drafts;
+    const int len = length_of(a, b);
     const bool point = kGreedy || !a.draft;
-    // A greedy target's log probabilities are at temperature 1.
-    const float scale = kGreedy ? kLog2e : kLog2e / a.temperature, q_scale = point ? 0.0f : kLog2e / a.draft_temperature;
+    const float scale = target_scale<kGreedy>(a), q_scale = point ? 0.0f : kLog2e / a.draft_temperature;
     const int rows = len + 1 + (point ? 0 : len);
-    RowStats* across = stats + rows * kWarps;
     auto target_row = [&](int i) { return static_cast<const T*>(a.target) + (b * (drafts + 1) + i) * a.ldt; };
     auto draft_row = [&](int i) { return static_cast<const T*>(a.draft) + (b * drafts + i) * a.ldq; };
     if (ctas > 1)
@@ -125,90 +330,23 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sat_verify_kernel(const __grid_
     }
     if (threadIdx.x == 0)
         refused = len;
-
-    // The shares' softmaxes.
-    for (int i = 0; i < rows; ++i) {
-        const Packs<T> s(i <= len ? target_row(i) : draft_row(i - len - 1), vocab);
+    // What the first kernel left, a warp a row: lanes, then the lanes' sums in order.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = warp; i < rows; i += kWarps) {
         const float by = i <= len ? scale : q_scale;
+        const int64_t row = b * (2 * drafts + 1) + (i <= len ? i : i - len + drafts);
+        const RowStats* shares = static_cast<const RowStats*>(a.workspace) + row * parts.per_row;
         RowStats st = {Softmax::none(), -INFINITY, -1};
-        RunningSoftmax run;
-        auto add = [&](const uint4& w, int pack) {
-            if (kGreedy && largest<T>(w) > st.value) {
-                float v[N];
-                unpack16<T>(w, v);
-#pragma unroll
-                for (int e = 0; e < N; ++e)
-                    if (v[e] > st.value)
-                        st.value = v[e], st.best = s.element(pack) + e;
-            }
-            run.add<T>(w, by);
-        };
-        constexpr int U = 4;
-        int j = s.inside + rank * NT + threadIdx.x;
-        for (; j + (U - 1) * ctas * NT < s.end; j += U * ctas * NT) {
-            uint4 w[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                w[u] = s.load(j + u * ctas * NT);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                add(w[u], j + u * ctas * NT);
+        for (int c = lane; c < parts.per_row; c += 32) {
+            const RowStats u = shares[c];
+            st.q.add(u.q, by);
+            take(st.value, st.best, u.value, u.best);
         }
-        for (; j < s.end; j += ctas * NT)
-            add(s.load(j), j);
-        st.q = run.whole();
-        // The ends' elements, a lane each.
-        if (rank == 0 && warp == kWarps - 1 && lane < 2 * N) {
-            const int c = lane < N ? (s.inside ? lane - s.shift : -1) : s.element(s.end) + lane - N;
-            if (c >= 0 && c < vocab) {
-                const float v = to_f32(s.row[c]);
-                if (kGreedy && v > -INFINITY)
-                    take(st.value, st.best, v, c);
-                st.q.add(v, by);
-            }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            RowStats u;
-            u.q.max = __shfl_down_sync(0xffffffffu, st.q.max, o);
-            u.q.sum = __shfl_down_sync(0xffffffffu, st.q.sum, o);
-            if (kGreedy) {
-                u.value = __shfl_down_sync(0xffffffffu, st.value, o);
-                u.best = __shfl_down_sync(0xffffffffu, st.best, o);
-                st.add(u, by);
-            } else {
-                st.q.add(u.q, by);
-            }
-        }
+        st.q = warp_softmax(st.q, by);
+        if (kGreedy)
+            warp_best(st.value, st.best);
         if (lane == 0)
-            stats[i * kWarps + warp] = st;
-    }
-    __syncthreads();
-    // Put together: the CTA's warps, then the cluster's CTAs, in order.
-    auto scale_of = [&](int i) { return i <= len ? scale : q_scale; };
-    if (ctas > 1) {
-        __syncwarp();
-        cluster_wait();
-    }
-    for (int i = threadIdx.x; i < rows; i += NT) {
-        RowStats st = stats[i * kWarps];
-        for (int w = 1; w < kWarps; ++w)
-            st.add(stats[i * kWarps + w], scale_of(i));
-        if (ctas == 1)
             whole[i] = st;
-        else
-            for (int c = 0; c < ctas; ++c)
-                st_cluster_v4(map_to_cta(smem_u32(&across[i * ctas + rank]), c), *reinterpret_cast<const uint4*>(&st));
-    }
-    if (ctas > 1) {
-        __syncwarp();
-        cluster_sync();
-        for (int i = threadIdx.x; i < rows; i += NT) {
-            RowStats st = across[i * ctas];
-            for (int c = 1; c < ctas; ++c)
-                st.add(across[i * ctas + c], scale_of(i));
-            whole[i] = st;
-        }
     }
     __syncthreads();
 
@@ -246,38 +384,76 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sat_verify_kernel(const __grid_
             const float inv = 1.0f / st.q.sum;
             const Softmax d = whole[minus ? len + 1 + n : 0].q;
             const float q_inv = 1.0f / d.sum;
-            const bool q_wide = minus && (reinterpret_cast<uint64_t>(q - s.shift) & 15) == 0;
-            const bool noise_wide = (reinterpret_cast<uint64_t>(noise - s.shift) & 15) == 0;
             // The race of max(p - q, 0), and where that is nowhere positive, of p.
             for (int pass = 0; pass < 2 && token < 0; ++pass) {
                 float best = -1.0f;
                 int at = -1;
-                auto run = [&](float t, float u, float e, int j) {
-                    // Products rounded by themselves: fused with the difference, equal distributions
-                    // would leave a residue of rounding size in the place of 0.
-                    const float p = __fmul_rn(ex2((t - st.q.max) * scale), inv);
-                    float r = p;
-                    if (pass == 0)
-                        r = minus ? p - __fmul_rn(ex2((u - d.max) * q_scale), q_inv) : j == without ? 0.0f : p;
-                    // The quotient only where it may be the largest.
-                    if (r > 0.0f && r >= best * e * 0.999999f)
-                        take(best, at, r / e, j);
+                // r / e, as a product with the reciprocal (good to about 2^-22, and the same for the same r and e).
+                // The products of p and q are rounded by themselves: fused with the difference, equal
+                // distributions would leave a residue of rounding size in the place of 0.
+                const uint64_t scale2 = pair(scale, scale), from2 = pair(-st.q.max, -st.q.max);
+                const uint64_t q_scale2 = pair(q_scale, q_scale), q_from2 = pair(-d.max, -d.max);
+                auto score2 = [&](uint64_t t, uint64_t u, float2 e) {
+                    const float2 x = halves(mul2(add2(t, from2), scale2));
+                    float2 r = make_float2(__fmul_rn(ex2(x.x), inv), __fmul_rn(ex2(x.y), inv));
+                    if (minus && pass == 0) {
+                        const float2 y = halves(mul2(add2(u, q_from2), q_scale2));
+                        r.x = __fsub_rn(r.x, __fmul_rn(ex2(y.x), q_inv));
+                        r.y = __fsub_rn(r.y, __fmul_rn(ex2(y.y), q_inv));
+                    }
+                    return halves(mul2(pair(r.x, r.y), pair(rcp(e.x), rcp(e.y))));
                 };
-                for (int i = s.inside + rank * NT + threadIdx.x; i < s.end; i += ctas * NT) {
-                    float t[N], u[N] = {}, e[N];
-                    const int j = s.element(i);
-                    unpack16<T>(s.load(i), t);
-                    if (minus)
-                        load_beside(u, q, j, q_wide);
-                    load_beside(e, noise, j, noise_wide);
+                auto one = [&](float t, float u, float e, int j) {
+                    if (j == without && pass == 0)
+                        return;
+                    const float s = score2(pair(t, t), pair(u, u), make_float2(e, e)).x;
+                    if (s > 0.0f)
+                        take(best, at, s, j);
+                };
+                constexpr int U = 2;
+                const int stride = ctas * kThreads;
+                for (int i = s.inside + rank * kThreads + threadIdx.x; i < s.end; i += U * stride) {
+                    uint4 packed[U];
+                    float u[U][N], e[U][N];
 #pragma unroll
-                    for (int k = 0; k < N; ++k)
-                        run(t[k], u[k], e[k], j + k);
+                    for (int h = 0; h < U; ++h) {
+                        const int pack = min(i + h * stride, s.end - 1), j = s.element(pack);  // past the end: the last again
+                        packed[h] = s.load(pack);
+                        if (minus && pass == 0)
+                            load_window(u[h], q, j, vocab);
+                        load_window(e[h], noise, j, vocab);
+                    }
+#pragma unroll
+                    for (int h = 0; h < U; ++h) {
+                        const int j = s.element(min(i + h * stride, s.end - 1));
+                        uint64_t t[kPairs<T>];
+                        float sc[N], top = 0.0f;
+                        unpack_pairs<T>(packed[h], t);
+#pragma unroll
+                        for (int k = 0; k < kPairs<T>; ++k) {
+                            const float2 x = score2(t[k], minus && pass == 0 ? pair(u[h][2 * k], u[h][2 * k + 1]) : 0,
+                                                    make_float2(e[h][2 * k], e[h][2 * k + 1]));
+                            sc[2 * k] = x.x, sc[2 * k + 1] = x.y;
+                        }
+                        if (pass == 0 && static_cast<unsigned>(without - j) < N)
+#pragma unroll
+                            for (int k = 0; k < N; ++k)
+                                sc[k] = j + k == without ? 0.0f : sc[k];
+#pragma unroll
+                        for (int k = 0; k < N; ++k)
+                            top = fmaxf(top, sc[k]);
+                        if (top > best && top > 0.0f) {  // of equals the lower token: later packs are higher
+                            best = top;
+#pragma unroll
+                            for (int k = N - 1; k >= 0; --k)
+                                at = sc[k] == top ? j + k : at;
+                        }
+                    }
                 }
                 if (rank == 0 && warp == kWarps - 1 && lane < 2 * N) {
                     const int j = lane < N ? (s.inside ? lane - s.shift : -1) : s.element(s.end) + lane - N;
                     if (j >= 0 && j < vocab)
-                        run(to_f32(s.row[j]), minus ? to_f32(q[j]) : 0.0f, noise[j], j);
+                        one(to_f32(s.row[j]), minus ? to_f32(q[j]) : 0.0f, noise[j], j);
                 }
                 warp_best(best, at);
                 __syncthreads();  // the pass before has read these
@@ -287,6 +463,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sat_verify_kernel(const __grid_
                 for (int w = 0; w < kWarps; ++w)
                     take(best, at, values[w], where[w]);
                 if (ctas > 1) {
+                    if (pass == 0) {
+                        __syncwarp();
+                        cluster_wait();
+                    }
                     if (threadIdx.x < ctas) {
                         const uint4 v = make_uint4(__float_as_uint(best), static_cast<uint32_t>(at), 0, 0);
                         st_cluster_v4(map_to_cta(smem_u32(&races[rank]), threadIdx.x), v);
@@ -294,7 +474,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sat_verify_kernel(const __grid_
                     __syncwarp();
                     cluster_sync();
                     for (int c = 0; c < ctas; ++c) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(&races[c]);
+                        const uint4 v = races[c];
                         take(best, at, __uint_as_float(v.x), static_cast<int>(v.y));
                     }
                     if (pass == 0 && at < 0) {  // `races` is read before it is written again
@@ -306,9 +486,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sat_verify_kernel(const __grid_
             }
         }
     }
+    if (ctas > 1 && (kGreedy || !ok(st))) {
+        __syncwarp();
+        cluster_wait();  // of the arrival at the start; the race has waited for it
+    }
     if (rank)
         return;
-    for (int i = threadIdx.x; i <= drafts; i += NT) {
+    for (int i = threadIdx.x; i <= drafts; i += kThreads) {
         const int said = i < n ? a.tokens[b * drafts + i] : i == n ? token : -1;
         a.out[b * (drafts + 1) + i] = said;
         if (a.logprobs)
@@ -362,43 +546,40 @@ int check(const rowop_verify_args* a)
     return GEMM_OK;
 }
 
-template <typename T, int NT, bool kGreedy>
-cudaError_t launch_one(const rowop_verify_args& a, int ctas, cudaStream_t s)
+template <typename T, bool kGreedy>
+cudaError_t launch(const rowop_verify_args& a, cudaStream_t s)
 {
     const bool draft = a.draft && !kGreedy;
-    const int rows = static_cast<int>(a.drafts + 1 + (draft ? a.drafts : 0));
-    auto kernel = sat_verify_kernel<T, NT, kGreedy>;
-    static Prepared prepared;
-    const cudaError_t e = prepared.once(reinterpret_cast<const void*>(kernel),
-                                        kMaxRows * (NT / 32 + kMaxCluster) * static_cast<int>(sizeof(RowStats)));
+    const Parts parts = parts_of(a.batch, a.drafts, a.vocab);
+    const int64_t items = a.batch * (a.drafts + 1 + (draft ? a.drafts : 0)) * parts.per_row, ctas_wanted = (items + kWarps - 1) / kWarps;
+    const unsigned grid = static_cast<unsigned>(ctas_wanted < kCtas ? ctas_wanted : kCtas);
+    sat_verify_rows_kernel<T, kGreedy><<<grid, kThreads, 0, s>>>(a, parts);
+    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
+    // Three CTAs an SM, of at least 2048 elements of the race each; clusters of 8 at most, which any GPU takes.
+    const int64_t fit = 3 * 152 / a.batch, want = (a.vocab + 2047) / 2048;
+    int64_t ctas = fit < want ? fit : want;
+    ctas = kGreedy || ctas < 1 ? 1 : ctas < kMaxCluster ? ctas : kMaxCluster;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.batch * ctas));
-    cfg.blockDim = dim3(NT);
-    cfg.dynamicSmemBytes = rows * (NT / 32 + ctas) * sizeof(RowStats);
+    cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a, ctas);
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, sat_verify_draw_kernel<T, kGreedy>, a, parts, static_cast<int>(ctas));
 }
 
 template <typename T>
-cudaError_t launch(const rowop_verify_args& a, cudaStream_t s)
+cudaError_t launch_as(const rowop_verify_args& a, cudaStream_t s)
 {
-    // Four CTAs of 256 threads an SM, 608 in all, where the batch gives them;
-    // where even clusters of 16 leave SMs idle, the CTAs have 1024 threads.
-    int ctas = 1;
-    while (ctas < kMaxCluster && a.batch * ctas * 2 <= 608 && a.vocab * static_cast<int64_t>(sizeof(T)) > ctas * 4096)
-        ctas *= 2;
-    const bool few = a.batch * ctas <= 152;
-    if (a.temperature == 0.0f)
-        return few ? launch_one<T, 1024, true>(a, ctas, s) : launch_one<T, 256, true>(a, ctas, s);
-    return few ? launch_one<T, 1024, false>(a, ctas, s) : launch_one<T, 256, false>(a, ctas, s);
+    return a.temperature == 0.0f ? launch<T, true>(a, s) : launch<T, false>(a, s);
 }
 
 }  // namespace
@@ -409,7 +590,9 @@ int64_t rowop_verify_workspace(int64_t batch, int64_t drafts, int64_t vocab)
 {
     set_last_error("");
     const int rc = check_sizes(batch, drafts, vocab);
-    return rc ? rc : batch * (2 * drafts + 1) * static_cast<int64_t>(sizeof(RowStats));
+    if (rc || batch == 0)
+        return rc;
+    return batch * (2 * drafts + 1) * parts_of(batch, drafts, vocab).per_row * static_cast<int64_t>(sizeof(RowStats));
 }
 
 int rowop_verify(const rowop_verify_args* args, void* stream)
@@ -419,9 +602,9 @@ int rowop_verify(const rowop_verify_args* args, void* stream)
     if (rc || args->batch == 0)
         return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = args->logits_type == GEMM_C_F32    ? launch<float>(*args, s)
-                          : args->logits_type == GEMM_C_BF16 ? launch<__nv_bfloat16>(*args, s)
-                                                             : launch<__half>(*args, s);
+    const cudaError_t e = args->logits_type == GEMM_C_F32    ? launch_as<float>(*args, s)
+                          : args->logits_type == GEMM_C_BF16 ? launch_as<__nv_bfloat16>(*args, s)
+                                                             : launch_as<__half>(*args, s);
     return e == cudaSuccess ? GEMM_OK
                             : fail_with(GEMM_ERR_LAUNCH, "launching the verification: %s", cudaGetErrorString(e));
 }
