@@ -26,9 +26,9 @@ STAMP = os.path.join(LIB_DIR, "libsatgemm.stamp")
 # The kernel variants come as three translation units per dtype (they take
 # most of the build); the longest units are listed first.
 SOURCES = [f"kernels_{dt}{grp}.cu" for grp in ("", "_alt", "_trans") for dt in ("tf32", "bf16", "fp16")] + [
-    "device_call.cu", "api.cu", "aux_kernels.cu", "dispatch.cpp", "tensor_map.cpp", "noalloc.cu", "rowops.cu", "blocknorm.cu", "blocknorm_f32.cu",
-    "blocknorm_bf16.cu", "blocknorm_f16.cu",
-    "distill.cu", "verify.cu"]
+    "device_call.cu"] + [f"blocknorm_{d}_{dt}.cu" for d in ("backward", "forward") for dt in ("bf16", "f16", "f32")] + [
+    "api.cu", "aux_kernels.cu", "dispatch.cpp", "tensor_map.cpp", "noalloc.cu", "rowops.cu", "blocknorm.cu", "distill.cu",
+    "verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 # The GEMM kernel units: an explicit register ceiling (the launch bounds of
@@ -73,8 +73,11 @@ def source_hash() -> str:
 
 
 # Sources of the row operators only: no GEMM kernel includes or calls them.
-_ROWOP_ONLY = ("rowops.cu", "rowops.h", "rows.cuh", "blocknorm.h", "blocknorm.cuh", "blocknorm.cu", "blocknorm_f32.cu",
-                "blocknorm_bf16.cu", "blocknorm_f16.cu", "distill.cu", "verify.cu")
+_ROWOP_ONLY = ("rowops.cu", "rowops.h", "rows.cuh", "distill.cu", "verify.cu")
+
+
+def _rowop_only(name: str) -> bool:
+    return name in _ROWOP_ONLY or name.startswith("blocknorm")
 
 
 def gemm_source_hash() -> str:
@@ -83,7 +86,7 @@ def gemm_source_hash() -> str:
     GEMM kernel stays valid as long as this is unchanged."""
     h = hashlib.sha256()
     for f in _inputs():
-        if os.path.basename(f) in _ROWOP_ONLY:
+        if _rowop_only(os.path.basename(f)):
             continue
         with open(f, "rb") as fh:
             h.update(os.path.basename(f).encode() + b"\0" + _code_text(fh.read()))

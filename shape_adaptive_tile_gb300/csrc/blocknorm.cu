@@ -65,11 +65,17 @@ __global__ void __launch_bounds__(32 * kLanes)
 Split split_of(const rowop_block_norm_args& a, bool gate)
 {
     Split s = {};
-    const int threads = backward_threads(a.width);
-    s.sums = a.post_norm == ROWOP_NORM_LAYER || a.pre_norm == ROWOP_NORM_LAYER ? kSums : kPreBeta;
+    const bool layer = a.post_norm == ROWOP_NORM_LAYER || a.pre_norm == ROWOP_NORM_LAYER;
+    s.sums = layer ? kSums : kPreBeta;
+    s.mode = !layer ? kRms : a.gate && a.rows_per_gate < a.rows ? kLayerGrouped : kLayerShared;
     s.stride = (a.width + 7) / 8 * 8;
+    s.threads = a.width <= 256 ? 32 : a.width <= 1024 ? 128 : a.width <= 2048 ? 256 : 512;
     s.ctas = static_cast<int32_t>((a.width + 4095) / 4096);
-    const int64_t fill = threads == 32 ? kSMs * 8 : kSMs * 512 / (threads * s.ctas);
+    // Parts that run at once: eight warps an SM, CTAs of 512 threads an SM, or
+    // as many clusters of these as the GPU's groups of SMs hold (what
+    // cudaOccupancyMaxActiveClusters says of a GB300).
+    constexpr int64_t clusters[kMaxCluster + 1] = {0, 152, 76, 46, 36};
+    const int64_t fill = s.threads == 32 ? kSMs * 8 : clusters[s.ctas] * (512 / s.threads);
     s.group_rows = gate && a.rows_per_gate < a.rows ? a.rows_per_gate : a.rows;
     s.groups = a.rows ? (a.rows + s.group_rows - 1) / s.group_rows : 0;
     if (s.groups > 1 && s.groups >= fill) {

@@ -22,6 +22,34 @@ namespace blocknorm {
 
 using namespace rows;
 
+// Eight elements as four pairs, on which the arithmetic goes two at a time.
+struct Group {
+    uint64_t p[4];
+};
+
+__device__ __forceinline__ uint64_t both(float v) { return pair(v, v); }
+
+__device__ __forceinline__ Group fill(float v)
+{
+    return {{both(v), both(v), both(v), both(v)}};
+}
+
+template <typename T>
+__device__ __forceinline__ Group group_of(const Pack<T>& v)
+{
+    Group g;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 4) {
+            g.p[e] = pair(__uint_as_float(v.w[2 * e]), __uint_as_float(v.w[2 * e + 1]));
+        } else {
+            const float2 f = unpack2<T>(v.w[e]);
+            g.p[e] = pair(f.x, f.y);
+        }
+    }
+    return g;
+}
+
 // The thread's share of a row: column of its element e of group i.
 template <bool kPack, int NT>
 __device__ __forceinline__ int column(int lane, int i, int e)
@@ -31,29 +59,31 @@ __device__ __forceinline__ int column(int lane, int i, int e)
 
 // Group i of a row of `width` elements; columns from `width` on are 0.
 template <bool kPack, int NT, typename T>
-__device__ __forceinline__ void load_group(float (&v)[8], const T* row, int lane, int i, int width)
+__device__ __forceinline__ Group load_group(const T* row, int lane, int i, int width)
 {
     if constexpr (kPack) {
         const int c = column<true, NT>(lane, i, 0);
-        if (c < width) {
-            unpack(load_pack(row + c), v);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = 0.0f;
-        }
+        return c < width ? group_of(load_pack(row + c)) : fill(0.0f);
     } else {
+        float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int c = column<false, NT>(lane, i, e);
             v[e] = c < width ? to_f32(row[c]) : 0.0f;
         }
+        return {{pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7])}};
     }
 }
 
 template <bool kPack, int NT, typename T>
-__device__ __forceinline__ void store_group(T* row, const float (&v)[8], int lane, int i, int width)
+__device__ __forceinline__ void store_group(T* row, const Group& g, int lane, int i, int width)
 {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 f = halves(g.p[e]);
+        v[2 * e] = f.x, v[2 * e + 1] = f.y;
+    }
     if constexpr (kPack) {
         const int c = column<true, NT>(lane, i, 0);
         if (c < width)
@@ -68,38 +98,80 @@ __device__ __forceinline__ void store_group(T* row, const float (&v)[8], int lan
     }
 }
 
-// A vector of weights, or `otherwise` where there is none.
+// The group with 0 in columns from `width` on.
 template <bool kPack, int NT>
-__device__ __forceinline__ void load_weights(float (&v)[8], const float* w, float otherwise, int lane, int i, int width)
+__device__ __forceinline__ Group inside(const Group& g, int lane, int i, int width)
 {
-    if (w) {
-        load_group<kPack, NT>(v, w, lane, i, width);
+    if constexpr (kPack) {
+        return column<true, NT>(lane, i, 0) < width ? g : fill(0.0f);
     } else {
+        Group o;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = otherwise;
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = halves(g.p[e]);
+            o.p[e] = pair(column<false, NT>(lane, i, 2 * e) < width ? f.x : 0.0f,
+                          column<false, NT>(lane, i, 2 * e + 1) < width ? f.y : 0.0f);
+        }
+        return o;
     }
 }
 
-// The gate's row, in its own type: the block's or fp32 (a branch that all threads take alike).
-template <bool kPack, int NT, typename B>
-__device__ __forceinline__ void load_gate(float (&v)[8], const void* row, bool f32, int lane, int i, int width)
+// A vector of weights, or `otherwise` where there is none.
+template <bool kPack, int NT>
+__device__ __forceinline__ Group load_weights(const float* w, float otherwise, int lane, int i, int width)
 {
-    if (!row) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = 1.0f;
-    } else if (f32) {
-        load_group<kPack, NT>(v, static_cast<const float*>(row), lane, i, width);
+    return w ? load_group<kPack, NT>(w, lane, i, width) : fill(otherwise);
+}
+
+// A weight vector of `width` columns, or `otherwise`, into shared memory, with 0 behind it up to `room`.
+__device__ __forceinline__ void keep_weights(float* to, const float* w, float otherwise, int width, int room)
+{
+    for (int c = threadIdx.x; c < room; c += blockDim.x)
+        to[c] = c >= width ? 0.0f : w ? w[c] : otherwise;
+}
+
+// Group i of weights that lie in shared memory.
+template <bool kPack, int NT>
+__device__ __forceinline__ Group kept_group(const float* w, int lane, int i)
+{
+    if constexpr (kPack) {
+        const ulonglong2* at = reinterpret_cast<const ulonglong2*>(w + column<true, NT>(lane, i, 0));
+        const ulonglong2 x = at[0], y = at[1];
+        return {{x.x, x.y, y.x, y.y}};
     } else {
-        load_group<kPack, NT>(v, static_cast<const B*>(row), lane, i, width);
+        Group g;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            g.p[e] = pair(w[column<false, NT>(lane, i, 2 * e)], w[column<false, NT>(lane, i, 2 * e + 1)]);
+        return g;
     }
+}
+
+__device__ __forceinline__ float sum_of(uint64_t v)
+{
+    const float2 f = halves(v);
+    return f.x + f.y;
 }
 
 __device__ __forceinline__ const void* gate_row(const rowop_block_norm_args& a, int64_t r, int bytes)
 {
     return a.gate ? static_cast<const char*>(a.gate) + (a.rows_per_gate >= a.rows ? 0 : r / a.rows_per_gate) * a.ldg * bytes
                   : nullptr;
+}
+
+// The thread's group i of row r's gate, in the gate's type: the block's or
+// fp32 (a branch that all threads take alike). `off`: the first column.
+template <bool kPack, int NT, typename B>
+__device__ __forceinline__ Group gate_group(const rowop_block_norm_args& a, int64_t r, int lane, int i, int off, int width)
+{
+    const int bytes = a.gate_type == GEMM_C_F32 ? 4 : sizeof(B);
+    const char* gate = static_cast<const char*>(gate_row(a, r, bytes));
+    if (!gate)
+        return fill(1.0f);
+    gate += static_cast<int64_t>(off) * bytes;
+    if (bytes == 4)
+        return load_group<kPack, NT>(reinterpret_cast<const float*>(gate), lane, i, width);
+    return load_group<kPack, NT>(reinterpret_cast<const B*>(gate), lane, i, width);
 }
 
 // ---- rows through shared memory ------------------------------------------------------
@@ -213,32 +285,29 @@ struct Ring {
 
 // Group i of a row of `width` elements that lies in a stage; columns from `width` on are 0.
 template <bool kPack, int NT, typename T>
-__device__ __forceinline__ void stage_group(float (&v)[8], const unsigned char* stage, const Source& source, int64_t r, int lane,
-                                            int i, int width)
+__device__ __forceinline__ Group stage_group(const unsigned char* stage, const Source& source, int64_t r, int lane, int i, int width)
 {
     if constexpr (kPack) {
         const int c = column<true, NT>(lane, i, 0);
-        if (c < width) {
-            const uint4* at = reinterpret_cast<const uint4*>(stage + source.offset + c * sizeof(T));
-            if constexpr (sizeof(T) == 4) {
-                const uint4 a = at[0], b = at[1];
-                unpack(Pack<T>{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}}, v);
-            } else {
-                const uint4 a = at[0];
-                unpack(Pack<T>{{a.x, a.y, a.z, a.w}}, v);
-            }
+        if (c >= width)
+            return fill(0.0f);
+        const uint4* at = reinterpret_cast<const uint4*>(stage + source.offset + c * sizeof(T));
+        if constexpr (sizeof(T) == 4) {
+            const uint4 x = at[0], y = at[1];
+            return group_of(Pack<T>{{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}});
         } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = 0.0f;
+            const uint4 x = at[0];
+            return group_of(Pack<T>{{x.x, x.y, x.z, x.w}});
         }
     } else {
         const T* at = reinterpret_cast<const T*>(stage + source.offset + (source.row(r) & 15));
+        float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int c = column<false, NT>(lane, i, e);
             v[e] = c < width ? to_f32(at[c]) : 0.0f;
         }
+        return {{pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7])}};
     }
 }
 
@@ -273,95 +342,130 @@ __device__ __forceinline__ void ring_sums(float (&v)[N], float* scratch, int& tu
 
 // ---- forward -----------------------------------------------------------------------
 
+enum Weight { kPreGammaW, kPostGammaW, kGateW, kPreBetaW, kPostBetaW, kWeights };
+
+// A weight of all rows, or nullptr where there is none (1, or for a beta 0).
+__device__ __forceinline__ const float* weight_vector(const rowop_block_norm_args& a, int w)
+{
+    return w == kPreGammaW    ? (a.pre_norm != ROWOP_NORM_NONE ? a.pre_gamma : nullptr)
+           : w == kPostGammaW ? (a.post_norm != ROWOP_NORM_NONE ? a.post_gamma : nullptr)
+           : w == kPreBetaW   ? (a.pre_norm == ROWOP_NORM_LAYER ? a.pre_beta : nullptr)
+           : w == kPostBetaW  ? (a.post_norm == ROWOP_NORM_LAYER ? a.post_beta : nullptr)
+                              : nullptr;
+}
+
 // Mean and reciprocal deviation of a row held as NV groups a thread. The
 // variance is summed from the deviations, after the mean: the difference of
-// two large sums would lose what rows far from 0 have of it.
-template <bool kPack, int NT, int NV, typename Sums>
-__device__ __forceinline__ void moments(const float (&v)[NV][8], int width, int kind, float eps, int lane, Sums sums,
-                                        float& mean, float& r)
+// two large sums would lose what rows far from 0 have of it. Without a Layer
+// norm the mean is 0, and columns past the row's end hold 0 and add nothing.
+template <bool kLayer, bool kPack, int NT, int NV, typename Sums>
+__device__ __forceinline__ void moments(const Group (&v)[NV], int width, int kind, float eps, int lane, Sums sums, float& mean,
+                                        float& r)
 {
     const float inv = 1.0f / static_cast<float>(width);
     mean = 0.0f;
-    if (kind == ROWOP_NORM_LAYER) {
-        float s[1] = {0.0f};
+    uint64_t q = 0;
+    if (kLayer && kind == ROWOP_NORM_LAYER) {
+        uint64_t s = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                s[0] += v[i][e];
-        sums(s);
-        mean = s[0] * inv;
-    }
-    float q[1] = {0.0f};
+            for (int e = 0; e < 4; ++e)
+                s = add2(s, v[i].p[e]);
+        float total[1] = {sum_of(s)};
+        sums(total);
+        mean = total[0] * inv;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {
+            Group d;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float d = column<kPack, NT>(lane, i, e) < width ? v[i][e] - mean : 0.0f;
-            q[0] = fmaf(d, d, q[0]);
+            for (int e = 0; e < 4; ++e)
+                d.p[e] = add2(v[i].p[e], both(-mean));
+            d = inside<kPack, NT>(d, lane, i, width);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                q = fma2(d.p[e], d.p[e], q);
         }
-    sums(q);
-    r = 1.0f / sqrtf(q[0] * inv + eps);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                q = fma2(v[i].p[e], v[i].p[e], q);
+    }
+    float total[1] = {sum_of(q)};
+    sums(total);
+    r = 1.0f / sqrtf(total[0] * inv + eps);
 }
 
 // v = (v - mean) r gamma + beta
-template <bool kPack, int NT>
-__device__ __forceinline__ void apply(float (&v)[8], float mean, float r, const float* gamma, const float* beta, int lane,
-                                      int i, int width)
+template <bool kLayer, typename WeightAt>
+__device__ __forceinline__ void apply(Group& v, float mean, float r, WeightAt weight, int gamma, int beta, int i)
 {
-    float g[8], b[8];
-    load_weights<kPack, NT>(g, gamma, 1.0f, lane, i, width);
-    load_weights<kPack, NT>(b, beta, 0.0f, lane, i, width);
+    const Group g = weight(gamma, i);
+    const uint64_t r2 = both(r);
+    if constexpr (kLayer) {
+        const Group b = weight(beta, i);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        v[e] = fmaf((v[e] - mean) * r, g[e], b[e]);
+        for (int e = 0; e < 4; ++e)
+            v.p[e] = fma2(mul2(add2(v.p[e], both(-mean)), r2), g.p[e], b.p[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v.p[e] = mul2(mul2(v.p[e], r2), g.p[e]);
+    }
 }
 
-// What follows a row's read: v is y's share, x(i) gives x's groups; writes h,
-// z and the statistics. `lane` is the thread's place among the NT of its row.
-template <typename B, typename S, int NT, int NV, bool kPack, typename X, typename Sums>
-__device__ __forceinline__ void finish_row(const rowop_block_norm_args& a, int64_t r, float (&v)[NV][8], int lane, X x, Sums sums)
+// What follows a row's read: v is y's share, x(i) gives x's groups, weight(w,
+// i) a weight's; writes h, z and the statistics. `lane` is the thread's place
+// among the NT of its row.
+template <typename B, typename S, int NT, int NV, bool kPack, bool kLayer, typename X, typename WeightAt, typename Sums>
+__device__ __forceinline__ void finish_row(const rowop_block_norm_args& a, int64_t r, Group (&v)[NV], int lane, X x, WeightAt weight,
+                                           Sums sums)
 {
     const int width = static_cast<int>(a.width);
-    const bool gate_f32 = a.gate_type == GEMM_C_F32;
     float mean, rs;
     if (a.post_norm != ROWOP_NORM_NONE) {
-        moments<kPack, NT, NV>(v, width, a.post_norm, a.post_eps, lane, sums, mean, rs);
+        moments<kLayer, kPack, NT, NV>(v, width, a.post_norm, a.post_eps, lane, sums, mean, rs);
         if (a.post_stats && lane == 0)
             a.post_stats[2 * r] = mean, a.post_stats[2 * r + 1] = rs;
-        const float* beta = a.post_norm == ROWOP_NORM_LAYER ? a.post_beta : nullptr;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            apply<kPack, NT>(v[i], mean, rs, a.post_gamma, beta, lane, i, width);
+            apply<kLayer>(v[i], mean, rs, weight, kPostGammaW, kPostBetaW, i);
     }
-    const void* gate = gate_row(a, r, gate_f32 ? 4 : sizeof(B));
     S* h = static_cast<S*>(a.h) + r * a.ldh;
+    const uint64_t residual = both(a.residual_scale), branch = both(a.branch_scale);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        float g[8], u[8];
-        x(u, i);
-        load_gate<kPack, NT, B>(g, gate, gate_f32, lane, i, width);
+        const Group u = x(i);
+        if (a.gate) {
+            const Group g = weight(kGateW, i);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[i][e] = column<kPack, NT>(lane, i, e) < width ? fmaf(a.residual_scale, u[e], a.branch_scale * (v[i][e] * g[e])) : 0.0f;
+            for (int e = 0; e < 4; ++e)
+                v[i].p[e] = mul2(v[i].p[e], g.p[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[i].p[e] = fma2(residual, u.p[e], mul2(branch, v[i].p[e]));
+        if (kLayer)
+            v[i] = inside<kPack, NT>(v[i], lane, i, width);
         store_group<kPack, NT>(h, v[i], lane, i, width);
     }
     if (a.pre_norm == ROWOP_NORM_NONE)
         return;
-    moments<kPack, NT, NV>(v, width, a.pre_norm, a.pre_eps, lane, sums, mean, rs);
+    moments<kLayer, kPack, NT, NV>(v, width, a.pre_norm, a.pre_eps, lane, sums, mean, rs);
     if (a.pre_stats && lane == 0)
         a.pre_stats[2 * r] = mean, a.pre_stats[2 * r + 1] = rs;
-    const float* beta = a.pre_norm == ROWOP_NORM_LAYER ? a.pre_beta : nullptr;
     B* z = static_cast<B*>(a.z) + r * a.ldz;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        apply<kPack, NT>(v[i], mean, rs, a.pre_gamma, beta, lane, i, width);
+        apply<kLayer>(v[i], mean, rs, weight, kPreGammaW, kPreBetaW, i);
         store_group<kPack, NT>(z, v[i], lane, i, width);
     }
 }
 
 // Few rows, or narrow ones that a warp holds: rows straight into registers.
-template <typename B, typename S, int NT, int NV, bool kPack>
+template <typename B, typename S, int NT, int NV, bool kPack, bool kLayer>
 __global__ void __launch_bounds__(NT == 32 ? 128 : NT) sat_block_norm_kernel(const __grid_constant__ rowop_block_norm_args a)
 {
     __shared__ float scratch[2 * (NT / 32)];
@@ -372,29 +476,46 @@ __global__ void __launch_bounds__(NT == 32 ? 128 : NT) sat_block_norm_kernel(con
          r += gridDim.x * static_cast<int64_t>(kRows)) {
         const B* y = static_cast<const B*>(a.y) + r * a.ldy;
         const S* x = static_cast<const S*>(a.x) + r * a.ldx;
-        float v[NV][8], u[NV][8];
+        Group v[NV], u[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            load_group<kPack, NT>(v[i], y, lane, i, width);
+            v[i] = load_group<kPack, NT>(y, lane, i, width);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            load_group<kPack, NT>(u[i], x, lane, i, width);
-        finish_row<B, S, NT, NV, kPack>(
-            a, r, v, lane,
-            [&](float(&to)[8], int i) {
+            u[i] = load_group<kPack, NT>(x, lane, i, width);
+        // With one group a thread, the weights too are read before the first reduction.
+        constexpr bool kEarly = NV == 1;
+        Group early[kEarly ? kWeights : 1];
+        auto read = [&](int w, int i) {
+            return w == kGateW ? gate_group<kPack, NT, B>(a, r, lane, i, 0, width)
+                               : load_weights<kPack, NT>(weight_vector(a, w), w >= kPreBetaW ? 0.0f : 1.0f, lane, i, width);
+        };
+        if constexpr (kEarly) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    to[e] = u[i][e];
+            for (int w = 0; w < (kLayer ? kWeights : kPreBetaW); ++w)
+                early[w] = read(w, 0);
+        }
+        finish_row<B, S, NT, NV, kPack, kLayer>(
+            a, r, v, lane, [&](int i) { return u[i]; },
+            [&](int w, int i) {
+                if constexpr (kEarly)
+                    return early[w];
+                else
+                    return read(w, i);
             },
             [&](float(&s)[1]) { row_sums<NT>(s, scratch, turn); });
     }
 }
 
+// CTAs an SM that the ring's forward kernel is made for: a wide row's threads fill it.
+template <int NT>
+constexpr int kForwardPerSM = NT == 512 ? 1 : NT == 256 ? 2 : 4;
+
 // Many rows: a CTA's NT threads take every gridDim.x-th, through a ring of
-// `stages` stages of `stage_bytes`.
-template <typename B, typename S, int NT, int NV, bool kPack>
-__global__ void __launch_bounds__(NT + 32, NT == 512 ? (NV == 4 ? 1 : 2) : NT == 256 ? 3 : 5)
-    sat_block_norm_ring_kernel(const __grid_constant__ rowop_block_norm_args a, int stages, int stage_bytes)
+// `stages` stages of `stage_bytes`. `kept`: the weights lie behind the ring.
+template <typename B, typename S, int NT, int NV, bool kPack, bool kLayer>
+__global__ void __launch_bounds__(NT + 32, kForwardPerSM<NT>)
+    sat_block_norm_ring_kernel(const __grid_constant__ rowop_block_norm_args a, int stages, int stage_bytes, bool kept)
 {
     extern __shared__ __align__(128) unsigned char ring_memory[];
     __shared__ __align__(8) Ring ring;
@@ -404,6 +525,26 @@ __global__ void __launch_bounds__(NT + 32, NT == 512 ? (NV == 4 ? 1 : 2) : NT ==
     const Source sources[2] = {
         {static_cast<const char*>(a.y), a.ldy * static_cast<int64_t>(sizeof(B)), width * static_cast<int>(sizeof(B)), 0},
         {static_cast<const char*>(a.x), a.ldx * static_cast<int64_t>(sizeof(S)), width * static_cast<int>(sizeof(S)), y_bytes}};
+    constexpr int room = NT * NV * 8;
+    float* weights = reinterpret_cast<float*>(ring_memory + stages * stage_bytes);
+    const bool shared_gate = a.gate && a.rows_per_gate >= a.rows;
+    // Kept weights lie one after another in the order of Weight, those that the call does not have left out.
+    auto place = [&](int w) {
+        int at = 0;
+        for (int v = 0; v < w; ++v)
+            at += v == kGateW ? shared_gate : weight_vector(a, v) != nullptr;
+        return weights + at * room;
+    };
+    if (kept)
+        for (int w = 0; w < kWeights; ++w) {
+            if (w != kGateW && weight_vector(a, w))
+                keep_weights(place(w), weight_vector(a, w), 1.0f, width, room);
+            if (w == kGateW && shared_gate)
+                for (int c = threadIdx.x; c < room; c += blockDim.x)
+                    place(w)[c] = c >= width ? 0.0f
+                                  : a.gate_type == GEMM_C_F32 ? static_cast<const float*>(a.gate)[c]
+                                                              : to_f32(static_cast<const B*>(a.gate)[c]);
+        }
     if (threadIdx.x == 0)
         ring.init(stages, NT / 32);
     __syncthreads();
@@ -418,22 +559,31 @@ __global__ void __launch_bounds__(NT + 32, NT == 512 ? (NV == 4 ? 1 : 2) : NT ==
         return;
     }
     const int lane = threadIdx.x;
+    const float* at[kWeights];
+#pragma unroll
+    for (int w = 0; w < kWeights; ++w)
+        at[w] = kept && (w == kGateW ? shared_gate : weight_vector(a, w) != nullptr) ? place(w) : nullptr;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         ring.take(s, round, failed);
         const unsigned char* stage = ring_memory + s * stage_bytes;
-        float v[NV][8];
+        Group v[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            stage_group<kPack, NT, B>(v[i], stage, sources[0], r, lane, i, width);
-            if (failed)
-                v[i][0] = NAN;
-        }
-        finish_row<B, S, NT, NV, kPack>(
+        for (int i = 0; i < NV; ++i)
+            v[i] = failed ? fill(NAN) : stage_group<kPack, NT, B>(stage, sources[0], r, lane, i, width);
+        finish_row<B, S, NT, NV, kPack, kLayer>(
             a, r, v, lane,
-            [&](float(&to)[8], int i) {
-                stage_group<kPack, NT, S>(to, stage, sources[1], r, lane, i, width);
+            [&](int i) {
+                const Group u = stage_group<kPack, NT, S>(stage, sources[1], r, lane, i, width);
                 if (i == NV - 1)
                     ring.release(s);
+                return u;
+            },
+            [&](int w, int i) {
+                if (at[w])
+                    return kept_group<kPack, NT>(at[w], lane, i);
+                if (w == kGateW)
+                    return gate_group<kPack, NT, B>(a, r, lane, i, 0, width);
+                return load_weights<kPack, NT>(weight_vector(a, w), w >= kPreBetaW ? 0.0f : 1.0f, lane, i, width);
             },
             [&](float(&v)[1]) { ring_sums<NT>(v, scratch, turn); });
         if (++s == stages)
@@ -441,90 +591,104 @@ __global__ void __launch_bounds__(NT + 32, NT == 512 ? (NV == 4 ? 1 : 2) : NT ==
     }
 }
 
-template <typename B, typename S, int NT, int NV, bool kPack>
+template <typename B, typename S, int NT, int NV, bool kPack, bool kLayer>
 cudaError_t launch_forward(const rowop_block_norm_args& a, cudaStream_t s)
 {
     const int64_t ctas = NT == 32 ? (a.rows + 3) / 4 : a.rows;
-    sat_block_norm_kernel<B, S, NT, NV, kPack>
+    sat_block_norm_kernel<B, S, NT, NV, kPack, kLayer>
         <<<static_cast<unsigned>(ctas < (1 << 20) ? ctas : (1 << 20)), NT == 32 ? 128 : NT, 0, s>>>(a);
     return cudaGetLastError();
 }
 
-template <typename B, typename S, int NT, int NV, bool kPack>
+template <typename B, typename S, int NT, int NV, bool kPack, bool kLayer>
 cudaError_t launch_ring(const rowop_block_norm_args& a, cudaStream_t s)
 {
-    constexpr int per_sm = NT == 512 ? (NV == 4 ? 1 : 2) : NT == 256 ? 3 : 5;
+    constexpr int per_sm = kForwardPerSM<NT>;
     if (a.rows < 2 * per_sm * kSMs)  // under two rows a CTA there is nothing to fetch ahead
-        return launch_forward<B, S, NT, NV, kPack>(a, s);
+        return launch_forward<B, S, NT, NV, kPack, kLayer>(a, s);
     const int64_t w = a.width;
     const int stage = static_cast<int>((w * sizeof(B) + 31) / 16 * 16 + (w * sizeof(S) + 31) / 16 * 16);
-    const int room = kSmemPerSM / per_sm - 1024;
-    int stages = room / stage;
+    constexpr int room = kSmemPerSM / per_sm - 2048;
+    const bool post = a.post_norm != ROWOP_NORM_NONE, pre = a.pre_norm != ROWOP_NORM_NONE;
+    int weights = (post && a.post_gamma) + (pre && a.pre_gamma) + (a.gate && a.rows_per_gate >= a.rows) +
+                  (a.post_norm == ROWOP_NORM_LAYER && a.post_beta) + (a.pre_norm == ROWOP_NORM_LAYER && a.pre_beta);
+    weights *= NT * NV * 8 * 4;
+    // Weights stay on chip where two rows fit beside them.
+    const bool kept = room - weights >= 2 * stage;
+    int stages = (kept ? room - weights : room) / stage;
     stages = stages < kMaxStages ? stages : kMaxStages;
-    auto kernel = sat_block_norm_ring_kernel<B, S, NT, NV, kPack>;
+    if (stages < 2)
+        return launch_forward<B, S, NT, NV, kPack, kLayer>(a, s);
+    auto kernel = sat_block_norm_ring_kernel<B, S, NT, NV, kPack, kLayer>;
     static Prepared prepared;
     const cudaError_t e = prepared.once(reinterpret_cast<const void*>(kernel), room);
     if (e != cudaSuccess)
         return e;
-    kernel<<<static_cast<unsigned>(per_sm * kSMs), NT + 32, stages * stage, s>>>(a, stages, stage);
+    kernel<<<static_cast<unsigned>(per_sm * kSMs), NT + 32, stages * stage + (kept ? weights : 0), s>>>(a, stages, stage, kept);
     return cudaGetLastError();
+}
+
+template <typename B, typename S, bool kPack, bool kLayer>
+cudaError_t choose_forward_as(const rowop_block_norm_args& a, cudaStream_t s)
+{
+    // Four groups a thread, so that a row's fixed work (the reductions, its
+    // addresses) is spread over 32 columns; few rows take more threads each.
+    if (a.width <= 256)
+        return launch_forward<B, S, 32, 1, kPack, kLayer>(a, s);
+    if (a.width <= 1024)
+        return a.rows < 4 * kSMs ? launch_forward<B, S, 128, 1, kPack, kLayer>(a, s) : launch_forward<B, S, 32, 4, kPack, kLayer>(a, s);
+    if (a.width <= 4096)
+        return a.rows < 4 * kSMs ? launch_forward<B, S, 512, 1, kPack, kLayer>(a, s) : launch_ring<B, S, 128, 4, kPack, kLayer>(a, s);
+    if (a.width <= 8192)
+        return launch_ring<B, S, 256, 4, kPack, kLayer>(a, s);
+    return launch_ring<B, S, 512, 4, kPack, kLayer>(a, s);
 }
 
 template <typename B, typename S, bool kPack>
 cudaError_t choose_forward(const rowop_block_norm_args& a, cudaStream_t s)
 {
-    if (a.width <= 256)
-        return launch_forward<B, S, 32, 1, kPack>(a, s);
-    if (a.width <= 1024)
-        return launch_ring<B, S, 128, 1, kPack>(a, s);
-    if (a.width <= 2048)
-        return launch_ring<B, S, 256, 1, kPack>(a, s);
-    if (a.width <= 4096)
-        return launch_ring<B, S, 512, 1, kPack>(a, s);
-    if (a.width <= 8192)
-        return launch_ring<B, S, 512, 2, kPack>(a, s);
-    return launch_ring<B, S, 512, 4, kPack>(a, s);
+    return a.post_norm == ROWOP_NORM_LAYER || a.pre_norm == ROWOP_NORM_LAYER ? choose_forward_as<B, S, kPack, true>(a, s)
+                                                                             : choose_forward_as<B, S, kPack, false>(a, s);
 }
 
 // ---- backward ----------------------------------------------------------------------
 
-// The sources of the backward pass, and its weights.
+// The sources of the backward pass.
 enum Input { kDh, kDz, kH, kY, kInputs };
-enum Weight { kPreGammaW, kPostGammaW, kGateW, kPostBetaW, kWeights };
-
-// A weight of all rows, or nullptr where there is none (1, or for a beta 0).
-__device__ __forceinline__ const float* weight_vector(const rowop_block_norm_args& a, int w)
-{
-    return w == kPreGammaW    ? (a.pre_norm != ROWOP_NORM_NONE ? a.pre_gamma : nullptr)
-           : w == kPostGammaW ? (a.post_norm != ROWOP_NORM_NONE ? a.post_gamma : nullptr)
-           : w == kPostBetaW  ? (a.post_norm == ROWOP_NORM_LAYER ? a.post_beta : nullptr)
-                              : nullptr;
-}
-
-// The thread's group of row r's gate.
-template <bool kPack, int NT, typename B>
-__device__ __forceinline__ void gate_group(float (&v)[8], const rowop_block_norm_args& a, int64_t r, int lane, int off, int width)
-{
-    const int bytes = a.gate_type == GEMM_C_F32 ? 4 : sizeof(B);
-    const char* gate = static_cast<const char*>(gate_row(a, r, bytes));
-    load_gate<kPack, NT, B>(v, gate ? gate + static_cast<int64_t>(off) * bytes : nullptr, bytes == 4, lane, 0, width);
-}
 
 // A part's rows in order, with the sums over rows of the thread's own eight
-// columns in registers. `at(v, input, r)` gives the thread's group of a
-// matrix, `weight(v, w, r)` of a weight, `sums` adds over the row, `done(r)` is
-// called when the row's inputs have been read. `off` is the first of the CTA's
-// columns, `width` their number.
-template <typename B, typename S, int NT, bool kPack, bool kBeta, typename At, typename WeightAt, typename Sums, typename Done>
+// columns in registers. With t = dz gamma_pre, u = dh + r_pre t, hh and yh the
+// normed h and y and w = branch_scale gate gamma_post, the gradient of h is
+//
+//   D = u - r_pre (s0 + hh s1),   s1 = mean(t hh),  s0 = mean(t) (Layer)
+//
+// and the second norm's means, of w D yh and (Layer) w D, are linear in s0 and
+// s1: the sums that they are made of need nothing of the first norm, so a row
+// has one reduction and not two in turn. Columns past the row's end have
+// weights of 0 and gradients of 0.
+//
+// `at(input, r)` gives the thread's group of a matrix, `weight(w)` of a weight
+// and `gate(r)` of the gate, `sums` adds over the row once its inputs have been
+// read, `done()` ends it. `off` is the first of the CTA's columns, `width`
+// their number.
+template <typename B, typename S, int NT, int NV, bool kPack, int MODE, typename At, typename WeightAt, typename GateAt,
+          typename Sums, typename Done>
 __device__ __forceinline__ void backward_rows(const rowop_block_norm_args& a, const rowop_block_norm_grads& g, const Split& split,
-                                              int64_t part, int lane, int off, int width, At at, WeightAt weight, Sums sums,
-                                              Done done)
+                                              int64_t part, int lane, int off, int width, At at, WeightAt weight, GateAt gate,
+                                              Sums sums, Done done)
 {
+    constexpr bool kBeta = MODE != kRms, kGrouped = MODE == kLayerGrouped;
     const float inv = 1.0f / static_cast<float>(a.width);
     const bool pre = a.pre_norm != ROWOP_NORM_NONE, post = a.post_norm != ROWOP_NORM_NONE;
     const bool pre_layer = a.pre_norm == ROWOP_NORM_LAYER, post_layer = a.post_norm == ROWOP_NORM_LAYER;
-    const bool gate_f32 = a.gate_type == GEMM_C_F32;
-    float acc[kBeta ? kSums : kPreBeta][8] = {};
+    // A gate that all rows share multiplies the sums at the end; one that changes, the rows.
+    const bool grouped = kGrouped || (MODE == kRms && a.gate && a.rows_per_gate < a.rows);
+    const uint64_t branch = both(a.branch_scale), residual = both(a.residual_scale);
+    // Sums over rows of dz hh, D yh, gate D yh and, for betas, dz, D, gate D.
+    Group dz_hh[NV], d_yh[NV], gd_yh[NV], dz_1[NV], d_1[NV], gd_1[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        dz_hh[i] = d_yh[i] = gd_yh[i] = dz_1[i] = d_1[i] = gd_1[i] = fill(0.0f);
     int64_t first, end;
     split.range(part, a.rows, first, end);
     int64_t flush = split.direct ? min((first / a.rows_per_gate + 1) * a.rows_per_gate, end) : end;
@@ -534,97 +698,160 @@ __device__ __forceinline__ void backward_rows(const rowop_block_norm_args& a, co
         return make_float4(pre ? a.pre_stats[i] : 0.0f, pre ? a.pre_stats[i + 1] : 1.0f, post ? a.post_stats[i] : 0.0f,
                            post ? a.post_stats[i + 1] : 1.0f);
     };
+    // The gradient of the gate, of sums over its rows.
+    auto gate_grad = [&](int i) {
+        const Group gamma = weight(kPostGammaW, i), beta = kBeta ? weight(kPostBetaW, i) : fill(0.0f);
+        Group o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            o.p[e] = mul2(branch, kBeta ? fma2(gamma.p[e], d_yh[i].p[e], mul2(beta.p[e], d_1[i].p[e])) : mul2(gamma.p[e], d_yh[i].p[e]));
+        return o;
+    };
     float4 ahead = first < end ? stats(first) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int64_t r = first; r < end; ++r) {
-        float d[8], t[8], w[8], hh[8], sum[2] = {0.0f, 0.0f};
-        const float pre_mean = ahead.x, pre_rs = ahead.y, mean = ahead.z, rs = ahead.w;
+    S* dx = static_cast<S*>(g.dx) + first * g.lddx + off;
+    B* dy = static_cast<B*>(g.dy) + first * g.lddy + off;
+    for (int64_t r = first; r < end; ++r, dx += g.lddx, dy += g.lddy) {
+        const float4 st = ahead;
         ahead = stats(r + 1);
-        at(d, kDh, r);
-        if (pre) {
-            at(t, kDz, r);
-            at(hh, kH, r);
-            weight(w, kPreGammaW, r);
+        const uint64_t pre_rs = both(st.y), rs = both(st.w);
+        Group u[NV], hh[NV], yh[NV], w[NV];
+        uint64_t s[kBeta ? 8 : 3] = {};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                hh[e] = (hh[e] - pre_mean) * pre_rs;  // of a column past the row's end: not 0, but t is
-                acc[kPreGamma][e] = fmaf(t[e], hh[e], acc[kPreGamma][e]);
+        for (int i = 0; i < NV; ++i) {
+            u[i] = at(kDh, r, i), yh[i] = at(kY, r, i), w[i] = weight(kPostGammaW, i), hh[i] = fill(0.0f);
+            Group dz = fill(0.0f);
+            if (pre) {
+                dz = at(kDz, r, i);
+                hh[i] = at(kH, r, i);
+                const Group gamma = weight(kPreGammaW, i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (kBeta)
+                        hh[i].p[e] = add2(hh[i].p[e], both(-st.x));
+                    hh[i].p[e] = mul2(hh[i].p[e], pre_rs);
+                    dz_hh[i].p[e] = fma2(dz.p[e], hh[i].p[e], dz_hh[i].p[e]);
+                    if constexpr (kBeta)
+                        dz_1[i].p[e] = add2(dz_1[i].p[e], dz.p[e]);
+                    dz.p[e] = mul2(dz.p[e], gamma.p[e]);
+                    u[i].p[e] = fma2(dz.p[e], pre_rs, u[i].p[e]);
+                }
+            }
+            const Group gr = gate(r, i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
                 if constexpr (kBeta)
-                    acc[kPreBeta][e] += t[e];
-                t[e] *= w[e];
-                sum[0] = fmaf(t[e], hh[e], sum[0]);
-                sum[1] += t[e];
+                    yh[i].p[e] = add2(yh[i].p[e], both(-st.z));
+                yh[i].p[e] = mul2(yh[i].p[e], rs);
+                w[i].p[e] = mul2(mul2(w[i].p[e], branch), gr.p[e]);
+                const uint64_t c = mul2(w[i].p[e], yh[i].p[e]);
+                s[0] = fma2(dz.p[e], hh[i].p[e], s[0]);
+                s[1] = fma2(c, u[i].p[e], s[1]);
+                s[2] = fma2(c, hh[i].p[e], s[2]);
+                if constexpr (kBeta) {
+                    s[3] = add2(s[3], dz.p[e]);
+                    s[4] = add2(s[4], c);
+                    s[5] = fma2(w[i].p[e], u[i].p[e], s[5]);
+                    s[6] = add2(s[6], w[i].p[e]);
+                    s[7] = fma2(w[i].p[e], hh[i].p[e], s[7]);
+                }
             }
-            sums(sum);
-            const float s1 = sum[0] * inv, s0 = pre_layer ? sum[1] * inv : 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                d[e] += column<kPack, NT>(lane, 0, e) < width ? pre_rs * (t[e] - s0 - hh[e] * s1) : 0.0f;
         }
-        if (g.dx) {
+        constexpr int K = kBeta ? 8 : 3;
+        float sum[K];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                t[e] = a.residual_scale * d[e];
-            store_group<kPack, NT>(static_cast<S*>(g.dx) + r * g.lddx + off, t, lane, 0, width);
-        }
-        at(hh, kY, r);
-        done(r);
-        weight(w, kPostGammaW, r);
+        for (int k = 0; k < K; ++k)
+            sum[k] = sum_of(s[k]);
+        sums(sum);
+        done();
+        const float s1 = sum[0] * inv, s0 = kBeta && pre_layer ? sum[3] * inv : 0.0f;
+        float e1 = sum[1] - st.y * s1 * sum[2], e0 = 0.0f;
         if constexpr (kBeta) {
-            weight(t, kPostBetaW, r);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                t[e] = 0.0f;
+            e1 -= st.y * s0 * sum[4];
+            e0 = post_layer ? (sum[5] - st.y * (s0 * sum[6] + s1 * sum[7])) * inv : 0.0f;
         }
+        e1 = post ? e1 * inv : 0.0f;
+        const uint64_t h_by = both(-st.y * s1), h_less = both(-st.y * s0), y_by = both(-e1), y_less = both(-e0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            hh[e] = (hh[e] - mean) * rs;
-            d[e] *= a.branch_scale;
-            acc[kGate][e] = fmaf(d[e], fmaf(hh[e], w[e], t[e]), acc[kGate][e]);
-        }
-        weight(t, kGateW, r);
-        sum[0] = sum[1] = 0.0f;
+        for (int i = 0; i < NV; ++i) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            d[e] *= t[e];
-            acc[kPostGamma][e] = fmaf(d[e], hh[e], acc[kPostGamma][e]);
-            if constexpr (kBeta)
-                acc[kPostBeta][e] += d[e];
-            d[e] *= w[e];
-            sum[0] = fmaf(d[e], hh[e], sum[0]);
-            sum[1] += d[e];
-        }
-        if (post) {
-            sums(sum);
-            const float s1 = sum[0] * inv, s0 = post_layer ? sum[1] * inv : 0.0f;
+            for (int e = 0; e < 4; ++e) {
+                u[i].p[e] = fma2(hh[i].p[e], h_by, u[i].p[e]);
+                if constexpr (kBeta)
+                    u[i].p[e] = add2(u[i].p[e], h_less);
+            }
+            if (kBeta && pre_layer)
+                u[i] = inside<kPack, NT>(u[i], lane, i, width);
+            Group o;
+            if (g.dx) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                d[e] = rs * (d[e] - s0 - hh[e] * s1);
-        }
-        if (g.dy)
-            store_group<kPack, NT>(static_cast<B*>(g.dy) + r * g.lddy + off, d, lane, 0, width);
-        if (split.direct && r + 1 == flush) {  // the gate row's last row
-            if (g.dgate) {
-                const int64_t to = r / a.rows_per_gate * g.lddg + off;
-                if (gate_f32)
-                    store_group<kPack, NT>(static_cast<float*>(g.dgate) + to, acc[kGate], lane, 0, width);
-                else
-                    store_group<kPack, NT>(static_cast<B*>(g.dgate) + to, acc[kGate], lane, 0, width);
+                for (int e = 0; e < 4; ++e)
+                    o.p[e] = mul2(residual, u[i].p[e]);
+                store_group<kPack, NT>(dx, o, lane, i, width);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                acc[kGate][e] = 0.0f;
-            flush = min(flush + a.rows_per_gate, end);
+            for (int e = 0; e < 4; ++e) {
+                d_yh[i].p[e] = fma2(u[i].p[e], yh[i].p[e], d_yh[i].p[e]);
+                if constexpr (kBeta)
+                    d_1[i].p[e] = add2(d_1[i].p[e], u[i].p[e]);
+                o.p[e] = fma2(yh[i].p[e], y_by, mul2(w[i].p[e], u[i].p[e]));
+                if constexpr (kBeta)
+                    o.p[e] = add2(o.p[e], y_less);
+                o.p[e] = mul2(o.p[e], rs);
+            }
+            if (g.dy)
+                store_group<kPack, NT>(dy, o, lane, i, width);
+            if (MODE != kLayerShared && grouped) {
+                const Group gr = gate(r, i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t gd = mul2(gr.p[e], u[i].p[e]);
+                    gd_yh[i].p[e] = fma2(gd, yh[i].p[e], gd_yh[i].p[e]);
+                    if constexpr (kBeta)
+                        gd_1[i].p[e] = add2(gd_1[i].p[e], gd);
+                }
+                if (split.direct && r + 1 == flush) {  // the gate row's last row
+                    const int64_t to = r / a.rows_per_gate * g.lddg + off;
+                    if (a.gate_type == GEMM_C_F32)
+                        store_group<kPack, NT>(static_cast<float*>(g.dgate) + to, gate_grad(i), lane, i, width);
+                    else
+                        store_group<kPack, NT>(static_cast<B*>(g.dgate) + to, gate_grad(i), lane, i, width);
+                    d_yh[i] = d_1[i] = fill(0.0f);
+                }
+            }
         }
+        if (split.direct && r + 1 == flush)
+            flush = min(flush + a.rows_per_gate, end);
     }
     float* out = static_cast<float*>(g.workspace) + part * split.sums * split.stride + off;
 #pragma unroll
-    for (int s = 0; s < (kBeta ? kSums : kPreBeta); ++s)
-        store_group<kPack, NT>(out + s * split.stride, acc[s], lane, 0, width);
+    for (int i = 0; i < NV; ++i) {
+        store_group<kPack, NT>(out + kPreGamma * split.stride, dz_hh[i], lane, i, width);
+        store_group<kPack, NT>(out + kGate * split.stride, gate_grad(i), lane, i, width);
+        if (!grouped) {
+            const Group gr = gate(first, i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                gd_yh[i].p[e] = mul2(gr.p[e], d_yh[i].p[e]);
+                if constexpr (kBeta)
+                    gd_1[i].p[e] = mul2(gr.p[e], d_1[i].p[e]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            gd_yh[i].p[e] = mul2(branch, gd_yh[i].p[e]);
+            if constexpr (kBeta)
+                gd_1[i].p[e] = mul2(branch, gd_1[i].p[e]);
+        }
+        store_group<kPack, NT>(out + kPostGamma * split.stride, gd_yh[i], lane, i, width);
+        if constexpr (kBeta) {
+            store_group<kPack, NT>(out + kPreBeta * split.stride, dz_1[i], lane, i, width);
+            store_group<kPack, NT>(out + kPostBeta * split.stride, gd_1[i], lane, i, width);
+        }
+    }
 }
 
 // Narrow rows: a warp a part, rows straight into registers.
-template <typename B, typename S, bool kPack, bool kBeta>
+template <typename B, typename S, bool kPack, int MODE>
 __global__ void __launch_bounds__(128)
     sat_block_norm_backward_kernel(const __grid_constant__ rowop_block_norm_args a,
                                    const __grid_constant__ rowop_block_norm_grads g, const Split split)
@@ -634,165 +861,213 @@ __global__ void __launch_bounds__(128)
         return;
     const int lane = threadIdx.x % 32, width = static_cast<int>(a.width);
     int turn = 0;
-    backward_rows<B, S, 32, kPack, kBeta>(
+    backward_rows<B, S, 32, 1, kPack, MODE>(
         a, g, split, part, lane, 0, width,
-        [&](float(&v)[8], int input, int64_t r) {
-            if (input == kDz)
-                load_group<kPack, 32>(v, static_cast<const B*>(g.dz) + r * g.lddz, lane, 0, width);
-            else if (input == kY)
-                load_group<kPack, 32>(v, static_cast<const B*>(a.y) + r * a.ldy, lane, 0, width);
-            else if (input == kH)
-                load_group<kPack, 32>(v, static_cast<const S*>(a.h) + r * a.ldh, lane, 0, width);
-            else if (g.dh)
-                load_group<kPack, 32>(v, static_cast<const S*>(g.dh) + r * g.lddh, lane, 0, width);
-            else
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] = 0.0f;
+        [&](int input, int64_t r, int) {
+            return input == kDz  ? load_group<kPack, 32>(static_cast<const B*>(g.dz) + r * g.lddz, lane, 0, width)
+                   : input == kY ? load_group<kPack, 32>(static_cast<const B*>(a.y) + r * a.ldy, lane, 0, width)
+                   : input == kH ? load_group<kPack, 32>(static_cast<const S*>(a.h) + r * a.ldh, lane, 0, width)
+                   : g.dh        ? load_group<kPack, 32>(static_cast<const S*>(g.dh) + r * g.lddh, lane, 0, width)
+                                 : fill(0.0f);
         },
-        [&](float(&v)[8], int w, int64_t r) {
-            if (w == kGateW)
-                gate_group<kPack, 32, B>(v, a, r, lane, 0, width);
-            else
-                load_weights<kPack, 32>(v, weight_vector(a, w), w == kPostBetaW ? 0.0f : 1.0f, lane, 0, width);
+        [&](int w, int) {
+            return inside<kPack, 32>(load_weights<kPack, 32>(weight_vector(a, w), w >= kPreBetaW ? 0.0f : 1.0f, lane, 0, width),
+                                     lane, 0, width);
         },
-        [&](float(&v)[2]) { row_sums<32>(v, nullptr, turn); }, [](int64_t) {});
+        [&](int64_t r, int) { return gate_group<kPack, 32, B>(a, r, lane, 0, 0, width); },
+        [&](auto& v) { row_sums<32>(v, nullptr, turn); }, [] {});
 }
 
 // Wider rows: a CTA of NT threads a part, or a cluster of split.ctas, each of
 // which takes NT 8 columns; rows through a ring, weights (and a gate that all
 // rows share) kept in shared memory behind it. A cluster adds its CTAs' sums in
 // order of rank: each sends its own to all, counted on a barrier.
-template <typename B, typename S, int NT, bool kPack, bool kBeta>
-__global__ void __launch_bounds__(NT + 32, 512 / NT)
+//
+// The ring here has no warp of its own, which would take registers from all:
+// the barrier in a row's reduction says that all have read the row before, and
+// then thread 0 sends for the row that goes in its place. The ends of rows
+// that do not start on 16-byte boundaries are read by the first 64 threads, a
+// two-byte piece each, at the start of a row and written at its end.
+template <typename B, typename S, int NT, bool kPack, int MODE>
+__global__ void __launch_bounds__(NT, kBackwardPerSM<NT>)
     sat_block_norm_backward_ring_kernel(const __grid_constant__ rowop_block_norm_args a,
                                         const __grid_constant__ rowop_block_norm_grads g, const Split split, int stages,
                                         int stage_bytes)
 {
     extern __shared__ __align__(128) unsigned char ring_memory[];
-    __shared__ __align__(8) Ring ring;
-    __shared__ __align__(8) uint64_t arrived[2];
-    __shared__ __align__(8) float2 across[2][kMaxCluster];
-    __shared__ float scratch[2 * 2 * (NT / 32)];
+    __shared__ __align__(8) uint64_t full[kMaxStages], arrived[2];
+    __shared__ __align__(8) float across[2][kMaxCluster][8];
+    __shared__ float scratch[2 * 8 * (NT / 32)];
+    constexpr bool kBeta = MODE != kRms;
+    constexpr int room = NT * 8;
     const int ctas = split.ctas, rank = blockIdx.x % ctas, lane = threadIdx.x;
     const int64_t part = blockIdx.x / ctas;
-    const int off = rank * NT * 8, width = min(max(0, static_cast<int>(a.width) - off), NT * 8);
+    const int off = rank * room, width = min(max(0, static_cast<int>(a.width) - off), room);
     auto source = [&](const void* p, int64_t ld, int bytes, int offset) {
         return Source{p ? static_cast<const char*>(p) + static_cast<int64_t>(off) * bytes : nullptr, ld * bytes, width * bytes, offset};
     };
     const bool pre = a.pre_norm != ROWOP_NORM_NONE;
-    const int share = static_cast<int>(min(a.width, static_cast<int64_t>(NT * 8)));
+    const int share = static_cast<int>(min(a.width, static_cast<int64_t>(room)));
     const int s_bytes = (share * static_cast<int>(sizeof(S)) + 31) / 16 * 16, b_bytes = (share * static_cast<int>(sizeof(B)) + 31) / 16 * 16;
     const Source sources[kInputs] = {source(g.dh, g.lddh, sizeof(S), 0), source(pre ? g.dz : nullptr, g.lddz, sizeof(B), 2 * s_bytes),
                                      source(pre ? a.h : nullptr, a.ldh, sizeof(S), s_bytes),
                                      source(a.y, a.ldy, sizeof(B), 2 * s_bytes + b_bytes)};
-    constexpr int kept = kBeta ? kWeights : kPostBetaW;
+    // Kept: gamma before, gamma after, the gate and (Layer) the beta after.
     float* weights = reinterpret_cast<float*>(ring_memory + stages * stage_bytes);
     const bool shared_gate = !a.gate || a.rows_per_gate >= a.rows;
-    for (int w = 0; w < kept; ++w)
-        for (int c = threadIdx.x; c < width; c += NT + 32) {
-            const float* v = weight_vector(a, w);
-            float x = v ? v[off + c] : w == kPostBetaW ? 0.0f : 1.0f;
-            if (w == kGateW && a.gate && shared_gate)
-                x = a.gate_type == GEMM_C_F32 ? static_cast<const float*>(a.gate)[off + c] : to_f32(static_cast<const B*>(a.gate)[off + c]);
-            weights[w * NT * 8 + c] = x;
-        }
-    for (int w = 0; w < kept; ++w)  // past the row's end: finite
-        for (int c = width + threadIdx.x; c < NT * 8; c += NT + 32)
-            weights[w * NT * 8 + c] = 0.0f;
+    auto vector_of = [&](int w) { return weight_vector(a, w) ? weight_vector(a, w) + off : nullptr; };
+    keep_weights(weights, vector_of(kPreGammaW), 1.0f, width, room);
+    keep_weights(weights + room, vector_of(kPostGammaW), 1.0f, width, room);
+    if (a.gate && shared_gate && a.gate_type != GEMM_C_F32)
+        for (int c = threadIdx.x; c < room; c += NT)
+            weights[2 * room + c] = c < width ? to_f32(static_cast<const B*>(a.gate)[off + c]) : 0.0f;
+    else
+        keep_weights(weights + 2 * room, a.gate && shared_gate ? static_cast<const float*>(a.gate) + off : nullptr, 1.0f, width, room);
+    if (kBeta)
+        keep_weights(weights + 3 * room, vector_of(kPostBetaW), 0.0f, width, room);
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&arrived[0]), 1);
         mbar_init(smem_u32(&arrived[1]), 1);
-        ring.init(stages, NT / 32);
+        for (int s = 0; s < stages; ++s)
+            mbar_init(smem_u32(&full[s]), kPack ? 1 : 3);
+        fence_mbar_init();
     }
     __syncthreads();
     if (ctas > 1)
         cluster_sync();  // all have started and have their barriers
-    bool failed = false;
-    int s = 0, round = 0, turn = 0, swaps = 0;
-    auto next = [&] {
-        if (++s == stages)
-            s = 0, ++round;
+
+    int64_t first, end;
+    split.range(part, a.rows, first, end);
+    // Thread 0: row r's bulk copies into stage s.
+    auto send = [&](int64_t r, int s) {
+        unsigned char* stage = ring_memory + s * stage_bytes;
+        uint32_t total = 0;
+#pragma unroll
+        for (int i = 0; i < kInputs; ++i) {
+            const uint64_t lo = sources[i].row(r), hi = lo + sources[i].bytes, lo16 = (lo + 15) & ~15ull, hi16 = hi & ~15ull;
+            if (!sources[i].p || hi16 <= lo16)
+                continue;
+            const uint32_t bytes = static_cast<uint32_t>(hi16 - lo16);
+            total += bytes;
+            bulk_load(smem_u32(stage) + sources[i].offset + static_cast<uint32_t>(lo16 - (lo & ~15ull)), lo16, bytes, smem_u32(&full[s]));
+        }
+        mbar_arrive_expect_tx(smem_u32(&full[s]), total);
     };
-    if (threadIdx.x >= NT) {
-        int64_t first, end;
-        split.range(part, a.rows, first, end);
-        for (int64_t r = first; r < end; ++r, next())
-            ring.fill<kPack>(ring_memory + s * stage_bytes, s, round, sources, r, failed);
-        return;
+    // Threads 0 .. 63: this thread's piece of row r's ends: its address (0 for none) and its place in a stage.
+    const int input = lane / 16 % kInputs, piece = lane % 16;
+    const Source mine = input == kDh ? sources[kDh] : input == kDz ? sources[kDz] : input == kH ? sources[kH] : sources[kY];
+    auto end_of = [&](int64_t r, int& place) -> uint64_t {
+        const uint64_t lo = mine.row(r), hi = lo + mine.bytes, lo16 = (lo + 15) & ~15ull, hi16 = hi & ~15ull;
+        const uint64_t x = (piece < 8 ? lo & ~15ull : hi16) + piece % 8 * 2;
+        place = mine.offset + static_cast<int>(x - (lo & ~15ull));
+        return mine.p && x >= lo && x < hi && (x < lo16 || x >= hi16) && (piece < 8 || hi16 >= lo16) ? x : 0;
+    };
+    auto put_end = [&](int s, int place, uint64_t x, uint16_t v) {
+        if (x)
+            *reinterpret_cast<uint16_t*>(ring_memory + s * stage_bytes + place) = v;
+        __syncwarp();
+        if (lane % 32 == 0)
+            mbar_arrive(smem_u32(&full[s]));
+    };
+    for (int s = 0; s < stages && first + s < end; ++s) {
+        if (threadIdx.x == 0)
+            send(first + s, s);
+        if (!kPack && threadIdx.x < 64) {
+            int place;
+            const uint64_t x = end_of(first + s, place);
+            put_end(s, place, x, x ? *reinterpret_cast<const uint16_t*>(x) : 0);
+        }
     }
-    bool taken = false;
-    backward_rows<B, S, NT, kPack, kBeta>(
+
+    bool failed = false, taken = false;
+    int s = 0, round = 0, turn = 0, swaps = 0, place = 0;
+    uint64_t x = 0;
+    uint16_t held = 0;
+    int64_t now = first;  // the row at hand
+    backward_rows<B, S, NT, 1, kPack, MODE>(
         a, g, split, part, lane, off, width,
-        [&](float(&v)[8], int input, int64_t r) {
-            if (!taken)
-                ring.take(s, round, failed);
-            taken = true;
-            const unsigned char* stage = ring_memory + s * stage_bytes;
-            if (input == kDz || input == kY)
-                stage_group<kPack, NT, B>(v, stage, sources[input], r, lane, 0, width);
-            else if (sources[input].p)
-                stage_group<kPack, NT, S>(v, stage, sources[input], r, lane, 0, width);
-            else
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] = 0.0f;
-            if (failed)
-                v[0] = NAN;
-        },
-        [&](float(&v)[8], int w, int64_t r) {
-            if (w == kGateW && !shared_gate) {
-                gate_group<kPack, NT, B>(v, a, r, lane, off, width);
-            } else if constexpr (kPack) {
-                const float4* at = reinterpret_cast<const float4*>(weights + w * NT * 8) + 2 * lane;
-                const float4 x = at[0], y = at[1];
-                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] = weights[w * NT * 8 + e * NT + lane];
+        [&](int in, int64_t r, int) {
+            if (!taken) {
+                // The row that will take the place of the one before.
+                const int64_t ahead = r - 1 + stages;
+                if (!kPack && threadIdx.x < 64 && r > first && ahead < end) {
+                    x = end_of(ahead, place);
+                    held = x ? *reinterpret_cast<const uint16_t*>(x) : 0;
+                }
+                Ring::wait(&full[s], round & 1, failed);
+                taken = true;
             }
+            const unsigned char* stage = ring_memory + s * stage_bytes;
+            return in == kDz || in == kY ? stage_group<kPack, NT, B>(stage, sources[in], r, lane, 0, width)
+                   : sources[in].p       ? stage_group<kPack, NT, S>(stage, sources[in], r, lane, 0, width)
+                                         : fill(0.0f);
         },
-        [&](float(&v)[2]) {
+        [&](int w, int) { return kept_group<kPack, NT>(weights + (w == kPreGammaW ? 0 : w == kPostGammaW ? 1 : 3) * room, lane, 0); },
+        [&](int64_t r, int) {
+            return shared_gate ? kept_group<kPack, NT>(weights + 2 * room, lane, 0) : gate_group<kPack, NT, B>(a, r, lane, 0, off, width);
+        },
+        [&](auto& v) {
+            constexpr int K = sizeof(v) / sizeof(v[0]);
+            if (!kPack && threadIdx.x < 64)
+                fence_proxy_async_smem();  // of the ends written before: what follows them there comes by bulk copies
             ring_sums<NT>(v, scratch, turn);
+            const int before = s == 0 ? stages - 1 : s - 1;
+            if (now > first && now - 1 + stages < end) {
+                if (threadIdx.x == 0)
+                    send(now - 1 + stages, before);
+                if (!kPack && threadIdx.x < 64)
+                    put_end(before, place, x, held);
+            }
             if (ctas > 1) {
                 const int b = swaps & 1;
                 if (threadIdx.x == 0)
-                    mbar_arrive_expect_tx(smem_u32(&arrived[b]), ctas * 8);
-                if (threadIdx.x < ctas)
-                    send_b64(map_to_cta(smem_u32(&across[b][rank]), threadIdx.x), pair(v[0], v[1]),
-                             map_to_cta(smem_u32(&arrived[b]), threadIdx.x));
+                    mbar_arrive_expect_tx(smem_u32(&arrived[b]), ctas * ((K + 1) / 2) * 8);
+                if (threadIdx.x < ctas) {
+                    const uint32_t bar = map_to_cta(smem_u32(&arrived[b]), threadIdx.x);
+                    const uint32_t to = map_to_cta(smem_u32(&across[b][rank][0]), threadIdx.x);
+#pragma unroll
+                    for (int k = 0; k < K; k += 2)
+                        send_b64(to + 4 * k, pair(v[k], k + 1 < K ? v[k + 1] : 0.0f), bar);
+                }
                 Ring::wait(&arrived[b], swaps >> 1 & 1, failed);
                 ++swaps;
-                v[0] = failed ? NAN : 0.0f, v[1] = 0.0f;
-                for (int c = 0; c < ctas; ++c)
-                    v[0] += across[b][c].x, v[1] += across[b][c].y;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    v[k] = 0.0f;
+                    for (int c = 0; c < ctas; ++c)
+                        v[k] += across[b][c][k];
+                }
             }
+            if (failed)
+                v[0] = NAN;
         },
-        [&](int64_t) {
-            ring.release(s);
-            next();
+        [&] {
             taken = false;
+            ++now;
+            if (++s == stages)
+                s = 0, ++round;
         });
 }
 
-template <typename B, typename S, int NT, bool kPack, bool kBeta>
+template <typename B, typename S, int NT, bool kPack, int MODE>
 cudaError_t launch_backward(const rowop_block_norm_args& a, const rowop_block_norm_grads& g, const Split& split,
                             cudaStream_t s)
 {
     const int64_t share = a.width < NT * 8 ? a.width : NT * 8;
     const int stage = static_cast<int>(2 * ((share * sizeof(S) + 31) / 16 * 16) + 2 * ((share * sizeof(B) + 31) / 16 * 16));
-    constexpr int room = kSmemPerSM / (512 / NT) - 2048, kept = (kBeta ? kWeights : kPostBetaW) * NT * 8 * 4;
+    constexpr int room = kSmemPerSM / kBackwardPerSM<NT> - 3072, kept = (MODE == kRms ? 3 : 4) * NT * 8 * 4;
     int stages = (room - kept) / stage;
     stages = stages < kMaxStages ? stages : kMaxStages;
-    auto kernel = sat_block_norm_backward_ring_kernel<B, S, NT, kPack, kBeta>;
+    if (stages < 2)
+        return cudaErrorInvalidConfiguration;
+    auto kernel = sat_block_norm_backward_ring_kernel<B, S, NT, kPack, MODE>;
     static Prepared prepared;
     const cudaError_t e = prepared.once(reinterpret_cast<const void*>(kernel), room);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(split.parts * split.ctas));
-    cfg.blockDim = dim3(NT + 32);
+    cfg.blockDim = dim3(NT);
     cfg.dynamicSmemBytes = stages * stage + kept;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -804,18 +1079,18 @@ cudaError_t launch_backward(const rowop_block_norm_args& a, const rowop_block_no
     return cudaLaunchKernelEx(&cfg, kernel, a, g, split, stages, stage);
 }
 
-template <typename B, typename S, bool kPack, bool kBeta>
+template <typename B, typename S, bool kPack, int MODE>
 cudaError_t choose_backward(const rowop_block_norm_args& a, const rowop_block_norm_grads& g, const Split& split,
                             cudaStream_t s)
 {
-    switch (backward_threads(a.width)) {
+    switch (split.threads) {
     case 32:
-        sat_block_norm_backward_kernel<B, S, kPack, kBeta>
+        sat_block_norm_backward_kernel<B, S, kPack, MODE>
             <<<static_cast<unsigned>((split.parts + 3) / 4), 128, 0, s>>>(a, g, split);
         return cudaGetLastError();
-    case 128: return launch_backward<B, S, 128, kPack, kBeta>(a, g, split, s);
-    case 256: return launch_backward<B, S, 256, kPack, kBeta>(a, g, split, s);
-    default: return launch_backward<B, S, 512, kPack, kBeta>(a, g, split, s);
+    case 128: return launch_backward<B, S, 128, kPack, MODE>(a, g, split, s);
+    case 256: return launch_backward<B, S, 256, kPack, MODE>(a, g, split, s);
+    default: return launch_backward<B, S, 512, kPack, MODE>(a, g, split, s);
     }
 }
 
@@ -834,9 +1109,13 @@ template <typename B, typename S>
 cudaError_t backward_as(const rowop_block_norm_args& a, const rowop_block_norm_grads& g, const Split& split, bool pack,
                         cudaStream_t s)
 {
-    if (split.sums == kSums)
-        return pack ? choose_backward<B, S, true, true>(a, g, split, s) : choose_backward<B, S, false, true>(a, g, split, s);
-    return pack ? choose_backward<B, S, true, false>(a, g, split, s) : choose_backward<B, S, false, false>(a, g, split, s);
+    switch (split.mode) {
+    case kRms: return pack ? choose_backward<B, S, true, kRms>(a, g, split, s) : choose_backward<B, S, false, kRms>(a, g, split, s);
+    case kLayerShared:
+        return pack ? choose_backward<B, S, true, kLayerShared>(a, g, split, s) : choose_backward<B, S, false, kLayerShared>(a, g, split, s);
+    default:
+        return pack ? choose_backward<B, S, true, kLayerGrouped>(a, g, split, s) : choose_backward<B, S, false, kLayerGrouped>(a, g, split, s);
+    }
 }
 
 template <typename B>

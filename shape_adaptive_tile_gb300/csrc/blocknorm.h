@@ -21,7 +21,7 @@ constexpr int kMaxCluster = 4;  // CTAs that share a row in the backward pass
 // equal pieces of one group.
 struct Split {
     int64_t parts, groups, pieces, group_rows, stride;
-    int32_t sums, ctas, direct;
+    int32_t sums, ctas, direct, threads, mode;
 
     __host__ __device__ void range(int64_t part, int64_t rows, int64_t& first, int64_t& end) const
     {
@@ -42,8 +42,15 @@ struct Split {
 // each. Without a Layer norm there are none for betas (sums = kPreBeta).
 enum Sum { kPreGamma, kPostGamma, kGate, kPreBeta, kPostBeta, kSums };
 
-// Threads that hold a row of the backward pass, eight columns each.
-inline int backward_threads(int64_t width) { return width <= 256 ? 32 : width <= 1024 ? 128 : width <= 2048 ? 256 : 512; }
+// What the backward pass's kernels are compiled for: no Layer norm, or one,
+// with a gate that all rows share (or none) or one that changes from row to row.
+enum Mode { kRms, kLayerShared, kLayerGrouped };
+
+// CTAs an SM that the backward pass is made for, by their threads: eight
+// columns a thread, a warp for rows of up to 256 columns, a cluster for those
+// of over 4096.
+template <int NT>
+constexpr int kBackwardPerSM = 512 / NT;
 
 // Kernels of one block type (blocknorm_<type>.cu). `pack`: all rows start on boundaries of eight elements.
 cudaError_t forward_f32(const rowop_block_norm_args& a, bool pack, cudaStream_t s);

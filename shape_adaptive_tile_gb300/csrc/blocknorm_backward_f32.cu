@@ -1,0 +1,13 @@
+// Block norm, backward kernels for blocks in f32.
+#include "blocknorm.cuh"
+
+namespace sat {
+namespace blocknorm {
+
+cudaError_t backward_f32(const rowop_block_norm_args& a, const rowop_block_norm_grads& g, const Split& split, bool pack, cudaStream_t s)
+{
+    return backward<float>(a, g, split, pack, s);
+}
+
+}  // namespace blocknorm
+}  // namespace sat
