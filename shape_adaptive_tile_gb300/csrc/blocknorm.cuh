@@ -147,28 +147,39 @@ __device__ __forceinline__ Group kept_group(const float* w, int lane, int i)
     }
 }
 
+// Puts the thread's first group there.
+template <bool kPack, int NT>
+__device__ __forceinline__ void keep_group(float* w, const Group& g, int lane)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 f = halves(g.p[e]);
+        w[column<kPack, NT>(lane, 0, 2 * e)] = f.x;
+        w[column<kPack, NT>(lane, 0, 2 * e + 1)] = f.y;
+    }
+}
+
 __device__ __forceinline__ float sum_of(uint64_t v)
 {
     const float2 f = halves(v);
     return f.x + f.y;
 }
 
-__device__ __forceinline__ const void* gate_row(const rowop_block_norm_args& a, int64_t r, int bytes)
+// The gate row of row r, by a 32-bit division (there are fewer than 2^31 rows).
+__device__ __forceinline__ int64_t gate_row(const rowop_block_norm_args& a, int64_t r)
 {
-    return a.gate ? static_cast<const char*>(a.gate) + (a.rows_per_gate >= a.rows ? 0 : r / a.rows_per_gate) * a.ldg * bytes
-                  : nullptr;
+    return a.rows_per_gate >= a.rows ? 0 : static_cast<uint32_t>(r) / static_cast<uint32_t>(a.rows_per_gate);
 }
 
-// The thread's group i of row r's gate, in the gate's type: the block's or
-// fp32 (a branch that all threads take alike). `off`: the first column.
+// The thread's group i of gate row k, in the gate's type: the block's or fp32
+// (a branch that all threads take alike). `off`: the first column.
 template <bool kPack, int NT, typename B>
-__device__ __forceinline__ Group gate_group(const rowop_block_norm_args& a, int64_t r, int lane, int i, int off, int width)
+__device__ __forceinline__ Group gate_group(const rowop_block_norm_args& a, int64_t k, int lane, int i, int off, int width)
 {
     const int bytes = a.gate_type == GEMM_C_F32 ? 4 : sizeof(B);
-    const char* gate = static_cast<const char*>(gate_row(a, r, bytes));
-    if (!gate)
+    if (!a.gate)
         return fill(1.0f);
-    gate += static_cast<int64_t>(off) * bytes;
+    const char* gate = static_cast<const char*>(a.gate) + (k * a.ldg + off) * bytes;
     if (bytes == 4)
         return load_group<kPack, NT>(reinterpret_cast<const float*>(gate), lane, i, width);
     return load_group<kPack, NT>(reinterpret_cast<const B*>(gate), lane, i, width);
@@ -187,6 +198,11 @@ struct Source {
     int offset;       // where it lies in a stage
 
     __device__ __forceinline__ uint64_t row(int64_t r) const { return reinterpret_cast<uint64_t>(p + r * pitch); }
+    // How many bytes after a 16-byte boundary it begins.
+    __device__ __forceinline__ uint32_t begins(int64_t r) const
+    {
+        return (static_cast<uint32_t>(reinterpret_cast<uint64_t>(p)) + static_cast<uint32_t>(r) * static_cast<uint32_t>(pitch)) & 15;
+    }
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, uint64_t src, uint32_t bytes, uint32_t bar)
@@ -300,7 +316,7 @@ __device__ __forceinline__ Group stage_group(const unsigned char* stage, const S
             return group_of(Pack<T>{{x.x, x.y, x.z, x.w}});
         }
     } else {
-        const T* at = reinterpret_cast<const T*>(stage + source.offset + (source.row(r) & 15));
+        const T* at = reinterpret_cast<const T*>(stage + source.offset + source.begins(r));
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -311,33 +327,50 @@ __device__ __forceinline__ Group stage_group(const unsigned char* stage, const S
     }
 }
 
-// Sums of N values over the NT threads that come before the filling warp, as
-// row_sums, behind a barrier of theirs alone.
+// Sums of N values (a power of two, at most 8) over NT threads of a CTA (the
+// `group`-th NT), to each of them, in a fixed order, behind a barrier of theirs.
+// Lanes halve the values that they hold while they double the lanes that
+// those are of, so that eight sums take nine exchanges and not forty.
+// `scratch`: 2 x N x NT / 32 floats; its halves take turns, so one barrier
+// does: a half is written again two reductions later.
 template <int NT, int N>
-__device__ __forceinline__ void ring_sums(float (&v)[N], float* scratch, int& turn)
+__device__ __forceinline__ void ring_sums(float (&v)[N], float* scratch, int& turn, int group)
 {
     constexpr int W = NT / 32;
+    static_assert((N & (N - 1)) == 0 && N <= 8 && W * N >= 4, "");
+    const int warp = (threadIdx.x >> 5) % W, lane = threadIdx.x & 31;
+    int n = N, bit = 16;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (; n > 1; n /= 2, bit /= 2) {
+        const bool upper = lane & bit;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        for (int i = 0; i < n / 2; ++i) {
+            const float give = upper ? v[i] : v[i + n / 2], keep = upper ? v[i + n / 2] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
+        }
+    }
+#pragma unroll
+    for (; bit > 0; bit /= 2)
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+    // Lanes l with the same l / (32 / N) hold the sum whose number is that.
     float* half = scratch + turn * (N * W);
     turn ^= 1;
-    if (lane == 0)
+    if (lane % (32 / N) == 0)
+        half[warp * N + lane / (32 / N)] = v[0];
+    named_bar_sync(1 + group, NT);
+    // Lane l: sum l % N of warps l / N, l / N + 32 / N, ...
+    constexpr int each = 32 / N;  // warps that the lanes read at once
+    float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            half[i * W + warp] = v[i];
-    named_bar_sync(1, NT);
+    for (int w = 0; w < W; w += each)
+        if (w + lane / N < W)
+            s += half[(w + lane / N) * N + lane % N];
+#pragma unroll
+    for (int o = 16; o >= N; o /= 2)
+        s += __shfl_xor_sync(0xffffffffu, s, o);
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        v[i] = half[i * W + lane % W];
-#pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        v[i] = __shfl_sync(0xffffffffu, s, i);
 }
 
 // ---- forward -----------------------------------------------------------------------
@@ -487,7 +520,7 @@ __global__ void __launch_bounds__(NT == 32 ? 128 : NT) sat_block_norm_kernel(con
         constexpr bool kEarly = NV == 1;
         Group early[kEarly ? kWeights : 1];
         auto read = [&](int w, int i) {
-            return w == kGateW ? gate_group<kPack, NT, B>(a, r, lane, i, 0, width)
+            return w == kGateW ? gate_group<kPack, NT, B>(a, gate_row(a, r), lane, i, 0, width)
                                : load_weights<kPack, NT>(weight_vector(a, w), w >= kPreBetaW ? 0.0f : 1.0f, lane, i, width);
         };
         if constexpr (kEarly) {
@@ -507,19 +540,18 @@ __global__ void __launch_bounds__(NT == 32 ? 128 : NT) sat_block_norm_kernel(con
     }
 }
 
-// CTAs an SM that the ring's forward kernel is made for: a wide row's threads fill it.
-template <int NT>
-constexpr int kForwardPerSM = NT == 512 ? 1 : NT == 256 ? 2 : 4;
-
-// Many rows: a CTA's NT threads take every gridDim.x-th, through a ring of
-// `stages` stages of `stage_bytes`. `kept`: the weights lie behind the ring.
+// Many rows: a CTA of 512 threads an SM, in groups of NT that each take a row
+// at a time and share a ring of `stages` stages of `stage_bytes` and, behind it
+// (`kept`), the weights. So several rows are at hand in an SM at once, one
+// group's reductions beside another's arithmetic, with one copy of the weights.
 template <typename B, typename S, int NT, int NV, bool kPack, bool kLayer>
-__global__ void __launch_bounds__(NT + 32, kForwardPerSM<NT>)
+__global__ void __launch_bounds__(512 + 32, 1)
     sat_block_norm_ring_kernel(const __grid_constant__ rowop_block_norm_args a, int stages, int stage_bytes, bool kept)
 {
+    constexpr int G = 512 / NT;
     extern __shared__ __align__(128) unsigned char ring_memory[];
     __shared__ __align__(8) Ring ring;
-    __shared__ float scratch[2 * (NT / 32)];
+    __shared__ float scratch[G][2 * (NT / 32)];
     const int width = static_cast<int>(a.width);
     const int y_bytes = (width * static_cast<int>(sizeof(B)) + 31) / 16 * 16;
     const Source sources[2] = {
@@ -529,28 +561,25 @@ __global__ void __launch_bounds__(NT + 32, kForwardPerSM<NT>)
     float* weights = reinterpret_cast<float*>(ring_memory + stages * stage_bytes);
     const bool shared_gate = a.gate && a.rows_per_gate >= a.rows;
     // Kept weights lie one after another in the order of Weight, those that the call does not have left out.
-    auto place = [&](int w) {
-        int at = 0;
-        for (int v = 0; v < w; ++v)
-            at += v == kGateW ? shared_gate : weight_vector(a, v) != nullptr;
-        return weights + at * room;
-    };
-    if (kept)
-        for (int w = 0; w < kWeights; ++w) {
-            if (w != kGateW && weight_vector(a, w))
-                keep_weights(place(w), weight_vector(a, w), 1.0f, width, room);
-            if (w == kGateW && shared_gate)
-                for (int c = threadIdx.x; c < room; c += blockDim.x)
-                    place(w)[c] = c >= width ? 0.0f
-                                  : a.gate_type == GEMM_C_F32 ? static_cast<const float*>(a.gate)[c]
-                                                              : to_f32(static_cast<const B*>(a.gate)[c]);
-        }
+    const float* at[kWeights];
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < kWeights; ++w) {
+        const bool there = kept && (w == kGateW ? shared_gate : weight_vector(a, w) != nullptr);
+        at[w] = there ? weights + n * room : nullptr;
+        if (there && w == kGateW && a.gate_type != GEMM_C_F32)
+            for (int c = threadIdx.x; c < room; c += blockDim.x)
+                weights[n * room + c] = c < width ? to_f32(static_cast<const B*>(a.gate)[c]) : 0.0f;
+        else if (there)
+            keep_weights(weights + n * room, w == kGateW ? static_cast<const float*>(a.gate) : weight_vector(a, w), 1.0f, width, room);
+        n += there;
+    }
     if (threadIdx.x == 0)
         ring.init(stages, NT / 32);
     __syncthreads();
     bool failed = false;
     int s = 0, round = 0, turn = 0;
-    if (threadIdx.x >= NT) {
+    if (threadIdx.x >= 512) {
         for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
             ring.fill<kPack>(ring_memory + s * stage_bytes, s, round, sources, r, failed);
             if (++s == stages)
@@ -558,18 +587,19 @@ __global__ void __launch_bounds__(NT + 32, kForwardPerSM<NT>)
         }
         return;
     }
-    const int lane = threadIdx.x;
-    const float* at[kWeights];
-#pragma unroll
-    for (int w = 0; w < kWeights; ++w)
-        at[w] = kept && (w == kGateW ? shared_gate : weight_vector(a, w) != nullptr) ? place(w) : nullptr;
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const int group = threadIdx.x / NT, lane = threadIdx.x % NT;
+    s = group;
+    for (int64_t r = blockIdx.x + group * static_cast<int64_t>(gridDim.x); r < a.rows; r += G * static_cast<int64_t>(gridDim.x), s += G) {
+        for (; s >= stages; s -= stages)
+            ++round;
         ring.take(s, round, failed);
         const unsigned char* stage = ring_memory + s * stage_bytes;
         Group v[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            v[i] = failed ? fill(NAN) : stage_group<kPack, NT, B>(stage, sources[0], r, lane, i, width);
+            v[i] = stage_group<kPack, NT, B>(stage, sources[0], r, lane, i, width);
+        if (failed)
+            v[0] = fill(NAN);
         finish_row<B, S, NT, NV, kPack, kLayer>(
             a, r, v, lane,
             [&](int i) {
@@ -582,12 +612,10 @@ __global__ void __launch_bounds__(NT + 32, kForwardPerSM<NT>)
                 if (at[w])
                     return kept_group<kPack, NT>(at[w], lane, i);
                 if (w == kGateW)
-                    return gate_group<kPack, NT, B>(a, r, lane, i, 0, width);
+                    return gate_group<kPack, NT, B>(a, gate_row(a, r), lane, i, 0, width);
                 return load_weights<kPack, NT>(weight_vector(a, w), w >= kPreBetaW ? 0.0f : 1.0f, lane, i, width);
             },
-            [&](float(&v)[1]) { ring_sums<NT>(v, scratch, turn); });
-        if (++s == stages)
-            s = 0, ++round;
+            [&](float(&v)[1]) { ring_sums<NT>(v, scratch[group], turn, group); });
     }
 }
 
@@ -603,45 +631,44 @@ cudaError_t launch_forward(const rowop_block_norm_args& a, cudaStream_t s)
 template <typename B, typename S, int NT, int NV, bool kPack, bool kLayer>
 cudaError_t launch_ring(const rowop_block_norm_args& a, cudaStream_t s)
 {
-    constexpr int per_sm = kForwardPerSM<NT>;
-    if (a.rows < 2 * per_sm * kSMs)  // under two rows a CTA there is nothing to fetch ahead
-        return launch_forward<B, S, NT, NV, kPack, kLayer>(a, s);
     const int64_t w = a.width;
     const int stage = static_cast<int>((w * sizeof(B) + 31) / 16 * 16 + (w * sizeof(S) + 31) / 16 * 16);
-    constexpr int room = kSmemPerSM / per_sm - 2048;
+    constexpr int room = kSmemPerSM - 2048, groups = 512 / NT;
     const bool post = a.post_norm != ROWOP_NORM_NONE, pre = a.pre_norm != ROWOP_NORM_NONE;
     int weights = (post && a.post_gamma) + (pre && a.pre_gamma) + (a.gate && a.rows_per_gate >= a.rows) +
                   (a.post_norm == ROWOP_NORM_LAYER && a.post_beta) + (a.pre_norm == ROWOP_NORM_LAYER && a.pre_beta);
     weights *= NT * NV * 8 * 4;
-    // Weights stay on chip where two rows fit beside them.
-    const bool kept = room - weights >= 2 * stage;
+    // Weights stay on chip where a row for every group and one more fit beside them.
+    const bool kept = room - weights >= (groups + 1) * stage;
     int stages = (kept ? room - weights : room) / stage;
     stages = stages < kMaxStages ? stages : kMaxStages;
-    if (stages < 2)
-        return launch_forward<B, S, NT, NV, kPack, kLayer>(a, s);
     auto kernel = sat_block_norm_ring_kernel<B, S, NT, NV, kPack, kLayer>;
     static Prepared prepared;
     const cudaError_t e = prepared.once(reinterpret_cast<const void*>(kernel), room);
     if (e != cudaSuccess)
         return e;
-    kernel<<<static_cast<unsigned>(per_sm * kSMs), NT + 32, stages * stage + (kept ? weights : 0), s>>>(a, stages, stage, kept);
+    if (stages < 1)
+        return cudaErrorInvalidConfiguration;
+    kernel<<<static_cast<unsigned>(kSMs), 512 + 32, stages * stage + (kept ? weights : 0), s>>>(a, stages, stage, kept);
     return cudaGetLastError();
 }
 
 template <typename B, typename S, bool kPack, bool kLayer>
 cudaError_t choose_forward_as(const rowop_block_norm_args& a, cudaStream_t s)
 {
-    // Four groups a thread, so that a row's fixed work (the reductions, its
-    // addresses) is spread over 32 columns; few rows take more threads each.
+    // Up to four rows an SM there is little to fetch ahead: a CTA a row, as many threads as it has groups.
+    const bool few = a.rows < 4 * kSMs;
     if (a.width <= 256)
         return launch_forward<B, S, 32, 1, kPack, kLayer>(a, s);
     if (a.width <= 1024)
-        return a.rows < 4 * kSMs ? launch_forward<B, S, 128, 1, kPack, kLayer>(a, s) : launch_forward<B, S, 32, 4, kPack, kLayer>(a, s);
+        return few ? launch_forward<B, S, 128, 1, kPack, kLayer>(a, s) : launch_forward<B, S, 32, 4, kPack, kLayer>(a, s);
+    // Else four groups of columns a thread, so that a row's fixed work (the
+    // reductions, its addresses) is spread over 32 of them.
     if (a.width <= 4096)
-        return a.rows < 4 * kSMs ? launch_forward<B, S, 512, 1, kPack, kLayer>(a, s) : launch_ring<B, S, 128, 4, kPack, kLayer>(a, s);
+        return few ? launch_forward<B, S, 512, 1, kPack, kLayer>(a, s) : launch_ring<B, S, 128, 4, kPack, kLayer>(a, s);
     if (a.width <= 8192)
-        return launch_ring<B, S, 256, 4, kPack, kLayer>(a, s);
-    return launch_ring<B, S, 512, 4, kPack, kLayer>(a, s);
+        return few ? launch_forward<B, S, 512, 2, kPack, kLayer>(a, s) : launch_ring<B, S, 256, 4, kPack, kLayer>(a, s);
+    return few ? launch_forward<B, S, 512, 4, kPack, kLayer>(a, s) : launch_ring<B, S, 512, 4, kPack, kLayer>(a, s);
 }
 
 template <typename B, typename S, bool kPack>
@@ -668,30 +695,38 @@ enum Input { kDh, kDz, kH, kY, kInputs };
 // weights of 0 and gradients of 0.
 //
 // `at(input, r)` gives the thread's group of a matrix, `weight(w)` of a weight
-// and `gate(r)` of the gate, `sums` adds over the row once its inputs have been
-// read, `done()` ends it. `off` is the first of the CTA's columns, `width`
+// and `gate()` of the gate, whose row `change_gate(k)` makes the k-th; `sums`
+// adds over the row once its inputs have been read, `done()` ends it. `off` is the first of the CTA's columns, `width`
 // their number.
 template <typename B, typename S, int NT, int NV, bool kPack, int MODE, typename At, typename WeightAt, typename GateAt,
-          typename Sums, typename Done>
+          typename ChangeGate, typename Sums, typename Done>
 __device__ __forceinline__ void backward_rows(const rowop_block_norm_args& a, const rowop_block_norm_grads& g, const Split& split,
                                               int64_t part, int lane, int off, int width, At at, WeightAt weight, GateAt gate,
-                                              Sums sums, Done done)
+                                              ChangeGate change_gate, Sums sums, Done done)
 {
     constexpr bool kBeta = MODE != kRms, kGrouped = MODE == kLayerGrouped;
     const float inv = 1.0f / static_cast<float>(a.width);
     const bool pre = a.pre_norm != ROWOP_NORM_NONE, post = a.post_norm != ROWOP_NORM_NONE;
     const bool pre_layer = a.pre_norm == ROWOP_NORM_LAYER, post_layer = a.post_norm == ROWOP_NORM_LAYER;
-    // A gate that all rows share multiplies the sums at the end; one that changes, the rows.
-    const bool grouped = kGrouped || (MODE == kRms && a.gate && a.rows_per_gate < a.rows);
     const uint64_t branch = both(a.branch_scale), residual = both(a.residual_scale);
-    // Sums over rows of dz hh, D yh, gate D yh and, for betas, dz, D, gate D.
-    Group dz_hh[NV], d_yh[NV], gd_yh[NV], dz_1[NV], d_1[NV], gd_1[NV];
+    // Sums over rows of dz hh, D yh and, for betas, dz, D. A gate that all rows
+    // share multiplies these at the end; one that changes, at its last row, into
+    // sums of gate D yh and gate D: registers, or (Layer) the part's own place
+    // in the workspace, where each thread adds up its own columns.
+    const bool grouped = kGrouped || (MODE == kRms && a.gate && a.rows_per_gate < a.rows);
+    Group dz_hh[NV], d_yh[NV], gd_yh[NV], dz_1[NV], d_1[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        dz_hh[i] = d_yh[i] = gd_yh[i] = dz_1[i] = d_1[i] = gd_1[i] = fill(0.0f);
+        dz_hh[i] = d_yh[i] = gd_yh[i] = dz_1[i] = d_1[i] = fill(0.0f);
     int64_t first, end;
     split.range(part, a.rows, first, end);
-    int64_t flush = split.direct ? min((first / a.rows_per_gate + 1) * a.rows_per_gate, end) : end;
+    float* out = static_cast<float*>(g.workspace) + part * split.sums * split.stride + off;
+    auto own = [&](int sum, int i) { return load_group<kPack, NT>(out + sum * split.stride, lane, i, width); };
+    auto put = [&](int sum, int i, const Group& v) { store_group<kPack, NT>(out + sum * split.stride, v, lane, i, width); };
+    if (kGrouped)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            put(kPostGamma, i, fill(0.0f)), put(kPostBeta, i, fill(0.0f));
     // A row's statistics, read a row ahead: (mean, reciprocal deviation) before and after.
     auto stats = [&](int64_t r) {
         const int64_t i = 2 * min(r, end - 1);
@@ -707,15 +742,36 @@ __device__ __forceinline__ void backward_rows(const rowop_block_norm_args& a, co
             o.p[e] = mul2(branch, kBeta ? fma2(gamma.p[e], d_yh[i].p[e], mul2(beta.p[e], d_1[i].p[e])) : mul2(gamma.p[e], d_yh[i].p[e]));
         return o;
     };
-    float4 ahead = first < end ? stats(first) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    // The sums with the gate, of what has come since its row began.
+    auto gate_ends = [&](int i) {
+        const Group gr = gate(i);
+        if constexpr (kGrouped) {
+            Group yh = own(kPostGamma, i), one = own(kPostBeta, i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                yh.p[e] = fma2(mul2(branch, gr.p[e]), d_yh[i].p[e], yh.p[e]);
+                one.p[e] = fma2(mul2(branch, gr.p[e]), d_1[i].p[e], one.p[e]);
+            }
+            put(kPostGamma, i, yh), put(kPostBeta, i, one);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                gd_yh[i].p[e] = fma2(mul2(branch, gr.p[e]), d_yh[i].p[e], gd_yh[i].p[e]);
+        }
+    };
+    // The gate row at hand and the row after its last.
+    int64_t gate_at = grouped ? first / a.rows_per_gate : 0, gate_end = grouped ? (gate_at + 1) * a.rows_per_gate : end;
+    if (first < end)
+        change_gate(gate_at);
     S* dx = static_cast<S*>(g.dx) + first * g.lddx + off;
     B* dy = static_cast<B*>(g.dy) + first * g.lddy + off;
+    float4 ahead = first < end ? stats(first) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int64_t r = first; r < end; ++r, dx += g.lddx, dy += g.lddy) {
         const float4 st = ahead;
         ahead = stats(r + 1);
         const uint64_t pre_rs = both(st.y), rs = both(st.w);
         Group u[NV], hh[NV], yh[NV], w[NV];
-        uint64_t s[kBeta ? 8 : 3] = {};
+        uint64_t s[kBeta ? 8 : 4] = {};  // the fourth of four is not used
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             u[i] = at(kDh, r, i), yh[i] = at(kY, r, i), w[i] = weight(kPostGammaW, i), hh[i] = fill(0.0f);
@@ -736,7 +792,7 @@ __device__ __forceinline__ void backward_rows(const rowop_block_norm_args& a, co
                     u[i].p[e] = fma2(dz.p[e], pre_rs, u[i].p[e]);
                 }
             }
-            const Group gr = gate(r, i);
+            const Group gr = gate(i);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if constexpr (kBeta)
@@ -756,7 +812,7 @@ __device__ __forceinline__ void backward_rows(const rowop_block_norm_args& a, co
                 }
             }
         }
-        constexpr int K = kBeta ? 8 : 3;
+        constexpr int K = kBeta ? 8 : 4;
         float sum[K];
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -800,52 +856,43 @@ __device__ __forceinline__ void backward_rows(const rowop_block_norm_args& a, co
             }
             if (g.dy)
                 store_group<kPack, NT>(dy, o, lane, i, width);
-            if (MODE != kLayerShared && grouped) {
-                const Group gr = gate(r, i);
+        }
+        if (grouped && (r + 1 == gate_end || r + 1 == end)) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint64_t gd = mul2(gr.p[e], u[i].p[e]);
-                    gd_yh[i].p[e] = fma2(gd, yh[i].p[e], gd_yh[i].p[e]);
-                    if constexpr (kBeta)
-                        gd_1[i].p[e] = add2(gd_1[i].p[e], gd);
+            for (int i = 0; i < NV; ++i) {
+                gate_ends(i);
+                if (split.direct) {  // the part has all of the gate row's rows
+                    if (g.dgate && a.gate_type == GEMM_C_F32)
+                        store_group<kPack, NT>(static_cast<float*>(g.dgate) + gate_at * g.lddg + off, gate_grad(i), lane, i, width);
+                    else if (g.dgate)
+                        store_group<kPack, NT>(static_cast<B*>(g.dgate) + gate_at * g.lddg + off, gate_grad(i), lane, i, width);
                 }
-                if (split.direct && r + 1 == flush) {  // the gate row's last row
-                    const int64_t to = r / a.rows_per_gate * g.lddg + off;
-                    if (a.gate_type == GEMM_C_F32)
-                        store_group<kPack, NT>(static_cast<float*>(g.dgate) + to, gate_grad(i), lane, i, width);
-                    else
-                        store_group<kPack, NT>(static_cast<B*>(g.dgate) + to, gate_grad(i), lane, i, width);
+                if (r + 1 < end)  // without the gate's gradient a part may go on from one gate row to the next
                     d_yh[i] = d_1[i] = fill(0.0f);
-                }
+            }
+            if (r + 1 < end) {
+                change_gate(++gate_at);
+                gate_end += a.rows_per_gate;
             }
         }
-        if (split.direct && r + 1 == flush)
-            flush = min(flush + a.rows_per_gate, end);
     }
-    float* out = static_cast<float*>(g.workspace) + part * split.sums * split.stride + off;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        store_group<kPack, NT>(out + kPreGamma * split.stride, dz_hh[i], lane, i, width);
-        store_group<kPack, NT>(out + kGate * split.stride, gate_grad(i), lane, i, width);
-        if (!grouped) {
-            const Group gr = gate(first, i);
+        if (!grouped)
+            gate_ends(i);
+        put(kPreGamma, i, dz_hh[i]);
+        put(kGate, i, gate_grad(i));
+        if constexpr (!kGrouped)
+            put(kPostGamma, i, gd_yh[i]);
+        if constexpr (kBeta)
+            put(kPreBeta, i, dz_1[i]);
+        if constexpr (MODE == kLayerShared) {
+            const Group gr = gate(i);
+            Group o;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                gd_yh[i].p[e] = mul2(gr.p[e], d_yh[i].p[e]);
-                if constexpr (kBeta)
-                    gd_1[i].p[e] = mul2(gr.p[e], d_1[i].p[e]);
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            gd_yh[i].p[e] = mul2(branch, gd_yh[i].p[e]);
-            if constexpr (kBeta)
-                gd_1[i].p[e] = mul2(branch, gd_1[i].p[e]);
-        }
-        store_group<kPack, NT>(out + kPostGamma * split.stride, gd_yh[i], lane, i, width);
-        if constexpr (kBeta) {
-            store_group<kPack, NT>(out + kPreBeta * split.stride, dz_1[i], lane, i, width);
-            store_group<kPack, NT>(out + kPostBeta * split.stride, gd_1[i], lane, i, width);
+            for (int e = 0; e < 4; ++e)
+                o.p[e] = mul2(mul2(branch, gr.p[e]), d_1[i].p[e]);
+            put(kPostBeta, i, o);
         }
     }
 }
@@ -861,6 +908,7 @@ __global__ void __launch_bounds__(128)
         return;
     const int lane = threadIdx.x % 32, width = static_cast<int>(a.width);
     int turn = 0;
+    Group gate_now = fill(0.0f);
     backward_rows<B, S, 32, 1, kPack, MODE>(
         a, g, split, part, lane, 0, width,
         [&](int input, int64_t r, int) {
@@ -874,7 +922,7 @@ __global__ void __launch_bounds__(128)
             return inside<kPack, 32>(load_weights<kPack, 32>(weight_vector(a, w), w >= kPreBetaW ? 0.0f : 1.0f, lane, 0, width),
                                      lane, 0, width);
         },
-        [&](int64_t r, int) { return gate_group<kPack, 32, B>(a, r, lane, 0, 0, width); },
+        [&](int) { return gate_now; }, [&](int64_t k) { gate_now = gate_group<kPack, 32, B>(a, k, lane, 0, 0, width); },
         [&](auto& v) { row_sums<32>(v, nullptr, turn); }, [] {});
 }
 
@@ -1003,14 +1051,16 @@ __global__ void __launch_bounds__(NT, kBackwardPerSM<NT>)
                                          : fill(0.0f);
         },
         [&](int w, int) { return kept_group<kPack, NT>(weights + (w == kPreGammaW ? 0 : w == kPostGammaW ? 1 : 3) * room, lane, 0); },
-        [&](int64_t r, int) {
-            return shared_gate ? kept_group<kPack, NT>(weights + 2 * room, lane, 0) : gate_group<kPack, NT, B>(a, r, lane, 0, off, width);
+        [&](int) { return kept_group<kPack, NT>(weights + 2 * room, lane, 0); },
+        [&](int64_t k) {  // each thread its own columns: nobody else reads them
+            if (!shared_gate)
+                keep_group<kPack, NT>(weights + 2 * room, gate_group<kPack, NT, B>(a, k, lane, 0, off, width), lane);
         },
         [&](auto& v) {
             constexpr int K = sizeof(v) / sizeof(v[0]);
             if (!kPack && threadIdx.x < 64)
                 fence_proxy_async_smem();  // of the ends written before: what follows them there comes by bulk copies
-            ring_sums<NT>(v, scratch, turn);
+            ring_sums<NT>(v, scratch, turn, 0);
             const int before = s == 0 ? stages - 1 : s - 1;
             if (now > first && now - 1 + stages < end) {
                 if (threadIdx.x == 0)
