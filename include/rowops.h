@@ -56,7 +56,7 @@ int rowop_layernorm(const float* X, int64_t ldx, const float* gamma, const float
  * consecutive columns and a row stride in elements. Element types are those
  * of gemm_ctype_t. Whatever the types, sums, statistics and every
  * intermediate value are fp32, and each output is rounded once, to nearest
- * even. Results are identical from run to run: no atomics, every sum in a
+ * even. Results are identical from run to run: every sum is taken in a
  * fixed order. Calls enqueue on `stream` without synchronising and return 0
  * or a negative gemm_status_t, as above: GEMM_ERR_ARG for a bad size, stride,
  * type or a missing pointer, GEMM_ERR_ALIGN for a pointer that is not aligned

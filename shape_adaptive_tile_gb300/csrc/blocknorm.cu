@@ -14,8 +14,8 @@ using sat::rows::type_bytes;
 using sat::rows::type_ok;
 
 // The sums of all parts, or of a gate row's pieces, in the order of the parts
-// (eight interleaved runs, then those): a warp takes 32 columns of one sum.
-constexpr int kLanes = 8;
+// (32 interleaved runs, then those): a CTA takes 32 columns of one sum.
+constexpr int kLanes = 32;
 
 struct Outputs {
     float* weights[kSums];  // by Sum; the gate's is not used
@@ -34,6 +34,7 @@ __global__ void __launch_bounds__(32 * kLanes)
     sat_block_norm_sums_kernel(const float* parts, const Split split, int width, const Outputs out)
 {
     __shared__ float run[kLanes][32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // started before the parts were done
     const int c = blockIdx.x * 32 + threadIdx.x;
     // Blocks 0 .. sums - 1 in y: a weight's sum; from there on gate rows.
     const bool gate = blockIdx.y >= split.sums;
@@ -260,9 +261,17 @@ int rowop_block_norm_backward(const rowop_block_norm_args* args, const rowop_blo
     if (g.dpre_gamma || g.dpost_gamma || g.dpre_beta || g.dpost_beta || gate_sums) {
         const dim3 grid(static_cast<unsigned>((a.width + 31) / 32),
                         static_cast<unsigned>(split.sums + (gate_sums ? split.groups : 0)));
-        sat_block_norm_sums_kernel<<<grid, dim3(32, kLanes), 0, s>>>(static_cast<const float*>(g.workspace), split,
-                                                                    static_cast<int>(a.width), out);
-        rc = launched(cudaGetLastError());
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(32, kLanes);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        rc = launched(cudaLaunchKernelEx(&cfg, sat_block_norm_sums_kernel, static_cast<const float*>(g.workspace), split,
+                                         static_cast<int>(a.width), out));
     }
     return rc;
 }

@@ -3,11 +3,12 @@
 // Two kernels. The first reads every row of every sequence once: each warp
 // takes its share of the rows' parts, 4 KB in 16-bit types and all of them in
 // flight at once, and leaves a part's maximum and sum of exponentials in the
-// workspace; HBM bandwidth bounds it. In the second a cluster of CTAs takes a
+// workspace; HBM bandwidth bounds it. In the second several CTAs take a
 // sequence: each puts the parts together, all decide alike which token is the
 // first refused, and each races through its share of that one row (from L2,
-// mostly, and the noise with it, which the first kernel had fetched there).
-// It starts while the first one's last CTAs run.
+// mostly, and the noise with it, which the first kernel had fetched there). The
+// last of them to finish has the winner. The second kernel's CTAs start while
+// the first one's last ones run.
 #include "rows.cuh"
 
 namespace {
@@ -16,7 +17,6 @@ using namespace sat;
 using namespace sat::rows;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
 constexpr int kMaxRows = 2 * ROWOP_VERIFY_MAX_DRAFTS + 1;
 
 // What is kept of a row (or of a part or a warp's share of it): its softmax,
@@ -39,12 +39,6 @@ __device__ __forceinline__ void warp_best(float& v, int& at)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         take(v, at, __shfl_xor_sync(0xffffffffu, v, o), __shfl_xor_sync(0xffffffffu, at, o));
-}
-
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, const uint4& v)
-{
-    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
 }
 
 // A row as packs of 16 bytes on their boundaries in memory: pack i starts with
@@ -114,6 +108,20 @@ __device__ __forceinline__ void load_window(float (&v)[N], const T* row, int j, 
     }
 }
 
+// The same where that is a boundary.
+template <int N, typename T>
+__device__ __forceinline__ void load_beside(float (&v)[N], const T* row, int j)
+{
+#pragma unroll
+    for (int h = 0; h < N / kPer16<T>; ++h) {
+        float u[kPer16<T>];
+        unpack16<T>(*reinterpret_cast<const uint4*>(row + j + h * kPer16<T>), u);
+#pragma unroll
+        for (int e = 0; e < kPer16<T>; ++e)
+            v[h * kPer16<T> + e] = u[e];
+    }
+}
+
 // The rows' parts: `elements` of a row each.
 struct Parts {
     int elements, per_row;
@@ -135,6 +143,29 @@ Parts parts_of(int64_t batch, int64_t drafts, int64_t vocab)
     while (count() > 512 || rows * count() > (1 << 30))
         each *= 2;
     return {static_cast<int>(each), static_cast<int>(count())};
+}
+
+// CTAs of the second kernel for a sequence: three an SM in all, of at least
+// 2048 elements of the race each.
+int racers_of(int64_t batch, int64_t vocab)
+{
+    const int64_t fit = 3 * 152 / batch, want = (vocab + 2047) / 2048, n = fit < want ? fit : want;
+    return static_cast<int>(n < 1 ? 1 : n < 64 ? n : 64);
+}
+
+// What the second kernel's CTAs of a sequence leave for the last of them.
+constexpr int kMaxRacers = 64;
+
+struct __align__(16) Races {
+    float value[kMaxRacers];
+    int token[kMaxRacers];
+    unsigned done;
+};
+
+// Behind the parts in the workspace.
+__device__ __forceinline__ Races* races_of(const rowop_verify_args& a, const Parts& parts)
+{
+    return reinterpret_cast<Races*>(static_cast<RowStats*>(a.workspace) + a.batch * (2 * a.drafts + 1) * parts.per_row);
 }
 
 __device__ __forceinline__ int length_of(const rowop_verify_args& a, int64_t b)
@@ -289,6 +320,9 @@ __global__ void __launch_bounds__(kThreads, 4)
                        (static_cast<int64_t>(b) * (2 * drafts + 1) + (target ? r : drafts + 1 + r)) * parts.per_row + part;
         for (int c = lane; c < more; c += 32)
             to[c] = c == 0 ? st : RowStats{Softmax::none(), -INFINITY, -1};
+        // The sequence's CTAs of the second kernel count themselves from 0.
+        if (i == 0 && part == 0 && lane == 0)
+            races_of(a, parts)[b].done = 0;
         // The noise that the sequence's draw will want, towards L2.
         if (!kGreedy && i == 0) {
             const char* noise = reinterpret_cast<const char*>(a.noise + b * a.ldn);
@@ -299,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
 }
 
-// A cluster of `ctas` a sequence: the decisions, then the draw.
+// `ctas` CTAs a sequence: the decisions, then the draw.
 template <typename T, bool kGreedy>
 __global__ void __launch_bounds__(kThreads, 3)
     sat_verify_draw_kernel(const __grid_constant__ rowop_verify_args a, const Parts parts, int ctas)
@@ -307,10 +341,10 @@ __global__ void __launch_bounds__(kThreads, 3)
     constexpr int N = kPer16<T>;
     __shared__ RowStats whole[kMaxRows];  // of the target's rows, then the draft's
     __shared__ float logit[2][ROWOP_VERIFY_MAX_DRAFTS];  // the target's and the draft's at the drafted tokens
-    __shared__ __align__(16) uint4 races[kMaxCluster];
     __shared__ float values[kWarps];
     __shared__ int where[kWarps];
     __shared__ int refused;
+    __shared__ bool last;
     const int rank = blockIdx.x % ctas, drafts = static_cast<int>(a.drafts), vocab = static_cast<int>(a.vocab);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t b = blockIdx.x / ctas;
@@ -320,8 +354,6 @@ __global__ void __launch_bounds__(kThreads, 3)
     const int rows = len + 1 + (point ? 0 : len);
     auto target_row = [&](int i) { return static_cast<const T*>(a.target) + (b * (drafts + 1) + i) * a.ldt; };
     auto draft_row = [&](int i) { return static_cast<const T*>(a.draft) + (b * drafts + i) * a.ldq; };
-    if (ctas > 1)
-        cluster_arrive();  // waited for before the first store to another CTA, which has to have started by then
     if (threadIdx.x < len) {
         const int i = threadIdx.x, token = a.tokens[b * drafts + i];
         const bool there = token >= 0 && token < vocab;
@@ -384,44 +416,45 @@ __global__ void __launch_bounds__(kThreads, 3)
             const float inv = 1.0f / st.q.sum;
             const Softmax d = whole[minus ? len + 1 + n : 0].q;
             const float q_inv = 1.0f / d.sum;
-            // The race of max(p - q, 0), and where that is nowhere positive, of p.
-            for (int pass = 0; pass < 2 && token < 0; ++pass) {
-                float best = -1.0f;
-                int at = -1;
-                // r / e, as a product with the reciprocal (good to about 2^-22, and the same for the same r and e).
-                // The products of p and q are rounded by themselves: fused with the difference, equal
-                // distributions would leave a residue of rounding size in the place of 0.
-                const uint64_t scale2 = pair(scale, scale), from2 = pair(-st.q.max, -st.q.max);
-                const uint64_t q_scale2 = pair(q_scale, q_scale), q_from2 = pair(-d.max, -d.max);
-                auto score2 = [&](uint64_t t, uint64_t u, float2 e) {
-                    const float2 x = halves(mul2(add2(t, from2), scale2));
-                    float2 r = make_float2(__fmul_rn(ex2(x.x), inv), __fmul_rn(ex2(x.y), inv));
-                    if (minus && pass == 0) {
-                        const float2 y = halves(mul2(add2(u, q_from2), q_scale2));
-                        r.x = __fsub_rn(r.x, __fmul_rn(ex2(y.x), q_inv));
-                        r.y = __fsub_rn(r.y, __fmul_rn(ex2(y.y), q_inv));
-                    }
-                    return halves(mul2(pair(r.x, r.y), pair(rcp(e.x), rcp(e.y))));
-                };
-                auto one = [&](float t, float u, float e, int j) {
-                    if (j == without && pass == 0)
-                        return;
-                    const float s = score2(pair(t, t), pair(u, u), make_float2(e, e)).x;
-                    if (s > 0.0f)
-                        take(best, at, s, j);
-                };
+            // Whether the rows' packs begin with the same elements, so that all come by whole 16-byte loads.
+            const bool wide = ((reinterpret_cast<uint64_t>(noise - s.shift) | (minus ? reinterpret_cast<uint64_t>(q - s.shift) : 0)) & 15) == 0;
+            float best = -1.0f;
+            int at = -1;
+            // r / e for r = max(p - q, 0) (kMinus) or p, as a product with the reciprocal (good to about 2^-22, and
+            // the same for the same r and e). The products of p and q are rounded by themselves: fused with the
+            // difference, equal distributions would leave a residue of rounding size in the place of 0.
+            const uint64_t scale2 = pair(scale, scale), from2 = pair(-st.q.max, -st.q.max);
+            const uint64_t q_scale2 = pair(q_scale, q_scale), q_from2 = pair(-d.max, -d.max);
+            auto score2 = [&](auto subtract, uint64_t t, uint64_t u, float2 e) {
+                const float2 x = halves(mul2(add2(t, from2), scale2));
+                float2 r = make_float2(__fmul_rn(ex2(x.x), inv), __fmul_rn(ex2(x.y), inv));
+                if constexpr (decltype(subtract)::value) {
+                    const float2 y = halves(mul2(add2(u, q_from2), q_scale2));
+                    r.x = __fsub_rn(r.x, __fmul_rn(ex2(y.x), q_inv));
+                    r.y = __fsub_rn(r.y, __fmul_rn(ex2(y.y), q_inv));
+                }
+                return halves(mul2(pair(r.x, r.y), pair(rcp(e.x), rcp(e.y))));
+            };
+            // The race over packs start, start + stride, ... of the row; `skip` is a token that has no part in it.
+            auto race = [&](auto subtract, auto whole_packs, int start, int stride, int skip, bool ends) {
+                constexpr bool kMinus = decltype(subtract)::value, kWide = decltype(whole_packs)::value;
                 constexpr int U = 2;
-                const int stride = ctas * kThreads;
-                for (int i = s.inside + rank * kThreads + threadIdx.x; i < s.end; i += U * stride) {
+                for (int i = s.inside + start; i < s.end; i += U * stride) {
                     uint4 packed[U];
                     float u[U][N], e[U][N];
 #pragma unroll
                     for (int h = 0; h < U; ++h) {
                         const int pack = min(i + h * stride, s.end - 1), j = s.element(pack);  // past the end: the last again
                         packed[h] = s.load(pack);
-                        if (minus && pass == 0)
-                            load_window(u[h], q, j, vocab);
-                        load_window(e[h], noise, j, vocab);
+                        if constexpr (kWide) {
+                            if constexpr (kMinus)
+                                load_beside(u[h], q, j);
+                            load_beside(e[h], noise, j);
+                        } else {
+                            if constexpr (kMinus)
+                                load_window(u[h], q, j, vocab);
+                            load_window(e[h], noise, j, vocab);
+                        }
                     }
 #pragma unroll
                     for (int h = 0; h < U; ++h) {
@@ -431,14 +464,14 @@ __global__ void __launch_bounds__(kThreads, 3)
                         unpack_pairs<T>(packed[h], t);
 #pragma unroll
                         for (int k = 0; k < kPairs<T>; ++k) {
-                            const float2 x = score2(t[k], minus && pass == 0 ? pair(u[h][2 * k], u[h][2 * k + 1]) : 0,
+                            const float2 x = score2(subtract, t[k], kMinus ? pair(u[h][2 * k], u[h][2 * k + 1]) : 0,
                                                     make_float2(e[h][2 * k], e[h][2 * k + 1]));
                             sc[2 * k] = x.x, sc[2 * k + 1] = x.y;
                         }
-                        if (pass == 0 && static_cast<unsigned>(without - j) < N)
+                        if (static_cast<unsigned>(skip - j) < N)
 #pragma unroll
                             for (int k = 0; k < N; ++k)
-                                sc[k] = j + k == without ? 0.0f : sc[k];
+                                sc[k] = j + k == skip ? 0.0f : sc[k];
 #pragma unroll
                         for (int k = 0; k < N; ++k)
                             top = fmaxf(top, sc[k]);
@@ -450,47 +483,60 @@ __global__ void __launch_bounds__(kThreads, 3)
                         }
                     }
                 }
-                if (rank == 0 && warp == kWarps - 1 && lane < 2 * N) {
+                // The ends' elements, a lane each.
+                if (ends && warp == kWarps - 1 && lane < 2 * N) {
                     const int j = lane < N ? (s.inside ? lane - s.shift : -1) : s.element(s.end) + lane - N;
-                    if (j >= 0 && j < vocab)
-                        one(to_f32(s.row[j]), minus ? to_f32(q[j]) : 0.0f, noise[j], j);
+                    if (j >= 0 && j < vocab && j != skip) {
+                        const float t = to_f32(s.row[j]), u = kMinus ? to_f32(q[j]) : 0.0f;
+                        const float sc = score2(subtract, pair(t, t), pair(u, u), make_float2(noise[j], noise[j])).x;
+                        if (sc > 0.0f)
+                            take(best, at, sc, j);
+                    }
                 }
+                // The CTA's best, to every thread.
+                __syncwarp();
                 warp_best(best, at);
-                __syncthreads();  // the pass before has read these
+                __syncthreads();  // a race before has read these
                 if (lane == 0)
                     values[warp] = best, where[warp] = at;
                 __syncthreads();
-                for (int w = 0; w < kWarps; ++w)
-                    take(best, at, values[w], where[w]);
-                if (ctas > 1) {
-                    if (pass == 0) {
-                        __syncwarp();
-                        cluster_wait();
-                    }
-                    if (threadIdx.x < ctas) {
-                        const uint4 v = make_uint4(__float_as_uint(best), static_cast<uint32_t>(at), 0, 0);
-                        st_cluster_v4(map_to_cta(smem_u32(&races[rank]), threadIdx.x), v);
-                    }
-                    __syncwarp();
-                    cluster_sync();
-                    for (int c = 0; c < ctas; ++c) {
-                        const uint4 v = races[c];
-                        take(best, at, __uint_as_float(v.x), static_cast<int>(v.y));
-                    }
-                    if (pass == 0 && at < 0) {  // `races` is read before it is written again
-                        __syncwarp();
-                        cluster_sync();
-                    }
+                best = values[lane % kWarps], at = where[lane % kWarps];
+                warp_best(best, at);
+            };
+            using Yes = std::true_type;
+            using No = std::false_type;
+            const int start = rank * kThreads + threadIdx.x, stride = ctas * kThreads;
+            if (minus && wide)
+                race(Yes(), Yes(), start, stride, -1, rank == 0);
+            else if (minus)
+                race(Yes(), No(), start, stride, -1, rank == 0);
+            else if (wide)
+                race(No(), Yes(), start, stride, without, rank == 0);
+            else
+                race(No(), No(), start, stride, without, rank == 0);
+            if (ctas > 1) {
+                // The last CTA of the sequence to come here has all of them. (Which one that is changes nothing.)
+                Races& races = races_of(a, parts)[b];
+                if (threadIdx.x == 0) {
+                    races.value[rank] = best, races.token[rank] = at;
+                    __threadfence();
+                    last = atomicAdd(&races.done, 1u) == static_cast<unsigned>(ctas) - 1;
+                    __threadfence();
                 }
-                token = at;
+                __syncthreads();
+                if (!last)
+                    return;
+                best = -1.0f, at = -1;
+                for (int c = lane; c < ctas; c += 32)
+                    take(best, at, __ldcg(&races.value[c]), __ldcg(&races.token[c]));
+                warp_best(best, at);
             }
+            if (at < 0)  // p - q is nowhere positive: from p
+                race(No(), No(), threadIdx.x, kThreads, -1, true);
+            token = at;
         }
     }
-    if (ctas > 1 && (kGreedy || !ok(st))) {
-        __syncwarp();
-        cluster_wait();  // of the arrival at the start; the race has waited for it
-    }
-    if (rank)
+    if (ctas > 1 && !ok(st) && rank)
         return;
     for (int i = threadIdx.x; i <= drafts; i += kThreads) {
         const int said = i < n ? a.tokens[b * drafts + i] : i == n ? token : -1;
@@ -557,23 +603,17 @@ cudaError_t launch(const rowop_verify_args& a, cudaStream_t s)
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-    // Three CTAs an SM, of at least 2048 elements of the race each; clusters of 8 at most, which any GPU takes.
-    const int64_t fit = 3 * 152 / a.batch, want = (a.vocab + 2047) / 2048;
-    int64_t ctas = fit < want ? fit : want;
-    ctas = kGreedy || ctas < 1 ? 1 : ctas < kMaxCluster ? ctas : kMaxCluster;
+    const int ctas = kGreedy ? 1 : racers_of(a.batch, a.vocab);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.batch * ctas));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, sat_verify_draw_kernel<T, kGreedy>, a, parts, static_cast<int>(ctas));
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sat_verify_draw_kernel<T, kGreedy>, a, parts, ctas);
 }
 
 template <typename T>
@@ -592,7 +632,8 @@ int64_t rowop_verify_workspace(int64_t batch, int64_t drafts, int64_t vocab)
     const int rc = check_sizes(batch, drafts, vocab);
     if (rc || batch == 0)
         return rc;
-    return batch * (2 * drafts + 1) * parts_of(batch, drafts, vocab).per_row * static_cast<int64_t>(sizeof(RowStats));
+    return batch * ((2 * drafts + 1) * parts_of(batch, drafts, vocab).per_row * static_cast<int64_t>(sizeof(RowStats)) +
+                    static_cast<int64_t>(sizeof(Races)));
 }
 
 int rowop_verify(const rowop_verify_args* args, void* stream)
