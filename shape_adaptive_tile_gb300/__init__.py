@@ -44,6 +44,8 @@ class GemmError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB):
@@ -205,12 +207,13 @@ class _Args(ctypes.Structure):
     def __init__(self, **fields):
         super().__init__()
         self._keep = {}
+        self.address = ctypes.addressof(self)
         for name, value in fields.items():
             setattr(self, name, value)
 
     def __setattr__(self, name, value):
         kind = self._kinds.get(name)
-        if kind is None and name != "_keep":
+        if kind is None and name not in ("_keep", "address"):
             raise AttributeError(f"{type(self).__name__} has no field {name}")
         if kind is ctypes.c_void_p:
             self._keep[name] = value
@@ -218,10 +221,6 @@ class _Args(ctypes.Structure):
         elif isinstance(value, str):
             value = (NORMS if name.endswith("_norm") else C_TYPES)[value]
         super().__setattr__(name, value)
-
-    @property
-    def address(self) -> int:
-        return ctypes.addressof(self)
 
 
 def _struct(name: str, layout: str, doc: str):

@@ -13,9 +13,10 @@ using sat::rows::packs;
 using sat::rows::type_bytes;
 using sat::rows::type_ok;
 
-// The sums of all parts, or of a gate row's pieces, in the order of the parts
-// (32 interleaved runs, then those): a CTA takes 32 columns of one sum.
-constexpr int kLanes = 32;
+// The sums of all parts, or of a gate row's pieces, in a fixed order
+// (interleaved runs of blockDim.y, then those): a CTA takes 32 columns of one
+// sum.
+constexpr int kMaxRuns = 32;
 
 struct Outputs {
     float* weights[kSums];  // by Sum; the gate's is not used
@@ -30,10 +31,10 @@ __device__ __forceinline__ void put(void* p, int64_t at, float v)
     static_cast<T*>(p)[at] = rows::from_f32<T>(v);
 }
 
-__global__ void __launch_bounds__(32 * kLanes)
+__global__ void __launch_bounds__(32 * kMaxRuns)
     sat_block_norm_sums_kernel(const float* parts, const Split split, int width, const Outputs out)
 {
-    __shared__ float run[kLanes][32];
+    __shared__ float run[kMaxRuns][32];
     asm volatile("griddepcontrol.wait;" ::: "memory");  // started before the parts were done
     const int c = blockIdx.x * 32 + threadIdx.x;
     // Blocks 0 .. sums - 1 in y: a weight's sum; from there on gate rows.
@@ -45,13 +46,13 @@ __global__ void __launch_bounds__(32 * kLanes)
     const int64_t first = gate ? group * split.pieces : 0, end = gate ? first + split.pieces : split.parts;
     float s = 0.0f;
     if (c < width)
-        for (int64_t p = first + threadIdx.y; p < end; p += kLanes)
+        for (int64_t p = first + threadIdx.y; p < end; p += blockDim.y)
             s += parts[(p * split.sums + sum) * split.stride + c];
     run[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y || c >= width)
         return;
-    for (int l = 1; l < kLanes; ++l)
+    for (int l = 1; l < blockDim.y; ++l)
         s += run[l][threadIdx.x];
     if (!gate)
         out.weights[sum][c] = s;
@@ -263,7 +264,7 @@ int rowop_block_norm_backward(const rowop_block_norm_args* args, const rowop_blo
                         static_cast<unsigned>(split.sums + (gate_sums ? split.groups : 0)));
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = grid;
-        cfg.blockDim = dim3(32, kLanes);
+        cfg.blockDim = dim3(32, split.parts > 64 ? kMaxRuns : 8);
         cfg.stream = s;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

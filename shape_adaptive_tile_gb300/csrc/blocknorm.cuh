@@ -123,11 +123,21 @@ __device__ __forceinline__ Group load_weights(const float* w, float otherwise, i
     return w ? load_group<kPack, NT>(w, lane, i, width) : fill(otherwise);
 }
 
-// A weight vector of `width` columns, or `otherwise`, into shared memory, with 0 behind it up to `room`.
-__device__ __forceinline__ void keep_weights(float* to, const float* w, float otherwise, int width, int room)
+// A weight vector of `width` columns, or `otherwise`, into shared memory, with
+// 0 behind it up to `room`; eight loads in flight a thread.
+template <typename T>
+__device__ __forceinline__ void keep_weights(float* to, const T* w, float otherwise, int width, int room)
 {
-    for (int c = threadIdx.x; c < room; c += blockDim.x)
-        to[c] = c >= width ? 0.0f : w ? w[c] : otherwise;
+    for (int c = threadIdx.x; c < room; c += 8 * blockDim.x) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = c + e * blockDim.x >= width ? 0.0f : w ? to_f32(w[c + e * blockDim.x]) : otherwise;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e * blockDim.x < room)
+                to[c + e * blockDim.x] = v[e];
+    }
 }
 
 // Group i of weights that lie in shared memory.
@@ -568,8 +578,7 @@ __global__ void __launch_bounds__(512 + 32, 1)
         const bool there = kept && (w == kGateW ? shared_gate : weight_vector(a, w) != nullptr);
         at[w] = there ? weights + n * room : nullptr;
         if (there && w == kGateW && a.gate_type != GEMM_C_F32)
-            for (int c = threadIdx.x; c < room; c += blockDim.x)
-                weights[n * room + c] = c < width ? to_f32(static_cast<const B*>(a.gate)[c]) : 0.0f;
+            keep_weights(weights + n * room, static_cast<const B*>(a.gate), 1.0f, width, room);
         else if (there)
             keep_weights(weights + n * room, w == kGateW ? static_cast<const float*>(a.gate) : weight_vector(a, w), 1.0f, width, room);
         n += there;
@@ -967,8 +976,7 @@ __global__ void __launch_bounds__(NT, kBackwardPerSM<NT>)
     keep_weights(weights, vector_of(kPreGammaW), 1.0f, width, room);
     keep_weights(weights + room, vector_of(kPostGammaW), 1.0f, width, room);
     if (a.gate && shared_gate && a.gate_type != GEMM_C_F32)
-        for (int c = threadIdx.x; c < room; c += NT)
-            weights[2 * room + c] = c < width ? to_f32(static_cast<const B*>(a.gate)[off + c]) : 0.0f;
+        keep_weights(weights + 2 * room, static_cast<const B*>(a.gate) + off, 1.0f, width, room);
     else
         keep_weights(weights + 2 * room, a.gate && shared_gate ? static_cast<const float*>(a.gate) + off : nullptr, 1.0f, width, room);
     if (kBeta)

@@ -1,14 +1,17 @@
 // Distillation from a teacher's top logits and its gradient (include/rowops.h).
 //
-// A row's logits are cut into slices that lie in shared memory while a CTA
-// works on them: fetched by bulk copies (all of a slice in flight at once),
-// reduced to a maximum and a sum of exponentials chunk by chunk as they
-// land, and, for the gradient, read a second time from there. The CTAs of a
-// cluster take a row's slices and put their maxima and sums together through
-// distributed shared memory, so a row that no SM could hold is read from
-// memory once and its gradient written once: 4 bytes a token in 16-bit
-// types, which HBM bandwidth bounds. Slices are cut on 16-byte boundaries of
-// memory, wherever the row starts; the ragged ends move by plain loads.
+// Of many rows a CTA takes one at a time, with two passes over its logits: the
+// maximum and the sum of exponentials, and the gradient. The second pass finds
+// the row in L2, as the rows at hand in all SMs fit there, so HBM sees 4 bytes a
+// token in 16-bit types, which its bandwidth bounds.
+//
+// Few rows, and the gradient alone, go in slices that lie in shared memory
+// while a CTA works on them: fetched by bulk copies (all of a slice in flight
+// at once), reduced to a maximum and a sum of exponentials chunk by chunk as
+// they land, and, for the gradient, read a second time from there. The CTAs of
+// a cluster take a row's slices and put their maxima and sums together through
+// distributed shared memory. Slices are cut on 16-byte boundaries of memory,
+// wherever the row starts; the ragged ends move by plain loads.
 #include "ptx.cuh"
 #include "rows.cuh"
 
@@ -317,6 +320,169 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+// ---- many rows: a CTA a row -----------------------------------------------------
+
+constexpr int64_t kFullRows = 2 * 152;
+
+// Threads of a row's CTA, and CTAs an SM: the loss alone does best with four
+// rows at hand in an SM, the gradient with two, whose second passes find more
+// of their rows in L2.
+template <int MODE>
+constexpr int kRowThreads = MODE == kLoss ? 256 : 512;
+
+// The factors of a gradient: of logit v it is share 2^((v times - from) power),
+// less the teacher's part.
+struct Gradient {
+    float share, times, from, power;
+
+    __device__ __forceinline__ float of(float v) const { return share * ex2(fmaf(v, times, -from) * power); }
+};
+
+template <typename T>
+__device__ __forceinline__ uint4 gradient_of(const uint4& w, const Gradient& f)
+{
+    const uint64_t times = pair(f.times, f.times), from = pair(-f.from, -f.from), power = pair(f.power, f.power);
+    const uint64_t share = pair(f.share, f.share);
+    uint64_t v[kPairs<T>];
+    unpack_pairs<T>(w, v);
+    float o[kPer16<T>];
+#pragma unroll
+    for (int e = 0; e < kPairs<T>; ++e) {
+        const float2 x = halves(mul2(fma2(v[e], times, from), power));
+        const float2 y = halves(mul2(pair(ex2(x.x), ex2(x.y)), share));
+        o[2 * e] = y.x, o[2 * e + 1] = y.y;
+    }
+    return pack16<T>(o);
+}
+
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kRowThreads<MODE>, 1024 / kRowThreads<MODE>) sat_distill_row_kernel(const __grid_constant__ rowop_distill_args a)
+{
+    constexpr int N = kPer16<T>, U = 8, NT = kRowThreads<MODE>, W = NT / 32;
+    extern __shared__ float entries[];
+    __shared__ Softmax scratch[2][W];
+    __shared__ float sums[2 * W];
+    const int k = static_cast<int>(a.k), vocab = static_cast<int>(a.vocab), warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    float *p = entries, *log_p = p + k, *at_id = log_p + k;  // the teacher's probabilities, their log2, the student's logits there
+    int* id = reinterpret_cast<int*>(at_id + k);             // -1 for an absent entry
+    const int64_t r = blockIdx.x;
+    const float weight = a.weight ? a.weight[r] : 1.0f, scale = kLog2e / a.temperature;
+    const Packs<T> s(static_cast<const T*>(a.logits) + r * a.ldl, vocab);
+    T* out = a.dlogits ? static_cast<T*>(a.dlogits) + r * a.ldd : nullptr;
+    int turn = 0;
+
+    // f(packs, first) for the row's packs in batches of U a thread, all of a batch's loads first; packs past the end are -inf.
+    auto batches = [&](auto f) {
+        int j = s.inside + threadIdx.x;
+        for (; j - static_cast<int>(threadIdx.x) + U * NT <= s.end; j += U * NT) {
+            uint4 w[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                w[u] = s.load(j + u * NT);
+            f(w, j, true);
+        }
+        if (j < s.end) {
+            uint4 w[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                w[u] = j + u * NT < s.end ? s.load(j + u * NT) : nothing<T>();
+            f(w, j, false);
+        }
+    };
+    // The column of the element at the row's ends, outside whole packs, that this lane of the last warp sees to.
+    const int end_column = warp < W - 1 || lane >= 2 * N ? -1
+                           : lane < N                            ? (s.inside ? lane - s.shift : -1)
+                                                                 : s.element(s.end) + lane - N;
+    const bool at_end = end_column >= 0 && end_column < vocab;
+
+    Softmax t = Softmax::none();
+    if (weight != 0.0f)
+        for (int i = threadIdx.x; i < k; i += NT) {
+            const int token = a.ids[r * a.ldi + i];
+            const float v = teacher_logit(a, r * a.ldt + i);
+            const bool there = token >= 0 && token < vocab && v != -INFINITY;
+            id[i] = there ? token : -1;
+            log_p[i] = v;
+            at_id[i] = there ? to_f32(s.row[token]) : 0.0f;  // before the gradient, which may be in the logits' place
+            if (there)
+                t.add(v, scale);
+        }
+    t = cta_softmax<NT>(t, scale, scratch[0]);
+    if (t.max == -INFINITY) {  // masked, or no entry present
+        if (threadIdx.x == 0) {
+            a.loss[r] = 0.0f;
+            if (a.lse)
+                a.lse[r] = 0.0f;
+        }
+        if (MODE == kBoth) {
+            const Packs<T> o(out, vocab);
+            for (int j = o.inside + threadIdx.x; j < o.end; j += NT)
+                *reinterpret_cast<uint4*>(out + o.element(j)) = make_uint4(0, 0, 0, 0);
+            if (warp == W - 1 && lane < 2 * N) {
+                const int c = lane < N ? (o.inside ? lane - o.shift : -1) : o.element(o.end) + lane - N;
+                if (c >= 0 && c < vocab)
+                    out[c] = from_f32<T>(0.0f);
+            }
+        }
+        return;
+    }
+    const float top = a.teacher_lse ? 0.0f : t.max, rest = a.teacher_lse ? a.teacher_lse[r] * kLog2e : log2f(t.sum);
+
+    Softmax q = Softmax::none();
+    batches([&](const uint4(&w)[U], int, bool) { q.add(softmax_of<T>(w, scale), scale); });
+    if (at_end)
+        q.add(to_f32(s.row[end_column]), scale);
+    __syncwarp();
+    q = cta_softmax<NT>(q, scale, scratch[1]);
+    const float log_sum = log2f(q.sum);
+    float sum[2] = {0.0f, 0.0f};  // of p, and of p (log p - log q)
+    for (int i = threadIdx.x; i < k; i += NT) {
+        log_p[i] = (log_p[i] - top) * scale - rest;
+        p[i] = id[i] >= 0 ? exp2f(log_p[i]) : 0.0f;
+        sum[0] += p[i];
+        if (p[i] > 0.0f)
+            sum[1] += p[i] * (log_p[i] - ((at_id[i] - q.max) * scale - log_sum));
+    }
+    row_sums<NT>(sum, sums, turn);
+    if (threadIdx.x == 0) {
+        a.loss[r] = weight * a.temperature * a.temperature * kLn2 * sum[1];
+        if (a.lse)
+            a.lse[r] = (q.max * scale + log_sum) * kLn2;
+    }
+    if (MODE == kLoss)
+        return;
+    const float c = (a.dloss ? a.dloss[r] : 1.0f) * weight * a.temperature;
+    const Gradient f = {c * sum[0] / q.sum, 1.0f, q.max, scale};
+    if (((reinterpret_cast<uint64_t>(out) ^ reinterpret_cast<uint64_t>(s.row)) & 15) == 0) {
+        batches([&](const uint4(&w)[U], int j, bool all) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (all || j + u * NT < s.end)
+                    __stcs(reinterpret_cast<uint4*>(out + s.element(j + u * NT)), gradient_of<T>(w[u], f));
+        });
+        if (at_end)
+            out[end_column] = from_f32<T>(f.of(to_f32(s.row[end_column])));
+    } else {  // rows that begin on other bytes of 16 than the logits': element by element
+        for (int j = threadIdx.x; j < vocab; j += NT)
+            out[j] = from_f32<T>(f.of(to_f32(s.row[j])));
+    }
+    __syncthreads();
+    // The teacher's tokens, each once: by the first of the entries that name it.
+    for (int n = threadIdx.x; n < k; n += NT) {
+        if (id[n] < 0)
+            continue;
+        bool lowest = true;
+        float pn = 0.0f;
+        for (int l = 0; l < k; ++l)
+            if (id[l] == id[n]) {
+                lowest = lowest && l >= n;
+                pn += p[l];
+            }
+        if (lowest)
+            out[id[n]] = from_f32<T>(f.of(at_id[n]) - c * pn);
+    }
+}
+
 int check(const rowop_distill_args* a, bool forward)
 {
     if (!a)
@@ -351,6 +517,11 @@ int check(const rowop_distill_args* a, bool forward)
 template <typename T, int MODE>
 cudaError_t launch(const rowop_distill_args& a, cudaStream_t s)
 {
+    // Rows enough for two CTAs an SM: one a row. (Slices of a row each find the others' softmaxes only by waiting.)
+    if (MODE != kGrad && a.rows >= kFullRows) {
+        sat_distill_row_kernel<T, MODE><<<static_cast<unsigned>(a.rows), kRowThreads<MODE>, a.k * 16, s>>>(a);
+        return cudaGetLastError();
+    }
     // With what a row may need before its start to reach a 16-byte boundary.
     const bool even = aligned(a.logits, 16) && a.ldl * sizeof(T) % 16 == 0;
     const int64_t bytes = a.vocab * static_cast<int64_t>(sizeof(T)) + (even ? 0 : 15);

@@ -150,6 +150,25 @@ __device__ __forceinline__ uint4 pack16(const float (&in)[kPer16<T>])
     }
 }
 
+// A row as packs of 16 bytes on their boundaries in memory: pack i starts with
+// element i N - shift, and those from `inside` to `end` lie wholly in the row.
+template <typename T>
+struct Packs {
+    static constexpr int N = kPer16<T>;
+    const T* row;
+    int vocab, shift, count, inside, end;
+
+    __device__ __forceinline__ Packs(const T* r, int v) : row(r), vocab(v)
+    {
+        shift = static_cast<int>((reinterpret_cast<uint64_t>(r) & 15) / sizeof(T));
+        count = (v + shift + N - 1) / N;
+        inside = shift ? 1 : 0;
+        end = max((v + shift) / N, inside);
+    }
+    __device__ __forceinline__ int element(int i) const { return i * N - shift; }
+    __device__ __forceinline__ uint4 load(int i) const { return *reinterpret_cast<const uint4*>(row + element(i)); }
+};
+
 // Sums of N values over the NT threads that share a row, returned to each of
 // them, in a fixed order: lanes by shuffles, then (NT > 32) warps through
 // `scratch`, 2 x N x NT / 32 floats. Consecutive reductions alternate between

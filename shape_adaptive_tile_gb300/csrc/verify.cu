@@ -41,25 +41,6 @@ __device__ __forceinline__ void warp_best(float& v, int& at)
         take(v, at, __shfl_xor_sync(0xffffffffu, v, o), __shfl_xor_sync(0xffffffffu, at, o));
 }
 
-// A row as packs of 16 bytes on their boundaries in memory: pack i starts with
-// element i N - shift, and those from `inside` to `end` lie wholly in the row.
-template <typename T>
-struct Packs {
-    static constexpr int N = kPer16<T>;
-    const T* row;
-    int vocab, shift, count, inside, end;
-
-    __device__ __forceinline__ Packs(const T* r, int v) : row(r), vocab(v)
-    {
-        shift = static_cast<int>((reinterpret_cast<uint64_t>(r) & 15) / sizeof(T));
-        count = (v + shift + N - 1) / N;
-        inside = shift ? 1 : 0;
-        end = max((v + shift) / N, inside);
-    }
-    __device__ __forceinline__ int element(int i) const { return i * N - shift; }
-    __device__ __forceinline__ uint4 load(int i) const { return *reinterpret_cast<const uint4*>(row + element(i)); }
-};
-
 // N consecutive elements from row[j] on, of a row of `vocab`: by 16-byte loads
 // from the boundary before them, shifted into place, where all that these
 // touch lies in the row. The shift is the same for all lanes.
