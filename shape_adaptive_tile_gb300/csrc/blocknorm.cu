@@ -96,6 +96,7 @@ Split split_of(const rowop_block_norm_args& a, bool gate)
             }
         }
         s.parts = s.groups * s.pieces;
+        s.direct = s.groups > 1 && s.pieces == 1;
     }
     return s;
 }
@@ -264,7 +265,7 @@ int rowop_block_norm_backward(const rowop_block_norm_args* args, const rowop_blo
                         static_cast<unsigned>(split.sums + (gate_sums ? split.groups : 0)));
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = grid;
-        cfg.blockDim = dim3(32, split.parts > 64 ? kMaxRuns : 8);
+        cfg.blockDim = dim3(32, split.parts > 64 && grid.y <= 16 ? kMaxRuns : 8);  // many gate rows have few pieces each
         cfg.stream = s;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -29,6 +29,43 @@ constexpr int kWaitLimit = 1 << 22;  // polls of a barrier, each of which the ha
 
 enum Mode { kLoss, kBoth, kGrad };
 
+// The teacher's entries of a row in shared memory, four arrays of k rounded up
+// to whole 16 bytes, so that the tokens can be compared four at a time.
+struct Entries {
+    float *p, *log_p, *at_id;  // the teacher's probabilities, their logarithms, the student's logits there (for the loss)
+    int* id;                   // -1 for an absent entry, -2 past the last
+    int padded;
+
+    static __host__ __device__ constexpr int room(int k) { return (k + 3) / 4 * 16 * 4; }
+
+    __device__ __forceinline__ Entries(void* memory, int k) : padded((k + 3) / 4 * 4)
+    {
+        p = static_cast<float*>(memory);
+        log_p = p + padded, at_id = log_p + padded, id = reinterpret_cast<int*>(at_id + padded);
+    }
+
+    // The probability of entry n's token, of all entries that name it, for the first of these; for the others -1.
+    __device__ __forceinline__ float of(int n) const
+    {
+        const int token = id[n];
+        float sum = 0.0f;
+        for (int l = 0; l < padded; l += 4) {
+            const int4 four = *reinterpret_cast<const int4*>(id + l);
+            if (four.x != token && four.y != token && four.z != token && four.w != token)
+                continue;
+            const int names[4] = {four.x, four.y, four.z, four.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (names[e] == token) {
+                    if (l + e < n)
+                        return -1.0f;
+                    sum += p[l + e];
+                }
+        }
+        return sum;
+    }
+};
+
 // A row's slices, `bytes` each from the 16-byte boundary at or before its
 // start. CTA `rank` of the row's `ctas` takes slices rank, rank + ctas, ...
 struct Slices {
@@ -61,10 +98,9 @@ __global__ void __launch_bounds__(kThreads)
 {
     constexpr int N = kPer16<T>;
     extern __shared__ __align__(128) unsigned char slice[];
-    float* p = reinterpret_cast<float*>(slice + cut.bytes);  // the teacher's probabilities
-    float* log_p = p + a.k;                                  // its logits, then log2 of the probabilities
-    float* at_id = log_p + a.k;                              // the student's logits there (for the loss)
-    int* id = reinterpret_cast<int*>(at_id + a.k);           // -1 for an absent entry
+    const Entries teacher(slice + cut.bytes, static_cast<int>(a.k));
+    float *p = teacher.p, *log_p = teacher.log_p, *at_id = teacher.at_id;
+    int* id = teacher.id;
     __shared__ __align__(8) uint64_t bars[kMaxChunks];
     __shared__ Softmax scratch[2][kWarps];
     __shared__ float sums[2 * kWarps];
@@ -199,6 +235,8 @@ __global__ void __launch_bounds__(kThreads)
     int turn = 0;
     if (MODE != kLoss || rank == 0) {
         Softmax t = Softmax::none();
+        if (threadIdx.x < teacher.padded - k)
+            id[k + threadIdx.x] = -2;
         for (int i = threadIdx.x; i < k; i += kThreads) {
             const int token = a.ids[r * a.ldi + i];
             const float v = teacher_logit(a, r * a.ldt + i);
@@ -213,10 +251,10 @@ __global__ void __launch_bounds__(kThreads)
         }
         t = cta_softmax<kThreads>(t, scale, scratch[0]);
         empty = t.max == -INFINITY;
-        const float top = a.teacher_lse ? 0.0f : t.max, rest = a.teacher_lse ? a.teacher_lse[r] * kLog2e : log2f(t.sum);
+        const float top = a.teacher_lse ? 0.0f : t.max, rest = a.teacher_lse ? a.teacher_lse[r] : logf(t.sum);
         for (int i = threadIdx.x; i < k; i += kThreads) {
-            log_p[i] = (log_p[i] - top) * scale - rest;
-            p[i] = id[i] >= 0 ? exp2f(log_p[i]) : 0.0f;
+            log_p[i] = (log_p[i] - top) / a.temperature - rest;
+            p[i] = id[i] >= 0 ? expf(log_p[i]) : 0.0f;
             sum[0] += p[i];
         }
         row_sums<kThreads>(sum, sums, turn);
@@ -257,17 +295,17 @@ __global__ void __launch_bounds__(kThreads)
             cluster_sync();
             q = sum_softmax(across, 1, cut.ctas, scale);
         }
-        const float log_sum = log2f(q.sum);
+        const float log_sum = logf(q.sum);
         if (rank == 0) {
             float loss[1] = {0.0f};
             for (int i = threadIdx.x; i < k; i += kThreads)
                 if (p[i] > 0.0f)
-                    loss[0] += p[i] * (log_p[i] - ((at_id[i] - q.max) * scale - log_sum));
+                    loss[0] += p[i] * (log_p[i] - ((at_id[i] - q.max) / a.temperature - log_sum));
             row_sums<kThreads>(loss, sums, turn);
             if (threadIdx.x == 0) {
-                a.loss[r] = empty ? 0.0f : weight * a.temperature * a.temperature * kLn2 * loss[0];
+                a.loss[r] = empty ? 0.0f : weight * a.temperature * a.temperature * loss[0];
                 if (a.lse)
-                    a.lse[r] = empty ? 0.0f : (q.max * scale + log_sum) * kLn2;
+                    a.lse[r] = empty ? 0.0f : q.max / a.temperature + log_sum;
             }
         }
     }
@@ -305,14 +343,8 @@ __global__ void __launch_bounds__(kThreads)
         for (int n = threadIdx.x; n < k; n += kThreads) {
             if (id[n] < max(first, int64_t{0}) || id[n] >= last)
                 continue;
-            bool lowest = true;
-            float pn = 0.0f;
-            for (int l = 0; l < k; ++l)
-                if (id[l] == id[n]) {
-                    lowest = lowest && l >= n;
-                    pn += p[l];
-                }
-            if (lowest) {
+            const float pn = teacher.of(n);
+            if (pn >= 0.0f) {
                 const float v = to_f32(reinterpret_cast<const T*>(slice)[id[n] - first]);
                 out[id[n]] = from_f32<T>(one_of(v) - c * pn);
             }
@@ -322,13 +354,7 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---- many rows: a CTA a row -----------------------------------------------------
 
-constexpr int64_t kFullRows = 2 * 152;
-
-// Threads of a row's CTA, and CTAs an SM: the loss alone does best with four
-// rows at hand in an SM, the gradient with two, whose second passes find more
-// of their rows in L2.
-template <int MODE>
-constexpr int kRowThreads = MODE == kLoss ? 256 : 512;
+constexpr int64_t kFullRows = 2 * 152, kShortRow = 16384;
 
 // The factors of a gradient: of logit v it is share 2^((v times - from) power),
 // less the teacher's part.
@@ -355,16 +381,17 @@ __device__ __forceinline__ uint4 gradient_of(const uint4& w, const Gradient& f)
     return pack16<T>(o);
 }
 
-template <typename T, int MODE>
-__global__ void __launch_bounds__(kRowThreads<MODE>, 1024 / kRowThreads<MODE>) sat_distill_row_kernel(const __grid_constant__ rowop_distill_args a)
+template <typename T, int MODE, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) sat_distill_row_kernel(const __grid_constant__ rowop_distill_args a)
 {
-    constexpr int N = kPer16<T>, U = 8, NT = kRowThreads<MODE>, W = NT / 32;
-    extern __shared__ float entries[];
+    constexpr int N = kPer16<T>, U = 8, W = NT / 32;
+    extern __shared__ __align__(16) unsigned char entries[];
     __shared__ Softmax scratch[2][W];
     __shared__ float sums[2 * W];
     const int k = static_cast<int>(a.k), vocab = static_cast<int>(a.vocab), warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    float *p = entries, *log_p = p + k, *at_id = log_p + k;  // the teacher's probabilities, their log2, the student's logits there
-    int* id = reinterpret_cast<int*>(at_id + k);             // -1 for an absent entry
+    const Entries teacher(entries, k);
+    float *p = teacher.p, *log_p = teacher.log_p, *at_id = teacher.at_id;
+    int* id = teacher.id;
     const int64_t r = blockIdx.x;
     const float weight = a.weight ? a.weight[r] : 1.0f, scale = kLog2e / a.temperature;
     const Packs<T> s(static_cast<const T*>(a.logits) + r * a.ldl, vocab);
@@ -396,6 +423,8 @@ __global__ void __launch_bounds__(kRowThreads<MODE>, 1024 / kRowThreads<MODE>) s
     const bool at_end = end_column >= 0 && end_column < vocab;
 
     Softmax t = Softmax::none();
+    if (threadIdx.x < teacher.padded - k)
+        id[k + threadIdx.x] = -2;
     if (weight != 0.0f)
         for (int i = threadIdx.x; i < k; i += NT) {
             const int token = a.ids[r * a.ldi + i];
@@ -426,7 +455,7 @@ __global__ void __launch_bounds__(kRowThreads<MODE>, 1024 / kRowThreads<MODE>) s
         }
         return;
     }
-    const float top = a.teacher_lse ? 0.0f : t.max, rest = a.teacher_lse ? a.teacher_lse[r] * kLog2e : log2f(t.sum);
+    const float top = a.teacher_lse ? 0.0f : t.max, rest = a.teacher_lse ? a.teacher_lse[r] : logf(t.sum);
 
     Softmax q = Softmax::none();
     batches([&](const uint4(&w)[U], int, bool) { q.add(softmax_of<T>(w, scale), scale); });
@@ -434,20 +463,20 @@ __global__ void __launch_bounds__(kRowThreads<MODE>, 1024 / kRowThreads<MODE>) s
         q.add(to_f32(s.row[end_column]), scale);
     __syncwarp();
     q = cta_softmax<NT>(q, scale, scratch[1]);
-    const float log_sum = log2f(q.sum);
+    const float log_sum = logf(q.sum);
     float sum[2] = {0.0f, 0.0f};  // of p, and of p (log p - log q)
     for (int i = threadIdx.x; i < k; i += NT) {
-        log_p[i] = (log_p[i] - top) * scale - rest;
-        p[i] = id[i] >= 0 ? exp2f(log_p[i]) : 0.0f;
+        log_p[i] = (log_p[i] - top) / a.temperature - rest;
+        p[i] = id[i] >= 0 ? expf(log_p[i]) : 0.0f;
         sum[0] += p[i];
         if (p[i] > 0.0f)
-            sum[1] += p[i] * (log_p[i] - ((at_id[i] - q.max) * scale - log_sum));
+            sum[1] += p[i] * (log_p[i] - ((at_id[i] - q.max) / a.temperature - log_sum));
     }
     row_sums<NT>(sum, sums, turn);
     if (threadIdx.x == 0) {
-        a.loss[r] = weight * a.temperature * a.temperature * kLn2 * sum[1];
+        a.loss[r] = weight * a.temperature * a.temperature * sum[1];
         if (a.lse)
-            a.lse[r] = (q.max * scale + log_sum) * kLn2;
+            a.lse[r] = q.max / a.temperature + log_sum;
     }
     if (MODE == kLoss)
         return;
@@ -471,14 +500,8 @@ __global__ void __launch_bounds__(kRowThreads<MODE>, 1024 / kRowThreads<MODE>) s
     for (int n = threadIdx.x; n < k; n += NT) {
         if (id[n] < 0)
             continue;
-        bool lowest = true;
-        float pn = 0.0f;
-        for (int l = 0; l < k; ++l)
-            if (id[l] == id[n]) {
-                lowest = lowest && l >= n;
-                pn += p[l];
-            }
-        if (lowest)
+        const float pn = teacher.of(n);
+        if (pn >= 0.0f)
             out[id[n]] = from_f32<T>(f.of(at_id[n]) - c * pn);
     }
 }
@@ -517,10 +540,20 @@ int check(const rowop_distill_args* a, bool forward)
 template <typename T, int MODE>
 cudaError_t launch(const rowop_distill_args& a, cudaStream_t s)
 {
-    // Rows enough for two CTAs an SM: one a row. (Slices of a row each find the others' softmaxes only by waiting.)
-    if (MODE != kGrad && a.rows >= kFullRows) {
-        sat_distill_row_kernel<T, MODE><<<static_cast<unsigned>(a.rows), kRowThreads<MODE>, a.k * 16, s>>>(a);
-        return cudaGetLastError();
+    if constexpr (MODE != kGrad) {
+        // Rows enough for two CTAs an SM: one a row. (Slices of a row each find the others' softmaxes only by
+        // waiting.) Short rows, whose fixed work counts, are eight at hand in an SM; of long ones the loss alone
+        // does best with four and the gradient with two, whose second passes find more of their rows in L2.
+        if (a.rows >= kFullRows) {
+            constexpr int NT = MODE == kLoss ? 256 : 512;
+            const unsigned grid = static_cast<unsigned>(a.rows);
+            const int smem = Entries::room(static_cast<int>(a.k));
+            if (a.vocab <= kShortRow)
+                sat_distill_row_kernel<T, MODE, 128><<<grid, 128, smem, s>>>(a);
+            else
+                sat_distill_row_kernel<T, MODE, NT><<<grid, NT, smem, s>>>(a);
+            return cudaGetLastError();
+        }
     }
     // With what a row may need before its start to reach a 16-byte boundary.
     const bool even = aligned(a.logits, 16) && a.ldl * sizeof(T) % 16 == 0;
@@ -536,10 +569,10 @@ cudaError_t launch(const rowop_distill_args& a, cudaStream_t s)
     const int64_t each = (bytes + cut.ctas - 1) / cut.ctas;
     cut.bytes = static_cast<int>(each < kMaxSlice ? (each + 127) / 128 * 128 : kMaxSlice);
     cut.per_row = static_cast<int>((bytes + cut.bytes - 1) / cut.bytes);
-    const int smem = cut.bytes + static_cast<int>(a.k) * 16;
+    const int smem = cut.bytes + Entries::room(static_cast<int>(a.k));
     auto kernel = sat_distill_kernel<T, MODE>;
     static Prepared prepared;
-    const cudaError_t e = prepared.once(reinterpret_cast<const void*>(kernel), kMaxSlice + ROWOP_DISTILL_MAX_K * 16);
+    const cudaError_t e = prepared.once(reinterpret_cast<const void*>(kernel), kMaxSlice + Entries::room(ROWOP_DISTILL_MAX_K));
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};

@@ -250,20 +250,11 @@ __global__ void __launch_bounds__(kThreads, 4)
         const int first = part * (parts.elements / N), last = min(first + more * (parts.elements / N), s.count);
         const int begin = max(first, s.inside), end = min(last, s.end);
         RowStats st = {Softmax::none(), -INFINITY, -1};
+        int top_batch = 0;  // the first batch that has the largest value
         auto add = [&](const uint4(&w)[U], int j) {
             const Softmax q = softmax_of<T>(w, scale);
-            if (kGreedy && q.max > st.value) {  // of equals the lower token: later packs are higher
-                st.value = q.max;
-#pragma unroll
-                for (int u = U - 1; u >= 0; --u) {
-                    float v[N];
-                    unpack16<T>(w[u], v);
-#pragma unroll
-                    for (int e = N - 1; e >= 0; --e)
-                        if (v[e] == q.max)
-                            st.best = s.element(j + u * 32) + e;
-                }
-            }
+            if (kGreedy && q.max > st.value)
+                st.value = q.max, top_batch = j;
             st.q.add(q, scale);
         };
         int j = begin + lane;
@@ -281,6 +272,15 @@ __global__ void __launch_bounds__(kThreads, 4)
                 w[u] = j + u * 32 < end ? s.load(j + u * 32) : nothing<T>();
             add(w, j);
         }
+        if (kGreedy && st.value > -INFINITY)  // its lowest token: the batch again
+#pragma unroll 1
+            for (int u = 0; u < U && st.best < 0; ++u) {
+                float v[N];
+                unpack16<T>(top_batch + u * 32 < end ? s.load(top_batch + u * 32) : nothing<T>(), v);
+#pragma unroll
+                for (int e = N - 1; e >= 0; --e)
+                    st.best = v[e] == st.value ? s.element(top_batch + u * 32) + e : st.best;
+            }
         // The packs at the row's ends, an element a lane.
         if (lane < 2 * N) {
             const int c = lane < N ? (s.inside && part == 0 ? lane - s.shift : -1)
