@@ -112,6 +112,31 @@ def test_random_strides_and_offsets(i):
          int(rng.choice([0, 1, 3, 8])), int(rng.choice([0, 1, 5, 8])), bool(i % 2)).check()
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("vocab,k,pad", [(40, 7, 0), (9001, 300, 0), (16384, 5, 8), (16400, 33, 0), (33001, 12, 3)])
+def test_many_rows(vocab, k, pad, dtype):
+    # More rows than two an SM: a CTA each, of short rows and of long ones; in place too.
+    c = Case(vocab, 306, vocab, min(k, vocab), dtype, "fp32", 1.5, pad, pad)
+    c.weight[::7] = 0.0
+    c.ids[5] = -1
+    c.check()
+    loss, lse, d, d2, _ = c.run()
+    assert sat.rowop_distill(c.args(loss=lse, dlogits=c.logits, ldd=c.logits.stride(0)), stream()) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(c.logits, d) and torch.equal(loss, lse)
+
+
+@pytest.mark.parametrize("vocab", [50, 5000, 70000, 280000])
+def test_gradient_rows_on_other_bytes_than_the_logits(vocab):
+    for rows in (5, 306 if vocab < 10000 else 6):
+        c = Case(4, rows, vocab, 9, "bf16")
+        loss, lse, d, _, _ = c.run()
+        e, whole = ref.place(np.zeros((rows, vocab)), "bf16", 1, 3, -77.0)
+        assert sat.rowop_distill(c.args(loss=loss, dlogits=e, ldd=e.stride(0)), stream()) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(d, e) and ref.sentinel_intact(e, whole, -77.0)
+
+
 @pytest.mark.parametrize("vocab", [50, 5000, 70000, 280000])
 def test_masked_and_absent(vocab):
     c = Case(4, 9, vocab, 24, "bf16", "bf16", 2.0)
