@@ -126,11 +126,11 @@ Parts parts_of(int64_t batch, int64_t drafts, int64_t vocab)
     return {static_cast<int>(each), static_cast<int>(count())};
 }
 
-// CTAs of the second kernel for a sequence: three an SM in all, of at least
+// CTAs of the second kernel for a sequence: four an SM in all, of at least
 // 2048 elements of the race each.
 int racers_of(int64_t batch, int64_t vocab)
 {
-    const int64_t fit = 3 * 152 / batch, want = (vocab + 2047) / 2048, n = fit < want ? fit : want;
+    const int64_t fit = 4 * 152 / batch, want = (vocab + 2047) / 2048, n = fit < want ? fit : want;
     return static_cast<int>(n < 1 ? 1 : n < 64 ? n : 64);
 }
 
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 
 // `ctas` CTAs a sequence: the decisions, then the draw.
 template <typename T, bool kGreedy>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
     sat_verify_draw_kernel(const __grid_constant__ rowop_verify_args a, const Parts parts, int ctas)
 {
     constexpr int N = kPer16<T>;
@@ -419,49 +419,38 @@ __global__ void __launch_bounds__(kThreads, 3)
             // The race over packs start, start + stride, ... of the row; `skip` is a token that has no part in it.
             auto race = [&](auto subtract, auto whole_packs, int start, int stride, int skip, bool ends) {
                 constexpr bool kMinus = decltype(subtract)::value, kWide = decltype(whole_packs)::value;
-                constexpr int U = 2;
-                for (int i = s.inside + start; i < s.end; i += U * stride) {
-                    uint4 packed[U];
-                    float u[U][N], e[U][N];
-#pragma unroll
-                    for (int h = 0; h < U; ++h) {
-                        const int pack = min(i + h * stride, s.end - 1), j = s.element(pack);  // past the end: the last again
-                        packed[h] = s.load(pack);
-                        if constexpr (kWide) {
-                            if constexpr (kMinus)
-                                load_beside(u[h], q, j);
-                            load_beside(e[h], noise, j);
-                        } else {
-                            if constexpr (kMinus)
-                                load_window(u[h], q, j, vocab);
-                            load_window(e[h], noise, j, vocab);
-                        }
+                for (int i = s.inside + start; i < s.end; i += stride) {
+                    const int j = s.element(i);
+                    const uint4 packed = s.load(i);
+                    uint64_t t[kPairs<T>];
+                    float u[N], e[N], sc[N], top = 0.0f;
+                    if constexpr (kWide) {
+                        if constexpr (kMinus)
+                            load_beside(u, q, j);
+                        load_beside(e, noise, j);
+                    } else {
+                        if constexpr (kMinus)
+                            load_window(u, q, j, vocab);
+                        load_window(e, noise, j, vocab);
                     }
+                    unpack_pairs<T>(packed, t);
 #pragma unroll
-                    for (int h = 0; h < U; ++h) {
-                        const int j = s.element(min(i + h * stride, s.end - 1));
-                        uint64_t t[kPairs<T>];
-                        float sc[N], top = 0.0f;
-                        unpack_pairs<T>(packed[h], t);
-#pragma unroll
-                        for (int k = 0; k < kPairs<T>; ++k) {
-                            const float2 x = score2(subtract, t[k], kMinus ? pair(u[h][2 * k], u[h][2 * k + 1]) : 0,
-                                                    make_float2(e[h][2 * k], e[h][2 * k + 1]));
-                            sc[2 * k] = x.x, sc[2 * k + 1] = x.y;
-                        }
-                        if (static_cast<unsigned>(skip - j) < N)
-#pragma unroll
-                            for (int k = 0; k < N; ++k)
-                                sc[k] = j + k == skip ? 0.0f : sc[k];
+                    for (int k = 0; k < kPairs<T>; ++k) {
+                        const float2 x = score2(subtract, t[k], kMinus ? pair(u[2 * k], u[2 * k + 1]) : 0, make_float2(e[2 * k], e[2 * k + 1]));
+                        sc[2 * k] = x.x, sc[2 * k + 1] = x.y;
+                    }
+                    if (static_cast<unsigned>(skip - j) < N)
 #pragma unroll
                         for (int k = 0; k < N; ++k)
-                            top = fmaxf(top, sc[k]);
-                        if (top > best && top > 0.0f) {  // of equals the lower token: later packs are higher
-                            best = top;
+                            sc[k] = j + k == skip ? 0.0f : sc[k];
 #pragma unroll
-                            for (int k = N - 1; k >= 0; --k)
-                                at = sc[k] == top ? j + k : at;
-                        }
+                    for (int k = 0; k < N; ++k)
+                        top = fmaxf(top, sc[k]);
+                    if (top > best && top > 0.0f) {  // of equals the lower token: later packs are higher
+                        best = top;
+#pragma unroll
+                        for (int k = N - 1; k >= 0; --k)
+                            at = sc[k] == top ? j + k : at;
                     }
                 }
                 // The ends' elements, a lane each.
