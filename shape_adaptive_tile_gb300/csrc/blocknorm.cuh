@@ -665,19 +665,21 @@ cudaError_t launch_ring(const rowop_block_norm_args& a, cudaStream_t s)
 template <typename B, typename S, bool kPack, bool kLayer>
 cudaError_t choose_forward_as(const rowop_block_norm_args& a, cudaStream_t s)
 {
-    // Up to four rows an SM there is little to fetch ahead: a CTA a row, as many threads as it has groups.
-    const bool few = a.rows < 4 * kSMs;
+    // Up to eight rows an SM, and rows of up to 1024 columns: a CTA a row and as many threads as it has groups (us for
+    // bf16, a CTA a row | the ring: 608 x 4096 6.5 | 7.4, 1216 x 4096 15.2 | 13.6, 4864 x 4096 50 | 32, 4864 x 8192 66 |
+    // 60, 4864 x 1024 13.1 | 15.1). Beyond, four groups a thread, so that a row's fixed work (the reductions, its
+    // addresses) is spread over 32 columns. Past 8192 columns the ring has room for one row at a time beside the
+    // weights and gains nothing (4864 x 16384: 171 | 181).
+    const bool few = a.rows < 8 * kSMs;
     if (a.width <= 256)
         return launch_forward<B, S, 32, 1, kPack, kLayer>(a, s);
     if (a.width <= 1024)
-        return few ? launch_forward<B, S, 128, 1, kPack, kLayer>(a, s) : launch_forward<B, S, 32, 4, kPack, kLayer>(a, s);
-    // Else four groups of columns a thread, so that a row's fixed work (the
-    // reductions, its addresses) is spread over 32 of them.
+        return launch_forward<B, S, 128, 1, kPack, kLayer>(a, s);
     if (a.width <= 4096)
         return few ? launch_forward<B, S, 512, 1, kPack, kLayer>(a, s) : launch_ring<B, S, 128, 4, kPack, kLayer>(a, s);
     if (a.width <= 8192)
         return few ? launch_forward<B, S, 512, 2, kPack, kLayer>(a, s) : launch_ring<B, S, 256, 4, kPack, kLayer>(a, s);
-    return few ? launch_forward<B, S, 512, 4, kPack, kLayer>(a, s) : launch_ring<B, S, 512, 4, kPack, kLayer>(a, s);
+    return launch_forward<B, S, 512, 4, kPack, kLayer>(a, s);
 }
 
 template <typename B, typename S, bool kPack>

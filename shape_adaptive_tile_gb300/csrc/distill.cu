@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---- many rows: a CTA a row -----------------------------------------------------
 
-constexpr int64_t kFullRows = 2 * 152, kShortRow = 16384;
+constexpr int64_t kSMs = 152;
 
 // The factors of a gradient: of logit v it is share 2^((v times - from) power),
 // less the teacher's part.
@@ -537,23 +537,41 @@ int check(const rowop_distill_args* a, bool forward)
     return GEMM_OK;
 }
 
+template <typename T, int MODE, int NT>
+cudaError_t launch_rows_by(const rowop_distill_args& a, cudaStream_t s)
+{
+    sat_distill_row_kernel<T, MODE, NT><<<static_cast<unsigned>(a.rows), NT, Entries::room(static_cast<int>(a.k)), s>>>(a);
+    return cudaGetLastError();
+}
+
+// The threads of a row's CTA, and with them the rows at hand in an SM (1024 /
+// NT): more of these overlap better, but with a gradient all rows at hand have to
+// stay in L2 for their second pass. (us for 128 | 256 | 512 | 1024 threads,
+// 1500 rows with gradient in 16-bit types: 24576 tokens 38 | 43 | 55 | 104, 49152
+// 79 | 62 | 78 | 117, 131072 202 | 180 | 160 | 186; 700 x 262144 179 | 199 | 173
+// | 164. Loss: 1500 x 32768 23 | 25 | 32 | 64, 131072 72 | 67 | 70 | 89.)
+template <typename T, int MODE>
+cudaError_t launch_rows(const rowop_distill_args& a, int64_t row, cudaStream_t s)
+{
+    if (row <= (MODE == kLoss ? 131072 : 49152))
+        return launch_rows_by<T, MODE, 128>(a, s);
+    if (MODE == kLoss || row <= 131072)
+        return launch_rows_by<T, MODE, 256>(a, s);
+    if constexpr (MODE == kBoth)
+        return row <= 393216 ? launch_rows_by<T, MODE, 512>(a, s) : launch_rows_by<T, MODE, 1024>(a, s);
+    return cudaErrorInvalidValue;
+}
+
 template <typename T, int MODE>
 cudaError_t launch(const rowop_distill_args& a, cudaStream_t s)
 {
     if constexpr (MODE != kGrad) {
-        // Rows enough for two CTAs an SM: one a row. (Slices of a row each find the others' softmaxes only by
-        // waiting.) Short rows, whose fixed work counts, are eight at hand in an SM; of long ones the loss alone
-        // does best with four and the gradient with two, whose second passes find more of their rows in L2.
-        if (a.rows >= kFullRows) {
-            constexpr int NT = MODE == kLoss ? 256 : 512;
-            const unsigned grid = static_cast<unsigned>(a.rows);
-            const int smem = Entries::room(static_cast<int>(a.k));
-            if (a.vocab <= kShortRow)
-                sat_distill_row_kernel<T, MODE, 128><<<grid, 128, smem, s>>>(a);
-            else
-                sat_distill_row_kernel<T, MODE, NT><<<grid, NT, smem, s>>>(a);
-            return cudaGetLastError();
-        }
+        // A CTA a row, or a row's slices in a cluster: a row by itself where there are rows for half of the SMs, or
+        // where it is short. (us, row | slices, 16-bit types: 76 x 32000 with gradient 9.1 | 10.2, 8 x 131072 15.7 |
+        // 8.9, 76 x 131072 18.3 | 17.9; loss 8 x 32000 5.0 | 6.6, 38 x 131072 8.6 | 7.8, 304 x 131072 17.9 | 32.3.)
+        const int64_t row = a.vocab * static_cast<int64_t>(sizeof(T));
+        if (a.rows >= kSMs / 2 || row <= (MODE == kLoss ? 65536 : 32768))
+            return launch_rows<T, MODE>(a, row, s);
     }
     // With what a row may need before its start to reach a 16-byte boundary.
     const bool even = aligned(a.logits, 16) && a.ldl * sizeof(T) % 16 == 0;
