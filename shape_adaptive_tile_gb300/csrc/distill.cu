@@ -206,6 +206,10 @@ __global__ void __launch_bounds__(kThreads)
             out[j] = from_f32<T>(0.0f);
     };
 
+    // A thread's first entry, on its way with the weight.
+    const bool entry = (MODE != kLoss || rank == 0) && threadIdx.x < k;
+    const int token0 = entry ? a.ids[r * a.ldi + threadIdx.x] : -1;
+    const float logit0 = entry ? teacher_logit(a, r * a.ldt + threadIdx.x) : 0.0f;
     if (weight == 0.0f) {  // alike for all CTAs of the cluster
         if (MODE != kGrad && rank == 0 && threadIdx.x == 0) {
             a.loss[r] = 0.0f;
@@ -238,8 +242,9 @@ __global__ void __launch_bounds__(kThreads)
         if (threadIdx.x < teacher.padded - k)
             id[k + threadIdx.x] = -2;
         for (int i = threadIdx.x; i < k; i += kThreads) {
-            const int token = a.ids[r * a.ldi + i];
-            const float v = teacher_logit(a, r * a.ldt + i);
+            const bool held = i == static_cast<int>(threadIdx.x);
+            const int token = held ? token0 : a.ids[r * a.ldi + i];
+            const float v = held ? logit0 : teacher_logit(a, r * a.ldt + i);
             const bool there = token >= 0 && token < a.vocab && v != -INFINITY;
             id[i] = there ? token : -1;
             log_p[i] = v;
