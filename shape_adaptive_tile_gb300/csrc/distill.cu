@@ -386,6 +386,16 @@ __device__ __forceinline__ uint4 gradient_of(const uint4& w, const Gradient& f)
     return pack16<T>(o);
 }
 
+// Sixteen bytes by a load that tells L2 how long to keep them.
+__device__ __forceinline__ uint4 load_hinted(const void* p, uint64_t policy)
+{
+    uint4 v;
+    asm volatile("ld.global.L2::cache_hint.v4.b32 {%0, %1, %2, %3}, [%4], %5;"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p), "l"(policy));
+    return v;
+}
+
 template <typename T, int MODE, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) sat_distill_row_kernel(const __grid_constant__ rowop_distill_args a)
 {
@@ -403,24 +413,29 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sat_distill_row_kernel(const __
     T* out = a.dlogits ? static_cast<T*>(a.dlogits) + r * a.ldd : nullptr;
     int turn = 0;
 
-    // f(packs, first) for the row's packs in batches of U a thread, all of a batch's loads first; packs past the end are -inf.
-    auto batches = [&](auto f) {
+    // f(packs, first, all) for the row's packs in batches of U a thread, all of a batch's loads first; packs past the end are -inf.
+    auto batches = [&](uint64_t policy, auto f) {
+        auto load = [&](int j) { return load_hinted(s.row + s.element(j), policy); };
         int j = s.inside + threadIdx.x;
         for (; j - static_cast<int>(threadIdx.x) + U * NT <= s.end; j += U * NT) {
             uint4 w[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                w[u] = s.load(j + u * NT);
+                w[u] = load(j + u * NT);
             f(w, j, true);
         }
         if (j < s.end) {
             uint4 w[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                w[u] = j + u * NT < s.end ? s.load(j + u * NT) : nothing<T>();
+                w[u] = j + u * NT < s.end ? load(j + u * NT) : nothing<T>();
             f(w, j, false);
         }
     };
+    // The first pass's lines are to stay in L2 for the second, after which they are of no more use.
+    uint64_t keep, drop;
+    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(drop));
     // The column of the element at the row's ends, outside whole packs, that this lane of the last warp sees to.
     const int end_column = warp < W - 1 || lane >= 2 * N ? -1
                            : lane < N                            ? (s.inside ? lane - s.shift : -1)
@@ -463,7 +478,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sat_distill_row_kernel(const __
     const float top = a.teacher_lse ? 0.0f : t.max, rest = a.teacher_lse ? a.teacher_lse[r] : logf(t.sum);
 
     Softmax q = Softmax::none();
-    batches([&](const uint4(&w)[U], int, bool) { q.add(softmax_of<T>(w, scale), scale); });
+    batches(MODE == kBoth ? keep : drop, [&](const uint4(&w)[U], int, bool) { q.add(softmax_of<T>(w, scale), scale); });
     if (at_end)
         q.add(to_f32(s.row[end_column]), scale);
     __syncwarp();
@@ -488,7 +503,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sat_distill_row_kernel(const __
     const float c = (a.dloss ? a.dloss[r] : 1.0f) * weight * a.temperature;
     const Gradient f = {c * sum[0] / q.sum, 1.0f, q.max, scale};
     if (((reinterpret_cast<uint64_t>(out) ^ reinterpret_cast<uint64_t>(s.row)) & 15) == 0) {
-        batches([&](const uint4(&w)[U], int j, bool all) {
+        batches(drop, [&](const uint4(&w)[U], int j, bool all) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (all || j + u * NT < s.end)
