@@ -388,6 +388,32 @@ __device__ __forceinline__ void ring_sums(float (&v)[N], float* scratch, int& tu
         v[i] = __shfl_sync(0xffffffffu, s, i);
 }
 
+// Sums of K values over a cluster's CTAs, in order of rank: each sends its own
+// to all, counted on a barrier there. `turn` counts the exchanges; `across` and
+// `arrived` of the exchange before are still in use.
+template <int K, int MAX>
+__device__ __forceinline__ void cluster_sums(float (&v)[K], float (&across)[2][MAX][8], uint64_t (&arrived)[2], int thread, int rank,
+                                             int ctas, int& turn, bool& failed)
+{
+    const int b = turn & 1;
+    if (thread == 0)
+        mbar_arrive_expect_tx(smem_u32(&arrived[b]), ctas * ((K + 1) / 2) * 8);
+    if (thread < ctas) {
+        const uint32_t bar = map_to_cta(smem_u32(&arrived[b]), thread), to = map_to_cta(smem_u32(&across[b][rank][0]), thread);
+#pragma unroll
+        for (int k = 0; k < K; k += 2)
+            send_b64(to + 4 * k, pair(v[k], k + 1 < K ? v[k + 1] : 0.0f), bar);
+    }
+    Ring::wait(&arrived[b], turn >> 1 & 1, failed);
+    ++turn;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        v[k] = 0.0f;
+        for (int c = 0; c < ctas; ++c)
+            v[k] += across[b][c][k];
+    }
+}
+
 // ---- forward -----------------------------------------------------------------------
 
 enum Weight { kPreGammaW, kPostGammaW, kGateW, kPreBetaW, kPostBetaW, kWeights };
@@ -402,15 +428,16 @@ __device__ __forceinline__ const float* weight_vector(const rowop_block_norm_arg
                               : nullptr;
 }
 
-// Mean and reciprocal deviation of a row held as NV groups a thread. The
+// Mean and reciprocal deviation of a row of `whole` columns, of which NT
+// threads hold `width` as NV groups each and `sums` adds up all. The
 // variance is summed from the deviations, after the mean: the difference of
 // two large sums would lose what rows far from 0 have of it. Without a Layer
 // norm the mean is 0, and columns past the row's end hold 0 and add nothing.
 template <bool kLayer, bool kPack, int NT, int NV, typename Sums>
-__device__ __forceinline__ void moments(const Group (&v)[NV], int width, int kind, float eps, int lane, Sums sums, float& mean,
-                                        float& r)
+__device__ __forceinline__ void moments(const Group (&v)[NV], int whole, int width, int kind, float eps, int lane, Sums sums,
+                                        float& mean, float& r)
 {
-    const float inv = 1.0f / static_cast<float>(width);
+    const float inv = 1.0f / static_cast<float>(whole);
     mean = 0.0f;
     uint64_t q = 0;
     if (kLayer && kind == ROWOP_NORM_LAYER) {
@@ -466,22 +493,22 @@ __device__ __forceinline__ void apply(Group& v, float mean, float r, WeightAt we
 
 // What follows a row's read: v is y's share, x(i) gives x's groups, weight(w,
 // i) a weight's; writes h, z and the statistics. `lane` is the thread's place
-// among the NT of its row.
+// among the NT that hold columns off .. off + width - 1 of the row.
 template <typename B, typename S, int NT, int NV, bool kPack, bool kLayer, typename X, typename WeightAt, typename Sums>
-__device__ __forceinline__ void finish_row(const rowop_block_norm_args& a, int64_t r, Group (&v)[NV], int lane, X x, WeightAt weight,
-                                           Sums sums)
+__device__ __forceinline__ void finish_row(const rowop_block_norm_args& a, int64_t r, Group (&v)[NV], int lane, int off, int width,
+                                           X x, WeightAt weight, Sums sums)
 {
-    const int width = static_cast<int>(a.width);
+    const int whole = static_cast<int>(a.width);
     float mean, rs;
     if (a.post_norm != ROWOP_NORM_NONE) {
-        moments<kLayer, kPack, NT, NV>(v, width, a.post_norm, a.post_eps, lane, sums, mean, rs);
-        if (a.post_stats && lane == 0)
+        moments<kLayer, kPack, NT, NV>(v, whole, width, a.post_norm, a.post_eps, lane, sums, mean, rs);
+        if (a.post_stats && lane == 0 && off == 0)
             a.post_stats[2 * r] = mean, a.post_stats[2 * r + 1] = rs;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             apply<kLayer>(v[i], mean, rs, weight, kPostGammaW, kPostBetaW, i);
     }
-    S* h = static_cast<S*>(a.h) + r * a.ldh;
+    S* h = static_cast<S*>(a.h) + r * a.ldh + off;
     const uint64_t residual = both(a.residual_scale), branch = both(a.branch_scale);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -501,10 +528,10 @@ __device__ __forceinline__ void finish_row(const rowop_block_norm_args& a, int64
     }
     if (a.pre_norm == ROWOP_NORM_NONE)
         return;
-    moments<kLayer, kPack, NT, NV>(v, width, a.pre_norm, a.pre_eps, lane, sums, mean, rs);
-    if (a.pre_stats && lane == 0)
+    moments<kLayer, kPack, NT, NV>(v, whole, width, a.pre_norm, a.pre_eps, lane, sums, mean, rs);
+    if (a.pre_stats && lane == 0 && off == 0)
         a.pre_stats[2 * r] = mean, a.pre_stats[2 * r + 1] = rs;
-    B* z = static_cast<B*>(a.z) + r * a.ldz;
+    B* z = static_cast<B*>(a.z) + r * a.ldz + off;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         apply<kLayer>(v[i], mean, rs, weight, kPreGammaW, kPreBetaW, i);
@@ -544,7 +571,7 @@ __global__ void __launch_bounds__(NT == 32 ? 128 : NT) sat_block_norm_kernel(con
                 early[w] = read(w, 0);
         }
         finish_row<B, S, NT, NV, kPack, kLayer>(
-            a, r, v, lane, [&](int i) { return u[i]; },
+            a, r, v, lane, 0, width, [&](int i) { return u[i]; },
             [&](int w, int i) {
                 if constexpr (kEarly)
                     return early[w];
@@ -559,7 +586,8 @@ __global__ void __launch_bounds__(NT == 32 ? 128 : NT) sat_block_norm_kernel(con
 // at a time and share a ring of `stages` stages of `stage_bytes` and, behind it
 // (`kept`), the weights. So several rows are at hand in an SM at once, one
 // group's reductions beside another's arithmetic, with one copy of the weights.
-template <typename B, typename S, int NT, int NV, bool kPack, bool kLayer>
+// Rows past 8192 columns have a pair of CTAs (C = 2), half of the columns each.
+template <typename B, typename S, int NT, int NV, int C, bool kPack, bool kLayer>
 __global__ void __launch_bounds__(512 + 32, 1)
     sat_block_norm_ring_kernel(const __grid_constant__ rowop_block_norm_args a, int stages, int stage_bytes, bool kept)
 {
@@ -567,12 +595,15 @@ __global__ void __launch_bounds__(512 + 32, 1)
     extern __shared__ __align__(128) unsigned char ring_memory[];
     __shared__ __align__(8) Ring ring;
     __shared__ float scratch[G][2 * (NT / 32)];
-    const int width = static_cast<int>(a.width);
-    const int y_bytes = (width * static_cast<int>(sizeof(B)) + 31) / 16 * 16;
-    const Source sources[2] = {
-        {static_cast<const char*>(a.y), a.ldy * static_cast<int64_t>(sizeof(B)), width * static_cast<int>(sizeof(B)), 0},
-        {static_cast<const char*>(a.x), a.ldx * static_cast<int64_t>(sizeof(S)), width * static_cast<int>(sizeof(S)), y_bytes}};
+    __shared__ __align__(8) uint64_t arrived[G][2];
+    __shared__ __align__(8) float across[G][2][2][8];
     constexpr int room = NT * NV * 8;
+    const int rank = blockIdx.x % C, off = rank * room, width = min(static_cast<int>(a.width) - off, room);
+    const int y_bytes = (min(static_cast<int>(a.width), room) * static_cast<int>(sizeof(B)) + 31) / 16 * 16;
+    const Source sources[2] = {{reinterpret_cast<const char*>(static_cast<const B*>(a.y) + off), a.ldy * static_cast<int64_t>(sizeof(B)),
+                                width * static_cast<int>(sizeof(B)), 0},
+                               {reinterpret_cast<const char*>(static_cast<const S*>(a.x) + off), a.ldx * static_cast<int64_t>(sizeof(S)),
+                                width * static_cast<int>(sizeof(S)), y_bytes}};
     float* weights = reinterpret_cast<float*>(ring_memory + stages * stage_bytes);
     const bool shared_gate = a.gate && a.rows_per_gate >= a.rows;
     // Kept weights lie one after another in the order of Weight, those that the call does not have left out.
@@ -583,18 +614,26 @@ __global__ void __launch_bounds__(512 + 32, 1)
         const bool there = kept && (w == kGateW ? shared_gate : weight_vector(a, w) != nullptr);
         at[w] = there ? weights + n * room : nullptr;
         if (there && w == kGateW && a.gate_type != GEMM_C_F32)
-            keep_weights(weights + n * room, static_cast<const B*>(a.gate), 1.0f, width, room);
+            keep_weights(weights + n * room, static_cast<const B*>(a.gate) + off, 1.0f, width, room);
         else if (there)
-            keep_weights(weights + n * room, w == kGateW ? static_cast<const float*>(a.gate) : weight_vector(a, w), 1.0f, width, room);
+            keep_weights(weights + n * room, (w == kGateW ? static_cast<const float*>(a.gate) : weight_vector(a, w)) + off, 1.0f, width, room);
         n += there;
     }
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < G; ++i) {
+            mbar_init(smem_u32(&arrived[i][0]), 1);
+            mbar_init(smem_u32(&arrived[i][1]), 1);
+        }
         ring.init(stages, NT / 32);
+    }
     __syncthreads();
+    if (C > 1)
+        cluster_sync();  // both have started and have their barriers
+    const int64_t pair_of = blockIdx.x / C, pairs = gridDim.x / C;
     bool failed = false;
     int s = 0, round = 0, turn = 0;
     if (threadIdx.x >= 512) {
-        for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        for (int64_t r = pair_of; r < a.rows; r += pairs) {
             ring.fill<kPack>(ring_memory + s * stage_bytes, s, round, sources, r, failed);
             if (++s == stages)
                 s = 0, ++round;
@@ -603,7 +642,8 @@ __global__ void __launch_bounds__(512 + 32, 1)
     }
     const int group = threadIdx.x / NT, lane = threadIdx.x % NT;
     s = group;
-    for (int64_t r = blockIdx.x + group * static_cast<int64_t>(gridDim.x); r < a.rows; r += G * static_cast<int64_t>(gridDim.x), s += G) {
+    int swaps = 0;
+    for (int64_t r = pair_of + group * pairs; r < a.rows; r += G * pairs, s += G) {
         for (; s >= stages; s -= stages)
             ++round;
         ring.take(s, round, failed);
@@ -615,7 +655,7 @@ __global__ void __launch_bounds__(512 + 32, 1)
         if (failed)
             v[0] = fill(NAN);
         finish_row<B, S, NT, NV, kPack, kLayer>(
-            a, r, v, lane,
+            a, r, v, lane, off, width,
             [&](int i) {
                 const Group u = stage_group<kPack, NT, S>(stage, sources[1], r, lane, i, width);
                 if (i == NV - 1)
@@ -626,10 +666,18 @@ __global__ void __launch_bounds__(512 + 32, 1)
                 if (at[w])
                     return kept_group<kPack, NT>(at[w], lane, i);
                 if (w == kGateW)
-                    return gate_group<kPack, NT, B>(a, gate_row(a, r), lane, i, 0, width);
-                return load_weights<kPack, NT>(weight_vector(a, w), w >= kPreBetaW ? 0.0f : 1.0f, lane, i, width);
+                    return gate_group<kPack, NT, B>(a, gate_row(a, r), lane, i, off, width);
+                const float* vector = weight_vector(a, w);
+                return load_weights<kPack, NT>(vector ? vector + off : nullptr, w >= kPreBetaW ? 0.0f : 1.0f, lane, i, width);
             },
-            [&](float(&v)[1]) { ring_sums<NT>(v, scratch[group], turn, group); });
+            [&](float(&v)[1]) {
+                ring_sums<NT>(v, scratch[group], turn, group);
+                if constexpr (C > 1) {
+                    cluster_sums(v, across[group], arrived[group], lane, rank, C, swaps, failed);
+                    if (failed)
+                        v[0] = NAN;
+                }
+            });
     }
 }
 
@@ -642,10 +690,10 @@ cudaError_t launch_forward(const rowop_block_norm_args& a, cudaStream_t s)
     return cudaGetLastError();
 }
 
-template <typename B, typename S, int NT, int NV, bool kPack, bool kLayer>
+template <typename B, typename S, int NT, int NV, int C, bool kPack, bool kLayer>
 cudaError_t launch_ring(const rowop_block_norm_args& a, cudaStream_t s)
 {
-    const int64_t w = a.width;
+    const int64_t w = a.width < NT * NV * 8 ? a.width : NT * NV * 8;
     const int stage = static_cast<int>((w * sizeof(B) + 31) / 16 * 16 + (w * sizeof(S) + 31) / 16 * 16);
     constexpr int room = kSmemPerSM - 2048, groups = 512 / NT;
     const bool post = a.post_norm != ROWOP_NORM_NONE, pre = a.pre_norm != ROWOP_NORM_NONE;
@@ -656,15 +704,25 @@ cudaError_t launch_ring(const rowop_block_norm_args& a, cudaStream_t s)
     const bool kept = room - weights >= (groups + 1) * stage;
     int stages = (kept ? room - weights : room) / stage;
     stages = stages < kMaxStages ? stages : kMaxStages;
-    auto kernel = sat_block_norm_ring_kernel<B, S, NT, NV, kPack, kLayer>;
+    if (stages < 1)
+        return cudaErrorInvalidConfiguration;
+    auto kernel = sat_block_norm_ring_kernel<B, S, NT, NV, C, kPack, kLayer>;
     static Prepared prepared;
     const cudaError_t e = prepared.once(reinterpret_cast<const void*>(kernel), room);
     if (e != cudaSuccess)
         return e;
-    if (stages < 1)
-        return cudaErrorInvalidConfiguration;
-    kernel<<<static_cast<unsigned>(kSMs), 512 + 32, stages * stage + (kept ? weights : 0), s>>>(a, stages, stage, kept);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(kSMs / C * C));
+    cfg.blockDim = dim3(512 + 32);
+    cfg.dynamicSmemBytes = stages * stage + (kept ? weights : 0);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = C > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, a, stages, stage, kept);
 }
 
 template <typename B, typename S, bool kPack, bool kLayer>
@@ -681,10 +739,10 @@ cudaError_t choose_forward_as(const rowop_block_norm_args& a, cudaStream_t s)
     if (a.width <= 1024)
         return launch_forward<B, S, 128, 1, kPack, kLayer>(a, s);
     if (a.width <= 4096)
-        return few ? launch_forward<B, S, 512, 1, kPack, kLayer>(a, s) : launch_ring<B, S, 128, 4, kPack, kLayer>(a, s);
+        return few ? launch_forward<B, S, 512, 1, kPack, kLayer>(a, s) : launch_ring<B, S, 128, 4, 1, kPack, kLayer>(a, s);
     if (a.width <= 8192)
-        return few ? launch_forward<B, S, 512, 2, kPack, kLayer>(a, s) : launch_ring<B, S, 256, 4, kPack, kLayer>(a, s);
-    return launch_forward<B, S, 512, 4, kPack, kLayer>(a, s);
+        return few ? launch_forward<B, S, 512, 2, kPack, kLayer>(a, s) : launch_ring<B, S, 256, 4, 1, kPack, kLayer>(a, s);
+    return few ? launch_forward<B, S, 512, 4, kPack, kLayer>(a, s) : launch_ring<B, S, 256, 4, 2, kPack, kLayer>(a, s);
 }
 
 template <typename B, typename S, bool kPack>
@@ -1072,7 +1130,6 @@ __global__ void __launch_bounds__(NT, kBackwardPerSM<NT>)
                 keep_group<kPack, NT>(weights + 2 * room, gate_group<kPack, NT, B>(a, k, lane, 0, off, width), lane);
         },
         [&](auto& v) {
-            constexpr int K = sizeof(v) / sizeof(v[0]);
             if (!kPack && threadIdx.x < 64)
                 fence_proxy_async_smem();  // of the ends written before: what follows them there comes by bulk copies
             ring_sums<NT>(v, scratch, turn, 0);
@@ -1083,26 +1140,8 @@ __global__ void __launch_bounds__(NT, kBackwardPerSM<NT>)
                 if (!kPack && threadIdx.x < 64)
                     put_end(before, place, x, held);
             }
-            if (ctas > 1) {
-                const int b = swaps & 1;
-                if (threadIdx.x == 0)
-                    mbar_arrive_expect_tx(smem_u32(&arrived[b]), ctas * ((K + 1) / 2) * 8);
-                if (threadIdx.x < ctas) {
-                    const uint32_t bar = map_to_cta(smem_u32(&arrived[b]), threadIdx.x);
-                    const uint32_t to = map_to_cta(smem_u32(&across[b][rank][0]), threadIdx.x);
-#pragma unroll
-                    for (int k = 0; k < K; k += 2)
-                        send_b64(to + 4 * k, pair(v[k], k + 1 < K ? v[k + 1] : 0.0f), bar);
-                }
-                Ring::wait(&arrived[b], swaps >> 1 & 1, failed);
-                ++swaps;
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    v[k] = 0.0f;
-                    for (int c = 0; c < ctas; ++c)
-                        v[k] += across[b][c][k];
-                }
-            }
+            if (ctas > 1)
+                cluster_sums(v, across, arrived, threadIdx.x, rank, ctas, swaps, failed);
             if (failed)
                 v[0] = NAN;
         },
