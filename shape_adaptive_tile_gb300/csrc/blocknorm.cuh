@@ -13,7 +13,7 @@
 //
 // Measured on a GB300, of its copy rate of 6.8 TB/s: forward 8192 x 8192 bf16
 // 88 us (6.07 TB/s, 89%); 2049 x 5001 fp32, whose rows move four bytes at a
-// time, 37 us (65%); backward 16384 x 4096 bf16 on an fp32 stream 206 us (5.87
+// time, 35.5 us (68%); backward 16384 x 4096 bf16 on an fp32 stream 206 us (5.87
 // TB/s, 86%); 4593 x 1537 fp16 with Layer norms, whose elements move by
 // themselves, 71 us (18%: the instructions bound it, 824 for a warp's 256 elements).
 #pragma once
@@ -728,21 +728,32 @@ cudaError_t launch_ring(const rowop_block_norm_args& a, cudaStream_t s)
 template <typename B, typename S, bool kPack, bool kLayer>
 cudaError_t choose_forward_as(const rowop_block_norm_args& a, cudaStream_t s)
 {
-    // Up to eight rows an SM, and rows of up to 1024 columns: a CTA a row and as many threads as it has groups (us for
-    // bf16, a CTA a row | the ring: 608 x 4096 6.5 | 7.4, 1216 x 4096 15.2 | 13.6, 4864 x 4096 50 | 32, 4864 x 8192 66 |
-    // 60, 4864 x 1024 13.1 | 15.1). Beyond, four groups a thread, so that a row's fixed work (the reductions, its
-    // addresses) is spread over 32 columns. Past 8192 columns the ring has room for one row at a time beside the
-    // weights and gains nothing (4864 x 16384: 171 | 181).
-    const bool few = a.rows < 8 * kSMs;
+    // Few rows, and rows of up to 1024 columns: a CTA a row and as many threads as it has groups. Beyond, two to four
+    // groups a thread, so that a row's fixed work (the reductions, its addresses) is spread over up to 32 columns. Few
+    // are up to four rows an SM, or eight between 2048 and 8192 columns, where a CTA's threads hold a row with room for
+    // a second. (us for bf16, a CTA a row | the ring: 304 x 2048 4.0 | 5.1, 608 x 2048 6.5 | 6.1, 4864 x 2048 43 | 21;
+    // 608 x 4096 6.5 | 7.4, 1216 x 4096 15.2 | 13.6; 912 x 8192 17.9 | 19.3, 1216 x 8192 21.9 | 22.3, 4864 x 8192 66 |
+    // 59; 304 x 16384 18.3 | 17.5, 608 x 16384 31 | 24, 4864 x 16384 170 | 120; 4864 x 1024 13.1 | 15.1.)
+    const bool few = a.rows < (a.width > 2048 && a.width <= 8192 ? 8 : 4) * kSMs;
     if (a.width <= 256)
         return launch_forward<B, S, 32, 1, kPack, kLayer>(a, s);
     if (a.width <= 1024)
         return launch_forward<B, S, 128, 1, kPack, kLayer>(a, s);
+    if (few)
+        return a.width <= 4096   ? launch_forward<B, S, 512, 1, kPack, kLayer>(a, s)
+               : a.width <= 8192 ? launch_forward<B, S, 512, 2, kPack, kLayer>(a, s)
+                                 : launch_forward<B, S, 512, 4, kPack, kLayer>(a, s);
+    if (a.width <= 2048)
+        return launch_ring<B, S, 128, 2, 1, kPack, kLayer>(a, s);
     if (a.width <= 4096)
-        return few ? launch_forward<B, S, 512, 1, kPack, kLayer>(a, s) : launch_ring<B, S, 128, 4, 1, kPack, kLayer>(a, s);
+        return launch_ring<B, S, 128, 4, 1, kPack, kLayer>(a, s);
+    if (a.width <= 6144)
+        return launch_ring<B, S, 256, 3, 1, kPack, kLayer>(a, s);
     if (a.width <= 8192)
-        return few ? launch_forward<B, S, 512, 2, kPack, kLayer>(a, s) : launch_ring<B, S, 256, 4, 1, kPack, kLayer>(a, s);
-    return few ? launch_forward<B, S, 512, 4, kPack, kLayer>(a, s) : launch_ring<B, S, 256, 4, 2, kPack, kLayer>(a, s);
+        return launch_ring<B, S, 256, 4, 1, kPack, kLayer>(a, s);
+    if (a.width <= 12288)
+        return launch_ring<B, S, 256, 3, 2, kPack, kLayer>(a, s);
+    return launch_ring<B, S, 256, 4, 2, kPack, kLayer>(a, s);
 }
 
 template <typename B, typename S, bool kPack>

@@ -206,7 +206,7 @@ def test_many_rows_share_parts_and_gates(rows, rows_per_gate, width):
 @pytest.mark.parametrize("width,pad", [(700, 0), (1032, 8), (1537, 0), (4096, 0), (5001, 3), (8192, 0), (12290, 1), (16384, 0)])
 @pytest.mark.parametrize("block,stream_type", [("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp32")])
 def test_many_rows_through_the_ring(width, pad, block, stream_type):
-    # More rows than eight an SM: CTAs that stay for several, with the weights kept on chip, or (the widest) not.
+    # More rows than eight an SM: CTAs, or pairs of them, that stay for several, with the weights kept on chip or not.
     i = width % 3
     c = Case(width, 1219, width, block, stream_type, KINDS[i], KINDS[1 + i % 2], [0, 1219, 40][i], pad=pad, residual_scale=1.25)
     c.forward()
