@@ -227,18 +227,28 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, uint64_t src, uint32_t b
                  : "memory");
 }
 
+// Groups of threads that may share a ring.
+constexpr int kMaxGroups = 4;
+
 // A ring of `stages` stages, each with a row of every source: filled by one
 // warp (Ring::fill), read by `warps` others (Ring::take, Ring::release). Bulk
 // copies move what lies between 16-byte boundaries of memory; where rows do
 // not start on them (not kPack), a row lies in its stage as many bytes after
 // a boundary as in memory, and the warp moves its ends by plain loads.
+//
+// Where groups of threads take the rows in turn, a stage is now one group's
+// and now another's (unless the stages are a multiple of the groups). A wait
+// tells a barrier's phases apart by their parity alone, so whoever waits has to
+// see every one of them: each group has its own `full` barriers, on which only
+// its own rows are counted. The filling warp waits for all of `empty`'s phases.
 struct Ring {
-    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t full[kMaxGroups][kMaxStages], empty[kMaxStages];
 
     __device__ __forceinline__ void init(int stages, int warps)
     {
         for (int s = 0; s < stages; ++s) {
-            mbar_init(smem_u32(&full[s]), 1);
+            for (int g = 0; g < kMaxGroups; ++g)
+                mbar_init(smem_u32(&full[g][s]), 1);
             mbar_init(smem_u32(&empty[s]), warps);
         }
         fence_mbar_init();
@@ -251,9 +261,10 @@ struct Ring {
     }
 
     template <bool kPack, int N>
-    __device__ __forceinline__ void fill(unsigned char* stage, int s, int round, const Source (&sources)[N], int64_t r,
+    __device__ __forceinline__ void fill(unsigned char* stage, int s, int round, int group, const Source (&sources)[N], int64_t r,
                                          bool& failed)
     {
+        uint64_t* const bar = &full[group][s];
         const int lane = threadIdx.x % 32;
         wait(&empty[s], round & 1 ^ 1, failed);
         uint32_t total = 0;
@@ -263,11 +274,11 @@ struct Ring {
                 for (int i = 0; i < N; ++i)
                     if (sources[i].p && sources[i].bytes > 0)
                         total += sources[i].bytes;
-                mbar_arrive_expect_tx(smem_u32(&full[s]), total);
+                mbar_arrive_expect_tx(smem_u32(bar), total);
 #pragma unroll
                 for (int i = 0; i < N; ++i)
                     if (sources[i].p && sources[i].bytes > 0)
-                        bulk_load(smem_u32(stage) + sources[i].offset, sources[i].row(r), sources[i].bytes, smem_u32(&full[s]));
+                        bulk_load(smem_u32(stage) + sources[i].offset, sources[i].row(r), sources[i].bytes, smem_u32(bar));
             }
             __syncwarp();
         } else {
@@ -284,7 +295,7 @@ struct Ring {
                 total += bytes;
                 if (lane == 0 && bytes)
                     bulk_load(smem_u32(stage) + sources[i].offset + static_cast<uint32_t>(lo16 - (lo & ~15ull)), lo16, bytes,
-                              smem_u32(&full[s]));
+                              smem_u32(bar));
                 const uint64_t x = (lane < 8 ? lo & ~15ull : hi16) + lane % 8 * 2;
                 if (lane < 16 && x >= lo && x < hi && (x < lo16 || x >= hi16) && (lane < 8 || hi16 >= lo16))
                     ends[i] = *reinterpret_cast<const uint16_t*>(x);
@@ -300,11 +311,12 @@ struct Ring {
             }
             __syncwarp();
             if (lane == 0)
-                mbar_arrive_expect_tx(smem_u32(&full[s]), total);
+                mbar_arrive_expect_tx(smem_u32(bar), total);
         }
     }
 
-    __device__ __forceinline__ void take(int s, int round, bool& failed) { wait(&full[s], round & 1, failed); }
+    // Waits for the use-th row that the group has had in stage s.
+    __device__ __forceinline__ void take(int group, int s, int use, bool& failed) { wait(&full[group][s], use & 1, failed); }
 
     __device__ __forceinline__ void release(int s)
     {
@@ -633,20 +645,27 @@ __global__ void __launch_bounds__(512 + 32, 1)
     bool failed = false;
     int s = 0, round = 0, turn = 0;
     if (threadIdx.x >= 512) {
+        int filling = 0;  // the group whose row it is
         for (int64_t r = pair_of; r < a.rows; r += pairs) {
-            ring.fill<kPack>(ring_memory + s * stage_bytes, s, round, sources, r, failed);
+            ring.fill<kPack>(ring_memory + s * stage_bytes, s, round, filling, sources, r, failed);
             if (++s == stages)
                 s = 0, ++round;
+            filling = filling + 1 == G ? 0 : filling + 1;
         }
         return;
     }
     const int group = threadIdx.x / NT, lane = threadIdx.x % NT;
-    s = group;
-    int swaps = 0;
-    for (int64_t r = pair_of + group * pairs; r < a.rows; r += G * pairs, s += G) {
-        for (; s >= stages; s -= stages)
-            ++round;
-        ring.take(s, round, failed);
+    // The group's k-th row of the CTA's: k = group, group + G, ... The rows that it has in one stage are as far apart as
+    // the least number that is a multiple of both the stages and the groups.
+    int apart = stages, use = 0, swaps = 0;
+    while (apart % G)
+        apart += stages;
+    s = group % stages;
+    int k = group, next_use = apart;
+    for (int64_t r = pair_of + group * pairs; r < a.rows; r += G * pairs, k += G, s = (s + G) % stages) {
+        if (k >= next_use)
+            ++use, next_use += apart;
+        ring.take(group, s, use, failed);
         const unsigned char* stage = ring_memory + s * stage_bytes;
         Group v[NV];
 #pragma unroll
