@@ -12,8 +12,8 @@
 // the reductions that each row has between its read and its write.
 //
 // Measured on a GB300, of its copy rate of 6.8 TB/s: forward 8192 x 8192 bf16
-// 88 us (6.07 TB/s, 89%); 2049 x 5001 fp32, whose rows move four bytes at a
-// time, 35.5 us (68%); backward 16384 x 4096 bf16 on an fp32 stream 206 us (5.87
+// 87 us (6.15 TB/s, 90%); 2049 x 5001 fp32, whose rows move four bytes at a
+// time, 36 us (67%); backward 16384 x 4096 bf16 on an fp32 stream 206 us (5.87
 // TB/s, 86%); 4593 x 1537 fp16 with Layer norms, whose elements move by
 // themselves, 71 us (18%: the instructions bound it, 824 for a warp's 256 elements).
 #pragma once
