@@ -321,14 +321,16 @@ struct Softmax {
 // Sums of 2^((v - top) scale) over packs of 16 bytes, `get(i)` for i < n: for
 // each pair of elements a multiply-add, two exponentials and an addition. The
 // multiply-add subtracts top scale as rounded, and what the rounding was goes
-// into the sum as a factor at the end, so rows far from 0 lose nothing. Where
-// that product might overflow (a maximum that is the type's lowest value) the
+// into the sum as a factor at the end, so rows far from 0 lose nothing. That
+// holds while the rounding is a small part of a binade: below 2^20 it is at most
+// 2^-5. Beyond (masks of -1e9, a tiny temperature), where it may be hundreds of
+// binades, and where the product overflows (the type's lowest value), the
 // difference is taken first instead, one instruction more.
 template <typename T, typename Get>
 __device__ __forceinline__ float sum_packs(Get get, int n, float top, float scale)
 {
     const float from = top == -INFINITY ? 0.0f : top;  // of nothing but -inf: 0 is subtracted, and 2^-inf is 0
-    const bool plain = fabsf(from) < 1e30f;
+    const bool plain = fabsf(from * scale) < 0x1p20f;
     const float off = plain ? -from * scale : -from;
     const uint64_t scale2 = pair(scale, scale), off2 = pair(off, off);
     uint64_t sums[2] = {0, 0};
