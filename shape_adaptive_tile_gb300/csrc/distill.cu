@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads)
                 t.add(v, scale);
         }
         t = cta_softmax<kThreads>(t, scale, scratch[0]);
-        empty = t.max == -INFINITY;
+        empty = t.max == -INFINITY && t.sum == 0.0f;  // entries of NaN are present: they are in the sum
         const float top = a.teacher_lse ? 0.0f : t.max, rest = a.teacher_lse ? a.teacher_lse[r] : logf(t.sum);
         for (int i = threadIdx.x; i < k; i += kThreads) {
             log_p[i] = (log_p[i] - top) / a.temperature - rest;
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kThreads)
         if (rank == 0) {
             float loss[1] = {0.0f};
             for (int i = threadIdx.x; i < k; i += kThreads)
-                if (p[i] > 0.0f)
+                if (p[i] != 0.0f)
                     loss[0] += p[i] * (log_p[i] - ((at_id[i] - q.max) / a.temperature - log_sum));
             row_sums<kThreads>(loss, sums, turn);
             if (threadIdx.x == 0) {
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sat_distill_row_kernel(const __
                 t.add(v, scale);
         }
     t = cta_softmax<NT>(t, scale, scratch[0]);
-    if (t.max == -INFINITY) {  // masked, or no entry present
+    if (t.max == -INFINITY && t.sum == 0.0f) {  // masked, or no entry present (those of NaN are in the sum)
         if (threadIdx.x == 0) {
             a.loss[r] = 0.0f;
             if (a.lse)
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sat_distill_row_kernel(const __
         log_p[i] = (log_p[i] - top) / a.temperature - rest;
         p[i] = id[i] >= 0 ? expf(log_p[i]) : 0.0f;
         sum[0] += p[i];
-        if (p[i] > 0.0f)
+        if (p[i] != 0.0f)
             sum[1] += p[i] * (log_p[i] - ((at_id[i] - q.max) / a.temperature - log_sum));
     }
     row_sums<NT>(sum, sums, turn);
