@@ -188,7 +188,9 @@ typedef struct {
  * once and writes their gradient once. */
 int rowop_distill(const rowop_distill_args* args, void* stream);
 
-/* Writes dlogits from a forward call's lse (loss is not used). */
+/* Writes dlogits from a forward call's lse (loss is not used). In 32 bits lse
+ * is good to |lse| 2^-24, a relative error of q; rows with |lse| above 64 (in
+ * 16-bit logits 512) are read a second time for their sums instead, by one CTA. */
 int rowop_distill_backward(const rowop_distill_args* args, void* stream);
 
 /* ---- verification of drafted tokens -------------------------------------------

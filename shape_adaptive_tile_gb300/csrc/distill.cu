@@ -34,6 +34,14 @@ constexpr int kWaitLimit = 1 << 22;  // polls of a barrier, each of which the ha
 
 enum Mode { kLoss, kBoth, kGrad };
 
+// The gradient alone comes from lse, whose rounding to 32 bits is a relative
+// error of up to |lse| 2^-24 in q. Rows with more than this (in their logits'
+// type, fp32: 4e-6, 16 bits: 3e-5, an eighth of fp16's rounding) have their sums
+// taken again: rows far from 0, and of the type's lowest value, which have
+// nothing of the sum in lse.
+template <typename T>
+constexpr float kFarLse = sizeof(T) == 4 ? 64.0f : 512.0f;
+
 // The teacher's entries of a row in shared memory, four arrays of k rounded up
 // to whole 16 bytes, so that the tokens can be compared four at a time.
 struct Entries {
@@ -215,6 +223,7 @@ __global__ void __launch_bounds__(kThreads)
     const bool entry = (MODE != kLoss || rank == 0) && threadIdx.x < k;
     const int token0 = entry ? a.ids[r * a.ldi + threadIdx.x] : -1;
     const float logit0 = entry ? teacher_logit(a, r * a.ldt + threadIdx.x) : 0.0f;
+    const float lse = MODE == kGrad ? a.lse[r] : 0.0f;
     if (weight == 0.0f) {  // alike for all CTAs of the cluster
         if (MODE != kGrad && rank == 0 && threadIdx.x == 0) {
             a.loss[r] = 0.0f;
@@ -270,9 +279,21 @@ __global__ void __launch_bounds__(kThreads)
         row_sums<kThreads>(sum, sums, turn);
     }
 
+    // Whether the row's sums are taken here. In the gradient's pass the row is then all its first CTA's, which may
+    // read it twice though the gradient goes in the logits' place.
+    const bool sums_here = MODE != kGrad || (!empty && fabsf(lse) > kFarLse<T>);
+    const int ctas = MODE == kGrad && sums_here ? 1 : cut.ctas;
+    if (MODE == kGrad && (empty || rank >= ctas)) {
+        if (any)  // the copies have to land before the CTA ends
+            for (int c = 0; c < kMaxChunks; ++c)
+                wait(c);
+        if (empty)
+            write_zeros();
+        return;
+    }
     Softmax q = Softmax::none();
-    if (MODE != kGrad) {
-        for (int i = rank; i < cut.per_row; i += cut.ctas) {
+    if (sums_here) {
+        for (int i = rank; i < cut.per_row; i += ctas) {
             if (i != rank)
                 refetch(i);
             __syncthreads();  // the ends are written
@@ -294,7 +315,7 @@ __global__ void __launch_bounds__(kThreads)
         if (failed)
             q.sum = NAN;
         q = cta_softmax<kThreads>(q, scale, scratch[1]);
-        if (cut.ctas > 1) {
+        if (MODE != kGrad && cut.ctas > 1) {
             cluster_wait();
             if (threadIdx.x < cut.ctas) {
                 const uint32_t at = map_to_cta(smem_u32(&across[rank]), threadIdx.x);
@@ -306,7 +327,7 @@ __global__ void __launch_bounds__(kThreads)
             q = sum_softmax(across, 1, cut.ctas, scale);
         }
         const float log_sum = logf(q.sum);
-        if (rank == 0) {
+        if (MODE != kGrad && rank == 0) {
             float loss[1] = {0.0f};
             for (int i = threadIdx.x; i < k; i += kThreads)
                 if (p[i] != 0.0f)
@@ -322,22 +343,19 @@ __global__ void __launch_bounds__(kThreads)
     if (MODE == kLoss)
         return;
     if (empty) {
-        if (MODE == kGrad && any)  // the copies have to land before the CTA ends
-            for (int c = 0; c < kMaxChunks; ++c)
-                wait(c);
         write_zeros();
         return;
     }
     const float c = (a.dloss ? a.dloss[r] : 1.0f) * weight * a.temperature;
-    if (MODE == kGrad) {
-        share = c * sum[0], times = 1.0f / a.temperature, from = a.lse[r], power = kLog2e;
+    if (!sums_here) {
+        share = c * sum[0], times = 1.0f / a.temperature, from = lse, power = kLog2e;
     } else {
         share = c * sum[0] / q.sum, from = q.max;
     }
-    const bool resident = MODE == kBoth && cut.per_row <= cut.ctas;
-    for (int i = rank; i < cut.per_row; i += cut.ctas) {
+    const bool resident = sums_here && cut.per_row <= ctas;
+    for (int i = rank; i < cut.per_row; i += ctas) {
         if (!resident) {
-            if (MODE == kBoth || i != rank)
+            if (sums_here || i != rank)
                 refetch(i);
             __syncthreads();
             for (int n = 0; n < kMaxChunks; ++n)
