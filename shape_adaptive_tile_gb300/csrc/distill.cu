@@ -98,6 +98,13 @@ __device__ __forceinline__ float teacher_logit(const rowop_distill_args& a, int6
                                            : teacher_at<__half>(a.teacher, i);
 }
 
+// t (log p - log q) for a student's logit `below` its row's maximum: multiplied
+// out, so that neither its quotient by a tiny t nor the square of t leaves fp32.
+__device__ __forceinline__ float scaled_log_ratio(const rowop_distill_args& a, float log_p, float below, float log_sum)
+{
+    return a.temperature * log_p - (below - a.temperature * log_sum);
+}
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -121,7 +128,7 @@ __global__ void __launch_bounds__(kThreads)
     const int rank = blockIdx.x % cut.ctas, k = static_cast<int>(a.k);
     const int64_t r = blockIdx.x / cut.ctas;
     const float weight = a.weight ? a.weight[r] : 1.0f;
-    const float scale = kLog2e / a.temperature;
+    const float scale = over_temperature(a.temperature, kLog2e);
     const T* row = static_cast<const T*>(a.logits) + r * a.ldl;
     T* out = a.dlogits ? static_cast<T*>(a.dlogits) + r * a.ldd : nullptr;
     // The row, and the slices, as addresses.
@@ -331,10 +338,10 @@ __global__ void __launch_bounds__(kThreads)
             float loss[1] = {0.0f};
             for (int i = threadIdx.x; i < k; i += kThreads)
                 if (p[i] != 0.0f)
-                    loss[0] += p[i] * (log_p[i] - ((at_id[i] - q.max) / a.temperature - log_sum));
+                    loss[0] += p[i] * scaled_log_ratio(a, log_p[i], at_id[i] - q.max, log_sum);
             row_sums<kThreads>(loss, sums, turn);
             if (threadIdx.x == 0) {
-                a.loss[r] = empty ? 0.0f : weight * a.temperature * a.temperature * loss[0];
+                a.loss[r] = empty ? 0.0f : weight * a.temperature * loss[0];
                 if (a.lse)
                     a.lse[r] = empty ? 0.0f : q.max / a.temperature + log_sum;
             }
@@ -348,7 +355,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     const float c = (a.dloss ? a.dloss[r] : 1.0f) * weight * a.temperature;
     if (!sums_here) {
-        share = c * sum[0], times = 1.0f / a.temperature, from = lse, power = kLog2e;
+        share = c * sum[0], times = over_temperature(a.temperature), from = lse, power = kLog2e;
     } else {
         share = c * sum[0] / q.sum, from = q.max;
     }
@@ -431,7 +438,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sat_distill_row_kernel(const __
     float *p = teacher.p, *log_p = teacher.log_p, *at_id = teacher.at_id;
     int* id = teacher.id;
     const int64_t r = blockIdx.x;
-    const float weight = a.weight ? a.weight[r] : 1.0f, scale = kLog2e / a.temperature;
+    const float weight = a.weight ? a.weight[r] : 1.0f, scale = over_temperature(a.temperature, kLog2e);
     const Packs<T> s(static_cast<const T*>(a.logits) + r * a.ldl, vocab);
     T* out = a.dlogits ? static_cast<T*>(a.dlogits) + r * a.ldd : nullptr;
     int turn = 0;
@@ -513,11 +520,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sat_distill_row_kernel(const __
         p[i] = id[i] >= 0 ? expf(log_p[i]) : 0.0f;
         sum[0] += p[i];
         if (p[i] != 0.0f)
-            sum[1] += p[i] * (log_p[i] - ((at_id[i] - q.max) / a.temperature - log_sum));
+            sum[1] += p[i] * scaled_log_ratio(a, log_p[i], at_id[i] - q.max, log_sum);
     }
     row_sums<NT>(sum, sums, turn);
     if (threadIdx.x == 0) {
-        a.loss[r] = weight * a.temperature * a.temperature * sum[1];
+        a.loss[r] = weight * a.temperature * sum[1];
         if (a.lse)
             a.lse[r] = q.max / a.temperature + log_sum;
     }
