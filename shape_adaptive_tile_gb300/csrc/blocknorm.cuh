@@ -180,10 +180,10 @@ __device__ __forceinline__ float sum_of(uint64_t v)
     return f.x + f.y;
 }
 
-// The gate row of row r, by a 32-bit division (there are fewer than 2^31 rows).
+// The gate row of row r, by a 32-bit division (there are fewer than 2^31 rows). Without a gate rows_per_gate may be 0.
 __device__ __forceinline__ int64_t gate_row(const rowop_block_norm_args& a, int64_t r)
 {
-    return a.rows_per_gate >= a.rows ? 0 : static_cast<uint32_t>(r) / static_cast<uint32_t>(a.rows_per_gate);
+    return !a.gate || a.rows_per_gate >= a.rows ? 0 : static_cast<uint32_t>(r) / static_cast<uint32_t>(a.rows_per_gate);
 }
 
 // The thread's group i of gate row k, in the gate's type: the block's or fp32
