@@ -62,7 +62,9 @@ int rowop_layernorm(const float* X, int64_t ldx, const float* gamma, const float
  * type or a missing pointer, GEMM_ERR_ALIGN for a pointer that is not aligned
  * to its element, GEMM_ERR_LAUNCH. Nothing is allocated: scratch is the
  * caller's, of the size that a ..._workspace function gives; concurrent calls
- * need scratch of their own. Rows of any alignment and stride are correct;
+ * need scratch of their own. Waits inside the kernels are bounded: where a
+ * copy has not come after two seconds, which no launch takes, the outputs
+ * that hang on it are NaN. Rows of any alignment and stride are correct;
  * rows that all start on 16-byte boundaries are the fast ones.
  */
 

@@ -203,7 +203,6 @@ __device__ __forceinline__ Group gate_group(const rowop_block_norm_args& a, int6
 // ---- rows through shared memory ------------------------------------------------------
 
 constexpr int kMaxStages = 8;
-constexpr int kWaitLimit = 1 << 22;  // polls of a barrier, each of which the hardware suspends for a while
 
 // One of the matrices that a kernel reads row by row (none where p is NULL).
 struct Source {
@@ -256,17 +255,17 @@ struct Ring {
 
     static __device__ __forceinline__ void wait(uint64_t* bar, int parity, bool& failed)
     {
-        for (int n = 0; !failed && !mbar_try_wait<true>(smem_u32(bar), parity); ++n)
-            failed = n > kWaitLimit;
+        failed = failed || !wait_bounded<true>(smem_u32(bar), parity);
     }
 
+    // Returns whether it has: not where the stage does not become free.
     template <bool kPack, int N>
-    __device__ __forceinline__ void fill(unsigned char* stage, int s, int round, int group, const Source (&sources)[N], int64_t r,
-                                         bool& failed)
+    __device__ __forceinline__ bool fill(unsigned char* stage, int s, int round, int group, const Source (&sources)[N], int64_t r)
     {
         uint64_t* const bar = &full[group][s];
         const int lane = threadIdx.x % 32;
-        wait(&empty[s], round & 1 ^ 1, failed);
+        if (!__all_sync(0xffffffffu, wait_bounded<true>(smem_u32(&empty[s]), round & 1 ^ 1)))
+            return false;
         uint32_t total = 0;
         if constexpr (kPack) {
             if (lane == 0) {
@@ -313,15 +312,26 @@ struct Ring {
             if (lane == 0)
                 mbar_arrive_expect_tx(smem_u32(bar), total);
         }
+        return true;
+    }
+
+    // The filling warp's last `stages` of `rows` rows for `groups` groups in turn: waits until they have landed.
+    __device__ __forceinline__ void drain(int rows, int stages, int groups, int apart)
+    {
+        for (int k = max(0, rows - stages); k < rows; ++k)
+            if (!wait_bounded<true, kDrainNs>(smem_u32(&full[k % groups][k % stages]), k / apart & 1))
+                break;
     }
 
     // Waits for the use-th row that the group has had in stage s.
     __device__ __forceinline__ void take(int group, int s, int use, bool& failed) { wait(&full[group][s], use & 1, failed); }
 
-    __device__ __forceinline__ void release(int s)
+    // The warp has read stage s: unless one of its lanes has given up, whose row may not have landed yet.
+    __device__ __forceinline__ void release(int s, bool failed)
     {
+        const bool read = !__any_sync(0xffffffffu, failed);
         __syncwarp();
-        if (threadIdx.x % 32 == 0)
+        if (read && threadIdx.x % 32 == 0)
             mbar_arrive(smem_u32(&empty[s]));
     }
 };
@@ -408,9 +418,9 @@ __device__ __forceinline__ void cluster_sums(float (&v)[K], float (&across)[2][M
                                              int ctas, int& turn, bool& failed)
 {
     const int b = turn & 1;
-    if (thread == 0)
+    if (thread == 0 && !failed)
         mbar_arrive_expect_tx(smem_u32(&arrived[b]), ctas * ((K + 1) / 2) * 8);
-    if (thread < ctas) {
+    if (thread < ctas && !failed) {
         const uint32_t bar = map_to_cta(smem_u32(&arrived[b]), thread), to = map_to_cta(smem_u32(&across[b][rank][0]), thread);
 #pragma unroll
         for (int k = 0; k < K; k += 2)
@@ -424,6 +434,20 @@ __device__ __forceinline__ void cluster_sums(float (&v)[K], float (&across)[2][M
         for (int c = 0; c < ctas; ++c)
             v[k] += across[b][c][k];
     }
+}
+
+// The end of a kernel whose CTAs wait. No CTA of a cluster ends while another
+// may still send to it. Where this thread has given up, copies that it has
+// started and sums that were sent to it before the barrier may be on their way,
+// with nothing here that counts them any more: they have the time that a wait
+// has, again.
+__device__ __forceinline__ void end_of_rows(bool clustered, bool failed)
+{
+    if (clustered)
+        cluster_sync();
+    if (failed)
+        for (const uint64_t since = globaltimer_ns(); globaltimer_ns() - since < kSettleNs;)
+            ;
 }
 
 // ---- forward -----------------------------------------------------------------------
@@ -642,24 +666,29 @@ __global__ void __launch_bounds__(512 + 32, 1)
     if (C > 1)
         cluster_sync();  // both have started and have their barriers
     const int64_t pair_of = blockIdx.x / C, pairs = gridDim.x / C;
+    // The rows that a group has in one stage are as far apart, counted in the CTA's rows, as the least number that is a
+    // multiple of both the stages and the groups.
+    int apart = stages;
+    while (apart % G)
+        apart += stages;
     bool failed = false;
     int s = 0, round = 0, turn = 0;
     if (threadIdx.x >= 512) {
-        int filling = 0;  // the group whose row it is
-        for (int64_t r = pair_of; r < a.rows; r += pairs) {
-            ring.fill<kPack>(ring_memory + s * stage_bytes, s, round, filling, sources, r, failed);
+        int filling = 0, filled = 0;  // the group whose row it is, and the rows so far
+        for (int64_t r = pair_of; r < a.rows; r += pairs, ++filled) {
+            if (!ring.fill<kPack>(ring_memory + s * stage_bytes, s, round, filling, sources, r))
+                break;
             if (++s == stages)
                 s = 0, ++round;
             filling = filling + 1 == G ? 0 : filling + 1;
         }
+        ring.drain(filled, stages, G, apart);
+        end_of_rows(C > 1, false);
         return;
     }
     const int group = threadIdx.x / NT, lane = threadIdx.x % NT;
-    // The group's k-th row of the CTA's: k = group, group + G, ... The rows that it has in one stage are as far apart as
-    // the least number that is a multiple of both the stages and the groups.
-    int apart = stages, use = 0, swaps = 0;
-    while (apart % G)
-        apart += stages;
+    // The group's k-th row of the CTA's: k = group, group + G, ...
+    int use = 0, swaps = 0;
     s = group % stages;
     int k = group, next_use = apart;
     for (int64_t r = pair_of + group * pairs; r < a.rows; r += G * pairs, k += G, s = (s + G) % stages) {
@@ -672,13 +701,15 @@ __global__ void __launch_bounds__(512 + 32, 1)
         for (int i = 0; i < NV; ++i)
             v[i] = stage_group<kPack, NT, B>(stage, sources[0], r, lane, i, width);
         if (failed)
-            v[0] = fill(NAN);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                v[i] = fill(NAN);
         finish_row<B, S, NT, NV, kPack, kLayer>(
             a, r, v, lane, off, width,
             [&](int i) {
                 const Group u = stage_group<kPack, NT, S>(stage, sources[1], r, lane, i, width);
                 if (i == NV - 1)
-                    ring.release(s);
+                    ring.release(s, failed);
                 return u;
             },
             [&](int w, int i) {
@@ -698,6 +729,7 @@ __global__ void __launch_bounds__(512 + 32, 1)
                 }
             });
     }
+    end_of_rows(C > 1, C > 1 && failed);
 }
 
 template <typename B, typename S, int NT, int NV, bool kPack, bool kLayer>
@@ -800,13 +832,13 @@ enum Input { kDh, kDz, kH, kY, kInputs };
 //
 // `at(input, r)` gives the thread's group of a matrix, `weight(w)` of a weight
 // and `gate()` of the gate, whose row `change_gate(k)` makes the k-th; `sums`
-// adds over the row once its inputs have been read, `done()` ends it. `off` is the first of the CTA's columns, `width`
-// their number.
+// adds over the row once its inputs have been read, `done()` ends it; `failed()` says at the end whether a row's inputs
+// did not come. `off` is the first of the CTA's columns, `width` their number.
 template <typename B, typename S, int NT, int NV, bool kPack, int MODE, typename At, typename WeightAt, typename GateAt,
-          typename ChangeGate, typename Sums, typename Done>
+          typename ChangeGate, typename Sums, typename Done, typename Failed>
 __device__ __forceinline__ void backward_rows(const rowop_block_norm_args& a, const rowop_block_norm_grads& g, const Split& split,
                                               int64_t part, int lane, int off, int width, At at, WeightAt weight, GateAt gate,
-                                              ChangeGate change_gate, Sums sums, Done done)
+                                              ChangeGate change_gate, Sums sums, Done done, Failed failed)
 {
     constexpr bool kBeta = MODE != kRms, kGrouped = MODE == kLayerGrouped;
     const float inv = 1.0f / static_cast<float>(a.width);
@@ -982,6 +1014,8 @@ __device__ __forceinline__ void backward_rows(const rowop_block_norm_args& a, co
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+        if (failed())  // the rows' sums have made the others NaN
+            dz_hh[i] = dz_1[i] = fill(NAN);
         if (!grouped)
             gate_ends(i);
         put(kPreGamma, i, dz_hh[i]);
@@ -1027,7 +1061,7 @@ __global__ void __launch_bounds__(128)
                                      lane, 0, width);
         },
         [&](int) { return gate_now; }, [&](int64_t k) { gate_now = gate_group<kPack, 32, B>(a, k, lane, 0, 0, width); },
-        [&](auto& v) { row_sums<32>(v, nullptr, turn); }, [] {});
+        [&](auto& v) { row_sums<32>(v, nullptr, turn); }, [] {}, [] { return false; });
 }
 
 // Wider rows: a CTA of NT threads a part, or a cluster of split.ctas, each of
@@ -1113,11 +1147,13 @@ __global__ void __launch_bounds__(NT, kBackwardPerSM<NT>)
         place = mine.offset + static_cast<int>(x - (lo & ~15ull));
         return mine.p && x >= lo && x < hi && (x < lo16 || x >= hi16) && (piece < 8 || hi16 >= lo16) ? x : 0;
     };
+    bool failed = false;
     auto put_end = [&](int s, int place, uint64_t x, uint16_t v) {
+        const bool sure = !__any_sync(0xffffffffu, failed);
         if (x)
             *reinterpret_cast<uint16_t*>(ring_memory + s * stage_bytes + place) = v;
         __syncwarp();
-        if (lane % 32 == 0)
+        if (sure && lane % 32 == 0)
             mbar_arrive(smem_u32(&full[s]));
     };
     for (int s = 0; s < stages && first + s < end; ++s) {
@@ -1130,7 +1166,7 @@ __global__ void __launch_bounds__(NT, kBackwardPerSM<NT>)
         }
     }
 
-    bool failed = false, taken = false;
+    bool taken = false;
     int s = 0, round = 0, turn = 0, swaps = 0, place = 0;
     uint64_t x = 0;
     uint16_t held = 0;
@@ -1162,10 +1198,12 @@ __global__ void __launch_bounds__(NT, kBackwardPerSM<NT>)
         [&](auto& v) {
             if (!kPack && threadIdx.x < 64)
                 fence_proxy_async_smem();  // of the ends written before: what follows them there comes by bulk copies
+            if (failed)  // with its sum the row's gradients are NaN, all of them
+                v[0] = NAN;
             ring_sums<NT>(v, scratch, turn, 0);
             const int before = s == 0 ? stages - 1 : s - 1;
             if (now > first && now - 1 + stages < end) {
-                if (threadIdx.x == 0)
+                if (threadIdx.x == 0 && !failed)
                     send(now - 1 + stages, before);
                 if (!kPack && threadIdx.x < 64)
                     put_end(before, place, x, held);
@@ -1180,7 +1218,9 @@ __global__ void __launch_bounds__(NT, kBackwardPerSM<NT>)
             ++now;
             if (++s == stages)
                 s = 0, ++round;
-        });
+        },
+        [&] { return failed; });
+    end_of_rows(ctas > 1, failed);
 }
 
 template <typename B, typename S, int NT, bool kPack, int MODE>

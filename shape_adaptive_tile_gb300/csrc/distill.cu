@@ -30,7 +30,6 @@ constexpr int kChunk = 16384;       // bytes of a bulk copy with its own barrier
 constexpr int kMaxSlice = 65536;    // so that three CTAs' slices fit an SM
 constexpr int kMaxChunks = kMaxSlice / kChunk;
 constexpr int kMaxCluster = 16;
-constexpr int kWaitLimit = 1 << 22;  // polls of a barrier, each of which the hardware suspends for a while
 
 enum Mode { kLoss, kBoth, kGrad };
 
@@ -134,6 +133,8 @@ __global__ void __launch_bounds__(kThreads)
     // The row, and the slices, as addresses.
     const uint64_t start = reinterpret_cast<uint64_t>(row), base = start & ~15ull, stop = start + a.vocab * sizeof(T);
     int phase = 0, packs = 0;
+    // This thread has given up a wait; some thread had before the last copies were to start, and they did not.
+    bool failed = false, stuck = false;
     int64_t first = 0;  // the element that the slice's first pack starts with (negative where that is before the row)
 
     // Starts the copies of slice i; every thread then knows its first element and number of packs.
@@ -145,6 +146,8 @@ __global__ void __launch_bounds__(kThreads)
         const uint64_t lo16 = (lo + 15) & ~15ull, hi16 = hi & ~15ull;
         first = (static_cast<int64_t>(at) - static_cast<int64_t>(start)) / static_cast<int64_t>(sizeof(T));
         packs = static_cast<int>((hi - at + 15) / 16);
+        if (stuck)
+            return;
         if (threadIdx.x == 0) {
             for (int c = 0; c < kMaxChunks; ++c) {
                 const uint64_t from = at + c * kChunk;
@@ -170,17 +173,14 @@ __global__ void __launch_bounds__(kThreads)
     // Into a slice that has been read, and had its ends written, by ordinary instructions.
     auto refetch = [&](int i) {
         fence_proxy_async_smem();
-        __syncthreads();
+        stuck = __syncthreads_or(failed);
         fetch(i);
     };
-    bool failed = false;
-    auto wait = [&](int c) {
-        int n = 0;
-        while (!mbar_try_wait<false>(smem_u32(&bars[c]), phase))
-            if (++n > kWaitLimit) {
-                failed = true;
-                break;
-            }
+    auto wait = [&](int c) { failed = failed || !wait_bounded<false>(smem_u32(&bars[c]), phase); };
+    // Before the CTA ends, where thread 0 has not seen its last copies, of phase `parity`, land.
+    auto drain = [&](int parity) {
+        for (int c = 0; c < kMaxChunks && threadIdx.x == 0; ++c)
+            wait_bounded<false, kDrainNs>(smem_u32(&bars[c]), parity);
     };
     // Writes share 2^((v times - from) power) for the logits v of the slice.
     float share = 0.0f, times = 1.0f, from = 0.0f, power = scale;
@@ -292,8 +292,7 @@ __global__ void __launch_bounds__(kThreads)
     const int ctas = MODE == kGrad && sums_here ? 1 : cut.ctas;
     if (MODE == kGrad && (empty || rank >= ctas)) {
         if (any)  // the copies have to land before the CTA ends
-            for (int c = 0; c < kMaxChunks; ++c)
-                wait(c);
+            drain(phase);
         if (empty)
             write_zeros();
         return;
@@ -304,6 +303,8 @@ __global__ void __launch_bounds__(kThreads)
             if (i != rank)
                 refetch(i);
             __syncthreads();  // the ends are written
+            if (stuck)
+                break;
             for (int c = 0; c < kMaxChunks; ++c) {
                 wait(c);
                 const int end = min(packs, (c + 1) * (kChunk / 16));
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kThreads)
             }
             phase ^= 1;
         }
-        if (failed)
+        if (failed || stuck)
             q.sum = NAN;
         q = cta_softmax<kThreads>(q, scale, scratch[1]);
         if (MODE != kGrad && cut.ctas > 1) {
@@ -347,10 +348,11 @@ __global__ void __launch_bounds__(kThreads)
             }
         }
     }
-    if (MODE == kLoss)
-        return;
-    if (empty) {
-        write_zeros();
+    if (MODE == kLoss || empty) {
+        if (failed)
+            drain(phase ^ 1);
+        if (MODE != kLoss)
+            write_zeros();
         return;
     }
     const float c = (a.dloss ? a.dloss[r] : 1.0f) * weight * a.temperature;
@@ -365,11 +367,11 @@ __global__ void __launch_bounds__(kThreads)
             if (sums_here || i != rank)
                 refetch(i);
             __syncthreads();
-            for (int n = 0; n < kMaxChunks; ++n)
+            for (int n = 0; n < kMaxChunks && !stuck; ++n)
                 wait(n);
-            phase ^= 1;
-            if (failed)
-                return;
+            phase ^= !stuck;
+            if (failed || stuck)
+                share = NAN;
         }
         write();
         __syncthreads();
@@ -385,6 +387,8 @@ __global__ void __launch_bounds__(kThreads)
             }
         }
     }
+    if (failed)
+        drain(phase ^ 1);
 }
 
 // ---- many rows: a CTA a row -----------------------------------------------------

@@ -425,6 +425,48 @@ __device__ __forceinline__ Softmax cta_softmax(Softmax s, float scale, Softmax* 
     return warp_softmax((threadIdx.x & 31) < NT / 32 ? scratch[threadIdx.x & 31] : Softmax::none(), scale);
 }
 
+// ---- bounded waits -----------------------------------------------------------------
+
+// Every wait for a copy or for another CTA's sums gives up after two seconds,
+// more than any launch takes. Whoever gave up has NaN for what it was to
+// compute, waits for nothing more and sends, fills and releases nothing more
+// (a barrier is armed again only by those who have seen its phase end). A CTA
+// ends when the copies that it has started have landed, or have had that time
+// again, and one of a cluster not before the others. Tests build with 0: then
+// a wait gives up at its first look.
+#ifndef SAT_ROWS_WAIT_NS
+#define SAT_ROWS_WAIT_NS 2000000000ull
+#endif
+constexpr uint64_t kWaitNs = SAT_ROWS_WAIT_NS, kDrainNs = 2000000000ull;
+constexpr uint64_t kSettleNs = kWaitNs ? kWaitNs : 10000000ull;
+
+// Whether the barrier's phase of this parity ended within the limit.
+template <bool kCluster, uint64_t kLimitNs = kWaitNs>
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity)
+{
+    if constexpr (kLimitNs == 0) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(bar), "r"(parity)
+                     : "memory");
+        return ok != 0;
+    } else {
+        uint64_t since = 0;
+        for (unsigned n = 1; !mbar_try_wait<kCluster>(bar, parity); ++n)
+            if (n % 32 == 0) {
+                const uint64_t now = globaltimer_ns();
+                if (n == 32)
+                    since = now;
+                else if (now - since > kLimitNs)
+                    return false;
+            }
+        return true;
+    }
+}
+
 // ---- clusters ----------------------------------------------------------------------
 
 // Stores to shared memory of any CTA of the cluster (which must have started).
