@@ -741,31 +741,45 @@ cudaError_t launch_forward(const rowop_block_norm_args& a, cudaStream_t s)
     return cudaGetLastError();
 }
 
+// What a ring's CTA has in shared memory, for `columns` columns and groups of NT threads.
+struct RingRoom {
+    static constexpr int bytes = kSmemPerSM - 2048;
+    int stage, weights;
+    bool kept;  // the weights stay on chip: a row for every group and one more fit beside them
+};
+
+template <typename B, typename S>
+RingRoom ring_room(const rowop_block_norm_args& a, int columns, int groups)
+{
+    const int64_t w = a.width < columns ? a.width : columns;
+    const bool post = a.post_norm != ROWOP_NORM_NONE, pre = a.pre_norm != ROWOP_NORM_NONE;
+    const int vectors = (post && a.post_gamma) + (pre && a.pre_gamma) + (a.gate && a.rows_per_gate >= a.rows) +
+                        (a.post_norm == ROWOP_NORM_LAYER && a.post_beta) + (a.pre_norm == ROWOP_NORM_LAYER && a.pre_beta);
+    RingRoom r;
+    r.stage = static_cast<int>((w * sizeof(B) + 31) / 16 * 16 + (w * sizeof(S) + 31) / 16 * 16);
+    r.weights = vectors * columns * 4;
+    r.kept = RingRoom::bytes - r.weights >= (groups + 1) * r.stage;
+    return r;
+}
+
 template <typename B, typename S, int NT, int NV, int C, bool kPack, bool kLayer>
 cudaError_t launch_ring(const rowop_block_norm_args& a, cudaStream_t s)
 {
-    const int64_t w = a.width < NT * NV * 8 ? a.width : NT * NV * 8;
-    const int stage = static_cast<int>((w * sizeof(B) + 31) / 16 * 16 + (w * sizeof(S) + 31) / 16 * 16);
-    constexpr int room = kSmemPerSM - 2048, groups = 512 / NT;
-    const bool post = a.post_norm != ROWOP_NORM_NONE, pre = a.pre_norm != ROWOP_NORM_NONE;
-    int weights = (post && a.post_gamma) + (pre && a.pre_gamma) + (a.gate && a.rows_per_gate >= a.rows) +
-                  (a.post_norm == ROWOP_NORM_LAYER && a.post_beta) + (a.pre_norm == ROWOP_NORM_LAYER && a.pre_beta);
-    weights *= NT * NV * 8 * 4;
-    // Weights stay on chip where a row for every group and one more fit beside them.
-    const bool kept = room - weights >= (groups + 1) * stage;
-    int stages = (kept ? room - weights : room) / stage;
+    const RingRoom r = ring_room<B, S>(a, NT * NV * 8, 512 / NT);
+    const int stage = r.stage, weights = r.kept ? r.weights : 0;
+    int stages = (RingRoom::bytes - weights) / stage;
     stages = stages < kMaxStages ? stages : kMaxStages;
     if (stages < 1)
         return cudaErrorInvalidConfiguration;
     auto kernel = sat_block_norm_ring_kernel<B, S, NT, NV, C, kPack, kLayer>;
     static Prepared prepared;
-    const cudaError_t e = prepared.once(reinterpret_cast<const void*>(kernel), room);
+    const cudaError_t e = prepared.once(reinterpret_cast<const void*>(kernel), RingRoom::bytes);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(kSMs / C * C));
     cfg.blockDim = dim3(512 + 32);
-    cfg.dynamicSmemBytes = stages * stage + (kept ? weights : 0);
+    cfg.dynamicSmemBytes = stages * stage + weights;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -773,24 +787,47 @@ cudaError_t launch_ring(const rowop_block_norm_args& a, cudaStream_t s)
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = C > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, a, stages, stage, kept);
+    return cudaLaunchKernelEx(&cfg, kernel, a, stages, stage, r.kept);
+}
+
+// Whether rows of over 1024 columns go through the ring, not to a CTA each,
+// whose threads hold a row with room for a second CTA's in the SM: by their
+// number an SM and by what lies in a stage, x's and y's columns of one CTA.
+// Large stages leave few in flight, and where the weights do not fit beside
+// them every row reads those again. Elements that move by themselves
+// (not kPack) cost a CTA a row more. Measured in us, a CTA a row | the ring,
+// inputs from HBM, RMS norms and a shared fp32 gate; b bf16, f fp32, m bf16
+// on an fp32 stream:
+//   2048 b: 304 rows 4.6 | 6.3, 456 7.1 | 6.7, 4864 43 | 21; f: 456 7.9 | 7.8, 912 12.1 | 10.5
+//   4096 b: 760 11.5 | 11.3, 1216 15.0 | 13.7, 4864 49 | 32; f: 608 11.3 | 12.1, 912 15.6 | 15.1; m: 912 14.1 | 13.7
+//   6144 b: 1216 20.0 | 20.1, 1520 23.3 | 22.3, 4864 60 | 51; f: 1520 29.3 | 30.3, 4864 76 | 88; m: 1520 26.2 | 25.3
+//   8192 b: 1520 25.8 | 25.9, 2128 33.5 | 32.3, 4864 67 | 61; f: 4864 96 | 125; m: 4864 78 | 112
+//   12288 b: 304 15.4 | 15.8, 456 19.9 | 19.1, 4864 135 | 104; f: 456 25.9 | 23.1, 4864 177 | 171; m: 4864 155 | 120
+//   16384 b: 380 23.9 | 20.1, 4864 170 | 121; m: 4864 212 | 231; f without weights: 4864 186 | 210
+//   not kPack: 1537 b 1216 14.4 | 14.1, 2432 26.3 | 22.0; 3001 f 1216 16.2 | 17.5, 2432 28.7 | 27.8; 6001 b 304 9.0 |
+//   11.3, 456 15.1 | 13.1; 8001 f 2432 65 | 75; 12001 f 304 21 | 18, 2432 128 | 82; 16001 f 304 25.5 | 25.9, 2432 155 | 144
+template <typename B, typename S, bool kPack>
+bool ring_pays(const rowop_block_norm_args& a)
+{
+    const bool one = a.width <= 8192;  // CTA, not a pair
+    const int columns = a.width <= 2048 ? 2048 : a.width <= 4096 ? 4096 : a.width <= 6144 || (!one && a.width <= 12288) ? 6144 : 8192;
+    const RingRoom r = ring_room<B, S>(a, columns, a.width <= 4096 ? 4 : 2);
+    if (!kPack)
+        return a.width <= 4096 ? a.rows >= 10 * kSMs : one ? a.rows >= 3 * kSMs && r.kept : a.rows >= 2 * kSMs;
+    return a.rows >= (a.width <= 2048 ? 3 : a.width <= 4096 ? 6 : one ? 10 : 3) * kSMs && r.kept && r.stage <= (one ? 40 : 49) * 1024;
 }
 
 template <typename B, typename S, bool kPack, bool kLayer>
 cudaError_t choose_forward_as(const rowop_block_norm_args& a, cudaStream_t s)
 {
-    // Few rows, and rows of up to 1024 columns: a CTA a row and as many threads as it has groups. Beyond, two to four
-    // groups a thread, so that a row's fixed work (the reductions, its addresses) is spread over up to 32 columns. Few
-    // are up to four rows an SM, or eight between 2048 and 8192 columns, where a CTA's threads hold a row with room for
-    // a second. (us for bf16, a CTA a row | the ring: 304 x 2048 4.0 | 5.1, 608 x 2048 6.5 | 6.1, 4864 x 2048 43 | 21;
-    // 608 x 4096 6.5 | 7.4, 1216 x 4096 15.2 | 13.6; 912 x 8192 17.9 | 19.3, 1216 x 8192 21.9 | 22.3, 4864 x 8192 66 |
-    // 59; 304 x 16384 18.3 | 17.5, 608 x 16384 31 | 24, 4864 x 16384 170 | 120; 4864 x 1024 13.1 | 15.1.)
-    const bool few = a.rows < (a.width > 2048 && a.width <= 8192 ? 8 : 4) * kSMs;
+    // Few rows, and rows of up to 1024 columns: a CTA a row and as many threads as it has groups (4864 x 1024 bf16 13.1 us, in
+    // the ring 15.1). In the ring two to four groups a thread, so that a row's fixed work (the reductions, its addresses) is
+    // spread over up to 32 columns; three where that is enough (4864 x 5120 bf16 50 us, with four 57; 10240 103 | 119).
     if (a.width <= 256)
         return launch_forward<B, S, 32, 1, kPack, kLayer>(a, s);
     if (a.width <= 1024)
         return launch_forward<B, S, 128, 1, kPack, kLayer>(a, s);
-    if (few)
+    if (!ring_pays<B, S, kPack>(a))
         return a.width <= 4096   ? launch_forward<B, S, 512, 1, kPack, kLayer>(a, s)
                : a.width <= 8192 ? launch_forward<B, S, 512, 2, kPack, kLayer>(a, s)
                                  : launch_forward<B, S, 512, 4, kPack, kLayer>(a, s);
