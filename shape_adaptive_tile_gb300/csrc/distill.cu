@@ -599,11 +599,14 @@ cudaError_t launch_rows_by(const rowop_distill_args& a, cudaStream_t s)
 }
 
 // The threads of a row's CTA, and with them the rows at hand in an SM (1024 /
-// NT): more of these overlap better, but with a gradient all rows at hand have to
-// stay in L2 for their second pass. (us for 128 | 256 | 512 | 1024 threads,
-// 1500 rows with gradient in 16-bit types: 24576 tokens 38 | 43 | 55 | 104, 49152
-// 79 | 62 | 78 | 117, 131072 202 | 180 | 160 | 186; 700 x 262144 179 | 199 | 173
-// | 164. Loss: 1500 x 32768 23 | 25 | 32 | 64, 131072 72 | 67 | 70 | 89.)
+// NT): more of these overlap better, but with a gradient the rows at hand
+// should be in L2 for their second pass. (us for 128 | 256 | 512 | 1024 threads,
+// with gradient: 1500 rows in 16-bit types of 24576 tokens 38 | 42 | 54 | 104,
+// 49152 72 | 62 | 77 | 118, 131072 200 | 172 | 152 | 182, 700 x 262144 179 | 197 |
+// 168 | 155; fp32 1500 x 24576 71 | 59 | 71 | 112, 700 x 131072 178 | 193 | 166 |
+// 150, 400 x 262144 206 | 204 | 206 | 184. Loss: 1500 x 32768 22 | 23 | 29 | 59,
+// 131072 68 | 65 | 67 | 84; 700 x 262144, one round of eight CTAs an SM and 1.2 of
+// four, 58 | 69 | 66 | 68.)
 template <typename T, int MODE>
 cudaError_t launch_rows(const rowop_distill_args& a, int64_t row, cudaStream_t s)
 {
@@ -620,11 +623,13 @@ template <typename T, int MODE>
 cudaError_t launch(const rowop_distill_args& a, cudaStream_t s)
 {
     if constexpr (MODE != kGrad) {
-        // A CTA a row, or a row's slices in a cluster: a row by itself where there are rows for half of the SMs, or
-        // where it is short. (us, row | slices, 16-bit types: 76 x 32000 with gradient 9.1 | 10.2, 8 x 131072 15.7 |
-        // 8.9, 76 x 131072 18.3 | 17.9; loss 8 x 32000 5.0 | 6.6, 38 x 131072 8.6 | 7.8, 304 x 131072 17.9 | 32.3.)
+        // A CTA a row, or a row's slices in a cluster: a row by itself where there are rows for two thirds of the SMs
+        // (about where clusters of four no longer all run at once), or where it is short. (us, row | slices, 16-bit types,
+        // inputs from HBM: with gradient 8 x 16384 7.7 | 7.7, 8 x 32000 8.8 | 8.1, 88 x 32000 11.2 | 11.3, 8 x 131072 17.9 |
+        // 9.6, 100 x 131072 20.5 | 19.5, 114 x 131072 20.5 | 28.2, 304 x 131072 36 | 50; loss 38 x 32000 7.2 | 7.6,
+        // 76 x 50304 10.0 | 8.4, 100 x 131072 12.6 | 12.6, 114 x 131072 12.7 | 17.3.)
         const int64_t row = a.vocab * static_cast<int64_t>(sizeof(T));
-        if (a.rows >= kSMs / 2 || row <= (MODE == kLoss ? 65536 : 32768))
+        if (3 * a.rows >= 2 * kSMs || row <= (MODE == kLoss ? 65536 : 32768))
             return launch_rows<T, MODE>(a, row, s);
     }
     // With what a row may need before its start to reach a 16-byte boundary.
