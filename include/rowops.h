@@ -64,8 +64,14 @@ int rowop_layernorm(const float* X, int64_t ldx, const float* gamma, const float
  * caller's, of the size that a ..._workspace function gives; concurrent calls
  * need scratch of their own. Waits inside the kernels are bounded: where a
  * copy has not come after two seconds, which no launch takes, the outputs
- * that hang on it are NaN. Rows of any alignment and stride are correct;
- * rows that all start on 16-byte boundaries are the fast ones.
+ * that hang on it are NaN. Rows of any alignment and stride are correct.
+ * The fast ones: in the block norm, where all of a call's rows start on
+ * boundaries of eight elements (16 bytes in 16-bit types, 32 in fp32), the
+ * weights' vectors on 32 bytes, and the width is a multiple of eight;
+ * otherwise all of its elements move one by one. In the distillation logits
+ * move by 16 bytes wherever their rows start, and the gradient where its rows
+ * start on the same byte of 16 as the logits'. In the verification the draw is
+ * fast where target, draft and noise rows start on 16 bytes.
  */
 
 /* ---- block norm: norm after a block, gate, residual, norm before the next --
@@ -83,7 +89,7 @@ int rowop_layernorm(const float* X, int64_t ldx, const float* gamma, const float
  */
 typedef enum { ROWOP_NORM_NONE = 0, ROWOP_NORM_RMS = 1, ROWOP_NORM_LAYER = 2 } rowop_norm_t;
 
-/* Widest row of the block norm. */
+/* Widest row of the block norm (of fewer than 2^31 rows). */
 #define ROWOP_BLOCK_NORM_MAX_WIDTH 16384
 
 typedef struct {
@@ -162,7 +168,7 @@ int rowop_block_norm_backward(const rowop_block_norm_args* args, const rowop_blo
  * >= vocab, or whose logit is -inf, is absent. A row of weight 0, or with no
  * entry present, has loss, lse and gradient 0, whatever its logits are.
  * Student logits of -inf are tokens of probability 0. lse[r] is
- * log sum_j exp(s_j / t).
+ * log sum_j exp(s_j / t). rows is at most 2^26, vocab 2^30.
  */
 #define ROWOP_DISTILL_MAX_K 1024
 
@@ -219,8 +225,9 @@ int rowop_distill_backward(const rowop_distill_args* args, void* stream);
  * logprobs[b], where not NULL, holds log p of each of out[b]'s tokens
  * (temperature 0: at temperature 1), then 0. A drafted token outside the vocabulary is
  * refused. Logits of -inf have probability 0. A row without a distribution (all -inf, or a NaN or
- * +inf in it) refuses the token and draws -1, with logprob 0. With drafts == 0
- * this is plain sampling.
+ * +inf in it) refuses the token and draws -1, with logprob 0; a draft row
+ * without one refuses the token, and the draw is from p_n. With drafts == 0
+ * this is plain sampling. batch is at most 2^20, vocab 2^30.
  */
 #define ROWOP_VERIFY_MAX_DRAFTS 64
 

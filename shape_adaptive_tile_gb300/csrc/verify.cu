@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     const int n = refused;
     const RowStats st = whole[n];
     int token = -1;
-    if (ok(st)) {  // alike for all CTAs of the cluster
+    if (ok(st)) {  // alike for all CTAs of the sequence
         if (kGreedy) {
             token = st.best;
         } else {
