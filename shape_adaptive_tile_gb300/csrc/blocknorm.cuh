@@ -15,7 +15,7 @@
 // 87 us (6.15 TB/s, 90%); 2049 x 5001 fp32, whose rows move four bytes at a
 // time, 36 us (67%); backward 16384 x 4096 bf16 on an fp32 stream 206 us (5.87
 // TB/s, 86%); 4593 x 1537 fp16 with Layer norms, whose elements move by
-// themselves, 71 us (18%: the instructions bound it, 824 for a warp's 256 elements).
+// themselves, 70 us (18%: the instructions bound it, 830 for a warp's 256 elements).
 #pragma once
 
 #include "blocknorm.h"

@@ -2,8 +2,10 @@
 //
 // Of many rows a CTA takes one at a time, with two passes over its logits: the
 // maximum and the sum of exponentials, and the gradient. The second pass finds
-// the row in L2, as the rows at hand in all SMs fit there, so HBM sees 4 bytes a
-// token in 16-bit types, which its bandwidth bounds.
+// the row in L2, mostly: the rows at hand in all SMs are 60 MB at most with 128
+// threads a CTA, 80 with 256, 120 with 512, and with 1024 as long as 152 rows are
+// (159 MB at 262144 tokens in fp32). DRAM reads of a row: 1.0 times at 32768
+// tokens in 16-bit types, 1.2 at 131072, 1.14 at 262144. HBM bandwidth bounds it.
 //
 // Few rows, and the gradient alone, go in slices that lie in shared memory
 // while a CTA works on them: fetched by bulk copies (all of a slice in flight
@@ -15,8 +17,8 @@
 //
 // Measured on a GB300, of its copy rate of 6.8 TB/s: 4096 x 131072 bf16 with its
 // gradient, an eighth of the rows masked, 361 us (5.58 TB/s, 82%); the loss of
-// 1000 x 49999 fp32 36.9 us (80%); the gradient alone of 2047 x 65537 fp16, in
-// slices, 88 us (90%); 7 x 32000, in slices, 7.2 us, a chain of latencies.
+// 1000 x 49999 fp32 36.6 us (81%); the gradient alone of 2047 x 65537 fp16, in
+// slices, 89 us (89%); 7 x 32000, in slices, 7.3 us, a chain of latencies.
 #include "ptx.cuh"
 #include "rows.cuh"
 

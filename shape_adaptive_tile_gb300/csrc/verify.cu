@@ -10,9 +10,9 @@
 // last of them to finish has the winner. The second kernel's CTAs start while
 // the first one's last ones run.
 //
-// Measured on a GB300: 64 x 5 drafts of 131072 tokens in bf16 40 us, of which the
+// Measured on a GB300: 64 x 5 drafts of 131072 tokens in bf16 39 us, of which the
 // first kernel 23 (134 MB, 70% of the DRAM rate) and the race most of the rest:
-// its loads' latency bounds it. 193 x 3 of 65537 in fp16 38 us; 1 x 4 of 32768
+// its loads' latency bounds it. 193 x 3 of 65537 in fp16 39 us; 1 x 4 of 32768
 // 10 us, a chain of two kernels' latencies. One kernel with a cluster a sequence
 // took 55 us for the first of these, a CTA a part of a row 56.
 #include "rows.cuh"
