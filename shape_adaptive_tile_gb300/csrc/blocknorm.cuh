@@ -180,10 +180,11 @@ __device__ __forceinline__ float sum_of(uint64_t v)
     return f.x + f.y;
 }
 
-// The gate row of row r, by a 32-bit division (there are fewer than 2^31 rows). Without a gate rows_per_gate may be 0.
+// The gate row of row r, by a 32-bit division (there are fewer than 2^31 rows); where there is a gate, as
+// rows_per_gate may be 0 without one.
 __device__ __forceinline__ int64_t gate_row(const rowop_block_norm_args& a, int64_t r)
 {
-    return !a.gate || a.rows_per_gate >= a.rows ? 0 : static_cast<uint32_t>(r) / static_cast<uint32_t>(a.rows_per_gate);
+    return a.rows_per_gate >= a.rows ? 0 : static_cast<uint32_t>(r) / static_cast<uint32_t>(a.rows_per_gate);
 }
 
 // The thread's group i of gate row k, in the gate's type: the block's or fp32
@@ -598,7 +599,7 @@ __global__ void __launch_bounds__(NT == 32 ? 128 : NT) sat_block_norm_kernel(con
         constexpr bool kEarly = NV == 1;
         Group early[kEarly ? kWeights : 1];
         auto read = [&](int w, int i) {
-            return w == kGateW ? gate_group<kPack, NT, B>(a, gate_row(a, r), lane, i, 0, width)
+            return w == kGateW ? (a.gate ? gate_group<kPack, NT, B>(a, gate_row(a, r), lane, i, 0, width) : fill(1.0f))
                                : load_weights<kPack, NT>(weight_vector(a, w), w >= kPreBetaW ? 0.0f : 1.0f, lane, i, width);
         };
         if constexpr (kEarly) {
