@@ -113,8 +113,83 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
+// The factors of a gradient: of logit v it is share 2^((v - from) scale), less
+// the teacher's part.
+struct Gradient {
+    float share, from, scale;
+
+    __device__ __forceinline__ float of(float v) const { return share * ex2((v - from) * scale); }
+};
+
+template <typename T>
+__device__ __forceinline__ uint4 gradient_of(const uint4& w, const Gradient& f)
+{
+    const uint64_t from = pair(-f.from, -f.from), scale = pair(f.scale, f.scale);
+    const uint64_t share = pair(f.share, f.share);
+    uint64_t v[kPairs<T>];
+    unpack_pairs<T>(w, v);
+    float o[kPer16<T>];
+#pragma unroll
+    for (int e = 0; e < kPairs<T>; ++e) {
+        const float2 x = halves(mul2(add2(v[e], from), scale));
+        const float2 y = halves(mul2(pair(ex2(x.x), ex2(x.y)), share));
+        o[2 * e] = y.x, o[2 * e + 1] = y.y;
+    }
+    return pack16<T>(o);
+}
+
+// The gradient of row r by one CTA that takes the row's sums again: a pass over
+// the logits in global memory for them, and one for the gradient, which may be
+// in the logits' place. `sum` is P, c the factor of the whole row. Not inlined:
+// the many rows that never come here would pay for its registers.
+template <typename T>
+__device__ __noinline__ void gradient_of_far_row(const rowop_distill_args& a, int64_t r, const Entries teacher, Softmax* scratch, float sum,
+                                                 float c, float scale)
+{
+    const Packs<T> s(static_cast<const T*>(a.logits) + r * a.ldl, static_cast<int>(a.vocab));
+    T* out = static_cast<T*>(a.dlogits) + r * a.ldd;
+    const int k = static_cast<int>(a.k);
+    Softmax q = Softmax::none();
+    for (int i = s.inside + threadIdx.x; i < s.end; i += kThreads) {
+        const uint4 w[1] = {s.load(i)};
+        q.add(softmax_of<T>(w, scale), scale);
+    }
+    // The elements before and after the whole packs.
+    const int before = s.inside ? min(s.element(1), s.vocab) : 0, after = max(s.element(s.end), before);
+    auto ends = [&](auto f) {
+        for (int j = threadIdx.x; j < before; j += kThreads)
+            f(j);
+        for (int j = after + threadIdx.x; j < s.vocab; j += kThreads)
+            f(j);
+    };
+    ends([&](int j) { q.add(to_f32(s.row[j]), scale); });
+    for (int i = threadIdx.x; i < k; i += kThreads)
+        teacher.at_id[i] = teacher.id[i] >= 0 ? to_f32(s.row[teacher.id[i]]) : 0.0f;
+    __syncwarp();
+    q = cta_softmax<kThreads>(q, scale, scratch);
+    const Gradient f = {c * sum / q.sum, q.max, scale};
+    if (((reinterpret_cast<uint64_t>(out) ^ reinterpret_cast<uint64_t>(s.row)) & 15) == 0) {
+        for (int i = s.inside + threadIdx.x; i < s.end; i += kThreads)
+            *reinterpret_cast<uint4*>(out + s.element(i)) = gradient_of<T>(s.load(i), f);
+        ends([&](int j) { out[j] = from_f32<T>(f.of(to_f32(s.row[j]))); });
+    } else {
+        for (int j = threadIdx.x; j < s.vocab; j += kThreads)
+            out[j] = from_f32<T>(f.of(to_f32(s.row[j])));
+    }
+    __syncthreads();
+    for (int n = threadIdx.x; n < k; n += kThreads) {
+        const float pn = teacher.id[n] >= 0 ? teacher.of(n) : -1.0f;
+        if (pn >= 0.0f)
+            out[teacher.id[n]] = from_f32<T>(f.of(teacher.at_id[n]) - c * pn);
+    }
+}
+
+// CTAs an SM whose registers fit: with short slices as many run.
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kThreads)
+constexpr int kSlicePerSM = MODE == kGrad && sizeof(T) == 2 ? 6 : 5;
+
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kThreads, kSlicePerSM<T, MODE>)
     sat_distill_kernel(const __grid_constant__ rowop_distill_args a, const Slices cut)
 {
     constexpr int N = kPer16<T>;
@@ -129,7 +204,7 @@ __global__ void __launch_bounds__(kThreads)
     const int rank = blockIdx.x % cut.ctas, k = static_cast<int>(a.k);
     const int64_t r = blockIdx.x / cut.ctas;
     const float weight = a.weight ? a.weight[r] : 1.0f;
-    const float scale = over_temperature(a.temperature, kLog2e);
+    const float scale = scale_at(a.temperature);
     const T* row = static_cast<const T*>(a.logits) + r * a.ldl;
     T* out = a.dlogits ? static_cast<T*>(a.dlogits) + r * a.ldd : nullptr;
     // The row, and the slices, as addresses.
@@ -184,9 +259,9 @@ __global__ void __launch_bounds__(kThreads)
         for (int c = 0; c < kMaxChunks && threadIdx.x == 0; ++c)
             wait_bounded<false, kDrainNs>(smem_u32(&bars[c]), parity);
     };
-    // Writes share 2^((v times - from) power) for the logits v of the slice.
-    float share = 0.0f, times = 1.0f, from = 0.0f, power = scale;
-    auto one_of = [&](float v) { return share * ex2(fmaf(v, times, -from) * power); };
+    // Writes share 2^((v - from) scale) for the logits v of the slice.
+    float share = 0.0f, from = 0.0f;
+    auto one_of = [&](float v) { return share * ex2((v - from) * scale); };
     auto write = [&] {
         if (packs == 0)
             return;
@@ -195,8 +270,7 @@ __global__ void __launch_bounds__(kThreads)
         const bool wide = ((reinterpret_cast<uint64_t>(out) ^ start) & 15) == 0;
         const int begin = !wide ? packs : first < 0 ? 1 : 0;
         const int end = wide && first + static_cast<int64_t>(packs) * N > a.vocab ? packs - 1 : packs;
-        const uint64_t times2 = pair(times, times), from2 = pair(-from, -from), power2 = pair(power, power);
-        const uint64_t share2 = pair(share, share);
+        const uint64_t from2 = pair(-from, -from), scale2 = pair(scale, scale), share2 = pair(share, share);
         T* to = out + first;
 #pragma unroll 4
         for (int i = begin + threadIdx.x; i < end; i += kThreads) {
@@ -205,7 +279,7 @@ __global__ void __launch_bounds__(kThreads)
             float o[N];
 #pragma unroll
             for (int e = 0; e < kPairs<T>; ++e) {
-                const float2 x = halves(mul2(fma2(v[e], times2, from2), power2));
+                const float2 x = halves(mul2(add2(v[e], from2), scale2));
                 const float2 y = halves(mul2(pair(ex2(x.x), ex2(x.y)), share2));
                 o[2 * e] = y.x, o[2 * e + 1] = y.y;
             }
@@ -288,20 +362,19 @@ __global__ void __launch_bounds__(kThreads)
         row_sums<kThreads>(sum, sums, turn);
     }
 
-    // Whether the row's sums are taken here. In the gradient's pass the row is then all its first CTA's, which may
-    // read it twice though the gradient goes in the logits' place.
-    const bool sums_here = MODE != kGrad || (!empty && fabsf(lse) > kFarLse<T>);
-    const int ctas = MODE == kGrad && sums_here ? 1 : cut.ctas;
-    if (MODE == kGrad && (empty || rank >= ctas)) {
+    auto factor = [&] { return (a.dloss ? a.dloss[r] : 1.0f) * weight * a.temperature; };
+    if (MODE == kGrad && (empty || fabsf(lse) > kFarLse<T>)) {
         if (any)  // the copies have to land before the CTA ends
             drain(phase);
         if (empty)
             write_zeros();
+        else if (rank == 0)
+            gradient_of_far_row<T>(a, r, teacher, scratch[1], sum[0], factor(), scale);
         return;
     }
     Softmax q = Softmax::none();
-    if (sums_here) {
-        for (int i = rank; i < cut.per_row; i += ctas) {
+    if (MODE != kGrad) {
+        for (int i = rank; i < cut.per_row; i += cut.ctas) {
             if (i != rank)
                 refetch(i);
             __syncthreads();  // the ends are written
@@ -325,7 +398,7 @@ __global__ void __launch_bounds__(kThreads)
         if (failed || stuck)
             q.sum = NAN;
         q = cta_softmax<kThreads>(q, scale, scratch[1]);
-        if (MODE != kGrad && cut.ctas > 1) {
+        if (cut.ctas > 1) {
             cluster_wait();
             if (threadIdx.x < cut.ctas) {
                 const uint32_t at = map_to_cta(smem_u32(&across[rank]), threadIdx.x);
@@ -337,7 +410,7 @@ __global__ void __launch_bounds__(kThreads)
             q = sum_softmax(across, 1, cut.ctas, scale);
         }
         const float log_sum = logf(q.sum);
-        if (MODE != kGrad && rank == 0) {
+        if (rank == 0) {
             float loss[1] = {0.0f};
             for (int i = threadIdx.x; i < k; i += kThreads)
                 if (p[i] != 0.0f)
@@ -357,16 +430,16 @@ __global__ void __launch_bounds__(kThreads)
             write_zeros();
         return;
     }
-    const float c = (a.dloss ? a.dloss[r] : 1.0f) * weight * a.temperature;
-    if (!sums_here) {
-        share = c * sum[0], times = over_temperature(a.temperature), from = lse, power = kLog2e;
+    const float c = factor();
+    if (MODE == kGrad) {
+        share = c * sum[0], from = lse * a.temperature;
     } else {
         share = c * sum[0] / q.sum, from = q.max;
     }
-    const bool resident = sums_here && cut.per_row <= ctas;
-    for (int i = rank; i < cut.per_row; i += ctas) {
+    const bool resident = MODE == kBoth && cut.per_row <= cut.ctas;
+    for (int i = rank; i < cut.per_row; i += cut.ctas) {
         if (!resident) {
-            if (sums_here || i != rank)
+            if (MODE == kBoth || i != rank)
                 refetch(i);
             __syncthreads();
             for (int n = 0; n < kMaxChunks && !stuck; ++n)
@@ -397,31 +470,6 @@ __global__ void __launch_bounds__(kThreads)
 
 constexpr int64_t kSMs = 152;
 
-// The factors of a gradient: of logit v it is share 2^((v times - from) power),
-// less the teacher's part.
-struct Gradient {
-    float share, times, from, power;
-
-    __device__ __forceinline__ float of(float v) const { return share * ex2(fmaf(v, times, -from) * power); }
-};
-
-template <typename T>
-__device__ __forceinline__ uint4 gradient_of(const uint4& w, const Gradient& f)
-{
-    const uint64_t times = pair(f.times, f.times), from = pair(-f.from, -f.from), power = pair(f.power, f.power);
-    const uint64_t share = pair(f.share, f.share);
-    uint64_t v[kPairs<T>];
-    unpack_pairs<T>(w, v);
-    float o[kPer16<T>];
-#pragma unroll
-    for (int e = 0; e < kPairs<T>; ++e) {
-        const float2 x = halves(mul2(fma2(v[e], times, from), power));
-        const float2 y = halves(mul2(pair(ex2(x.x), ex2(x.y)), share));
-        o[2 * e] = y.x, o[2 * e + 1] = y.y;
-    }
-    return pack16<T>(o);
-}
-
 // Sixteen bytes by a load that tells L2 how long to keep them.
 __device__ __forceinline__ uint4 load_hinted(const void* p, uint64_t policy)
 {
@@ -444,7 +492,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sat_distill_row_kernel(const __
     float *p = teacher.p, *log_p = teacher.log_p, *at_id = teacher.at_id;
     int* id = teacher.id;
     const int64_t r = blockIdx.x;
-    const float weight = a.weight ? a.weight[r] : 1.0f, scale = over_temperature(a.temperature, kLog2e);
+    const float weight = a.weight ? a.weight[r] : 1.0f, scale = scale_at(a.temperature);
     const Packs<T> s(static_cast<const T*>(a.logits) + r * a.ldl, vocab);
     T* out = a.dlogits ? static_cast<T*>(a.dlogits) + r * a.ldd : nullptr;
     int turn = 0;
@@ -537,7 +585,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sat_distill_row_kernel(const __
     if (MODE == kLoss)
         return;
     const float c = (a.dloss ? a.dloss[r] : 1.0f) * weight * a.temperature;
-    const Gradient f = {c * sum[0] / q.sum, 1.0f, q.max, scale};
+    const Gradient f = {c * sum[0] / q.sum, q.max, scale};
     if (((reinterpret_cast<uint64_t>(out) ^ reinterpret_cast<uint64_t>(s.row)) & 15) == 0) {
         batches(drop, [&](const uint4(&w)[U], int j, bool all) {
 #pragma unroll

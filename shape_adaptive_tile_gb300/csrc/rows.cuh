@@ -225,9 +225,10 @@ __device__ __forceinline__ float rcp(float x)
     return y;
 }
 
-// 1 / t for a temperature t, or `factor` / t: finite also where t is below the
-// smallest normal number, so that equal logits stay equal (0 times it is 0).
-__device__ __forceinline__ float over_temperature(float t, float factor = 1.0f) { return fminf(factor / t, FLT_MAX); }
+// The scale of a softmax's exponents at temperature t, log2 e / t: finite also
+// where t is below the smallest normal number, so that equal logits stay equal
+// (0 times it is 0).
+__device__ __forceinline__ float scale_at(float t) { return fminf(kLog2e / t, FLT_MAX); }
 
 // Two fp32 values in one 64-bit register, and arithmetic on both at once.
 __device__ __forceinline__ uint64_t pair(float a, float b)

@@ -165,7 +165,7 @@ __device__ __forceinline__ int length_of(const rowop_verify_args& a, int64_t b)
 template <bool kGreedy>
 __device__ __forceinline__ float target_scale(const rowop_verify_args& a)
 {
-    return kGreedy ? kLog2e : over_temperature(a.temperature, kLog2e);
+    return kGreedy ? kLog2e : scale_at(a.temperature);
 }
 
 // All sequences' rows in order (of each the target's 0 .. length, then the
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 4)
             continue;
         const Packs<T> s(target ? static_cast<const T*>(a.target) + (static_cast<int64_t>(b) * (drafts + 1) + r) * a.ldt
                                 : static_cast<const T*>(a.draft) + (static_cast<int64_t>(b) * drafts + r) * a.ldq, vocab);
-        const float scale = target ? target_scale<kGreedy>(a) : over_temperature(a.draft_temperature, kLog2e);
+        const float scale = target ? target_scale<kGreedy>(a) : scale_at(a.draft_temperature);
         const int first = part * (parts.elements / N), last = min(first + more * (parts.elements / N), s.count);
         const int begin = max(first, s.inside), end = min(last, s.end);
         RowStats st = {Softmax::none(), -INFINITY, -1};
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     const int64_t b = blockIdx.x / ctas;
     const int len = length_of(a, b);
     const bool point = kGreedy || !a.draft;
-    const float scale = target_scale<kGreedy>(a), q_scale = point ? 0.0f : over_temperature(a.draft_temperature, kLog2e);
+    const float scale = target_scale<kGreedy>(a), q_scale = point ? 0.0f : scale_at(a.draft_temperature);
     const int rows = len + 1 + (point ? 0 : len);
     auto target_row = [&](int i) { return static_cast<const T*>(a.target) + (b * (drafts + 1) + i) * a.ldt; };
     auto draft_row = [&](int i) { return static_cast<const T*>(a.draft) + (b * drafts + i) * a.ldq; };
