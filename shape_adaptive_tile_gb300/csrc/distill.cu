@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, kSlicePerSM<T, MODE>)
 
 // ---- many rows: a CTA a row -----------------------------------------------------
 
-constexpr int64_t kSMs = 152;
+constexpr int64_t kSMs = 152, kSmemPerSM = 227 * 1024;
 
 // Sixteen bytes by a load that tells L2 how long to keep them.
 __device__ __forceinline__ uint4 load_hinted(const void* p, uint64_t policy)
@@ -672,16 +672,6 @@ cudaError_t launch_rows(const rowop_distill_args& a, int64_t row, cudaStream_t s
 template <typename T, int MODE>
 cudaError_t launch(const rowop_distill_args& a, cudaStream_t s)
 {
-    if constexpr (MODE != kGrad) {
-        // A CTA a row, or a row's slices in a cluster: a row by itself where there are rows for two thirds of the SMs
-        // (about where clusters of four no longer all run at once), or where it is short. (us, row | slices, 16-bit types,
-        // inputs from HBM: with gradient 8 x 16384 7.7 | 7.7, 8 x 32000 8.8 | 8.1, 88 x 32000 11.2 | 11.3, 8 x 131072 17.9 |
-        // 9.6, 100 x 131072 20.5 | 19.5, 114 x 131072 20.5 | 28.2, 304 x 131072 36 | 50; loss 38 x 32000 7.2 | 7.6,
-        // 76 x 50304 10.0 | 8.4, 100 x 131072 12.6 | 12.6, 114 x 131072 12.7 | 17.3.)
-        const int64_t row = a.vocab * static_cast<int64_t>(sizeof(T));
-        if (3 * a.rows >= 2 * kSMs || row <= (MODE == kLoss ? 65536 : 32768))
-            return launch_rows<T, MODE>(a, row, s);
-    }
     // With what a row may need before its start to reach a 16-byte boundary.
     const bool even = aligned(a.logits, 16) && a.ldl * sizeof(T) % 16 == 0;
     const int64_t bytes = a.vocab * static_cast<int64_t>(sizeof(T)) + (even ? 0 : 15);
@@ -697,6 +687,18 @@ cudaError_t launch(const rowop_distill_args& a, cudaStream_t s)
     cut.bytes = static_cast<int>(each < kMaxSlice ? (each + 127) / 128 * 128 : kMaxSlice);
     cut.per_row = static_cast<int>((bytes + cut.bytes - 1) / cut.bytes);
     const int smem = cut.bytes + Entries::room(static_cast<int>(a.k));
+    if constexpr (MODE != kGrad) {
+        // A CTA a row, or a row's slices in a cluster: a row by itself where it is short, where there are rows for two thirds
+        // of the SMs, and from half of them on where the clusters do not all run at once. (us, row | slices, with gradient:
+        // bf16 8 x 16384 7.7 | 7.7, 8 x 32000 8.8 | 8.1, 88 x 32000 11.2 | 11.3, 8 x 131072 17.9 | 9.6, 100 x 131072 20.5 |
+        // 19.5, 114 x 131072 20.5 | 28.2, 304 x 131072 36 | 50; fp32 76 x 102336 24.1 | 19.2 (608 CTAs of 50 KB, four an SM),
+        // 88 x 102336 24.7 | 26.9, 64 x 262144 43.2 | 44.9, 76 x 262144 45.7 | 55.8. Loss: bf16 38 x 32000 7.2 | 7.6, 76 x 50304
+        // 10.0 | 8.4, 100 x 131072 12.6 | 12.6, 114 x 131072 12.7 | 17.3; fp32 64 x 262144 30.3 | 25.1, 76 x 262144 30.6 | 31.1.)
+        const int64_t row = a.vocab * static_cast<int64_t>(sizeof(T));
+        const int64_t fit = kSmemPerSM / (smem + 2048), at_once = kSMs * (fit < kSlicePerSM<T, MODE> ? fit : kSlicePerSM<T, MODE>);
+        if (row <= (MODE == kLoss ? 65536 : 32768) || 3 * a.rows >= 2 * kSMs || (2 * a.rows >= kSMs && a.rows * cut.ctas > at_once))
+            return launch_rows<T, MODE>(a, row, s);
+    }
     auto kernel = sat_distill_kernel<T, MODE>;
     static Prepared prepared;
     const cudaError_t e = prepared.once(reinterpret_cast<const void*>(kernel), kMaxSlice + Entries::room(ROWOP_DISTILL_MAX_K));
