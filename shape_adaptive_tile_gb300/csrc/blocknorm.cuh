@@ -794,28 +794,37 @@ cudaError_t launch_ring(const rowop_block_norm_args& a, cudaStream_t s)
 // Whether rows of over 1024 columns go through the ring, not to a CTA each,
 // whose threads hold a row with room for a second CTA's in the SM: by their
 // number an SM and by what lies in a stage, x's and y's columns of one CTA.
-// Large stages leave few in flight, and where the weights do not fit beside
-// them every row reads those again. Elements that move by themselves
-// (not kPack) cost a CTA a row more. Measured in us, a CTA a row | the ring,
-// inputs from HBM, RMS norms and a shared fp32 gate; b bf16, f fp32, m bf16
-// on an fp32 stream:
+// Large stages leave few in flight; weights that do not fit beside them, and
+// gates that change, are read again for every row. A CTA a row pays more where
+// elements move by themselves (not kPack) and for the Layer norm's further
+// reductions. Measured in us, a CTA a row | the ring, inputs from HBM; b bf16,
+// h fp16, f fp32, m bf16 on an fp32 stream, RMS norms and a shared gate where
+// nothing else is said:
 //   2048 b: 304 rows 4.6 | 6.3, 456 7.1 | 6.7, 4864 43 | 21; f: 456 7.9 | 7.8, 912 12.1 | 10.5
 //   4096 b: 760 11.5 | 11.3, 1216 15.0 | 13.7, 4864 49 | 32; f: 608 11.3 | 12.1, 912 15.6 | 15.1; m: 912 14.1 | 13.7
-//   6144 b: 1216 20.0 | 20.1, 1520 23.3 | 22.3, 4864 60 | 51; f: 1520 29.3 | 30.3, 4864 76 | 88; m: 1520 26.2 | 25.3
+//   6144 b: 1216 20.0 | 20.1, 1520 23.3 | 22.3, 4864 60 | 51; f: 1520 29.3 | 30.3, 4864 76 | 88; m: 1520 26.2 | 25.3;
+//   b, a gate a row: 1520 29.2 | 32.6, 2432 43.8 | 47.7
 //   8192 b: 1520 25.8 | 25.9, 2128 33.5 | 32.3, 4864 67 | 61; f: 4864 96 | 125; m: 4864 78 | 112
 //   12288 b: 304 15.4 | 15.8, 456 19.9 | 19.1, 4864 135 | 104; f: 456 25.9 | 23.1, 4864 177 | 171; m: 4864 155 | 120
 //   16384 b: 380 23.9 | 20.1, 4864 170 | 121; m: 4864 212 | 231; f without weights: 4864 186 | 210
-//   not kPack: 1537 b 1216 14.4 | 14.1, 2432 26.3 | 22.0; 3001 f 1216 16.2 | 17.5, 2432 28.7 | 27.8; 6001 b 304 9.0 |
-//   11.3, 456 15.1 | 13.1; 8001 f 2432 65 | 75; 12001 f 304 21 | 18, 2432 128 | 82; 16001 f 304 25.5 | 25.9, 2432 155 | 144
-template <typename B, typename S, bool kPack>
+//   Layer b: 2048 304 8.7 | 8.8, 608 14.7 | 9.9, 4096 608 15.7 | 12.7, 8192 1216 28 | 38, 16384 456 34.0 | 33.3; f: 4096 608
+//   16.8 | 15.0, 12288 304 25.3 | 22.4, 2432 141 | 124
+//   not kPack: 1537 b 1216 13.2 | 13.9, 2432 24.6 | 22.1; 3255 h 1216 16.4 | 16.4, a gate a row 22.9 | 19.3 (b 16.2 | 19.7);
+//   6001 b 304 9.0 | 11.3, 456 15.1 | 13.1; 8001 f 2432 65 | 75; 12001 f 304 21 | 18, 2432 128 | 82; 16001 f 304 25.5 | 25.9,
+//   2432 155 | 144; Layer b 1281 304 7.8 | 9.0, 608 14.1 | 11.3, 3001 608 16.0 | 14.3, 8001 2432 68 | 82
+template <typename B, typename S, bool kPack, bool kLayer>
 bool ring_pays(const rowop_block_norm_args& a)
 {
-    const bool one = a.width <= 8192;  // CTA, not a pair
-    const int columns = a.width <= 2048 ? 2048 : a.width <= 4096 ? 4096 : a.width <= 6144 || (!one && a.width <= 12288) ? 6144 : 8192;
-    const RingRoom r = ring_room<B, S>(a, columns, a.width <= 4096 ? 4 : 2);
+    const int64_t rows = a.rows, w = a.width;
+    const RingRoom r = ring_room<B, S>(a, w <= 2048 ? 2048 : w <= 4096 ? 4096 : w <= 6144 || (w > 8192 && w <= 12288) ? 6144 : 8192,
+                                       w <= 4096 ? 4 : 2);
+    if (w <= 4096)
+        return rows >= (kLayer ? 4 : !kPack ? 8 : w <= 2048 ? 3 : 6) * kSMs;
+    if (w > 8192)
+        return kLayer ? rows >= 3 * kSMs : !kPack ? rows >= 2 * kSMs : rows >= 3 * kSMs && r.kept && r.stage <= 49 * 1024;
     if (!kPack)
-        return a.width <= 4096 ? a.rows >= 10 * kSMs : one ? a.rows >= 3 * kSMs && r.kept : a.rows >= 2 * kSMs;
-    return a.rows >= (a.width <= 2048 ? 3 : a.width <= 4096 ? 6 : one ? 10 : 3) * kSMs && r.kept && r.stage <= (one ? 40 : 49) * 1024;
+        return rows >= 3 * kSMs && r.kept;
+    return rows >= 10 * kSMs && r.kept && r.stage <= 40 * 1024 && (!a.gate || a.rows_per_gate >= a.rows);
 }
 
 template <typename B, typename S, bool kPack, bool kLayer>
@@ -828,7 +837,7 @@ cudaError_t choose_forward_as(const rowop_block_norm_args& a, cudaStream_t s)
         return launch_forward<B, S, 32, 1, kPack, kLayer>(a, s);
     if (a.width <= 1024)
         return launch_forward<B, S, 128, 1, kPack, kLayer>(a, s);
-    if (!ring_pays<B, S, kPack>(a))
+    if (!ring_pays<B, S, kPack, kLayer>(a))
         return a.width <= 4096   ? launch_forward<B, S, 512, 1, kPack, kLayer>(a, s)
                : a.width <= 8192 ? launch_forward<B, S, 512, 2, kPack, kLayer>(a, s)
                                  : launch_forward<B, S, 512, 4, kPack, kLayer>(a, s);
