@@ -140,16 +140,19 @@ __device__ __forceinline__ uint4 gradient_of(const uint4& w, const Gradient& f)
 
 // The gradient of row r by one CTA that takes the row's sums again: a pass over
 // the logits in global memory for them, and one for the gradient, which may be
-// in the logits' place. `sum` is P, c the factor of the whole row. Not inlined:
-// the many rows that never come here would pay for its registers.
+// in the logits' place. `entries` are the row's, `sum` is P, c the factor of the
+// whole row. Not inlined, and with few registers: the many rows that never come
+// here would pay for them.
 template <typename T>
-__device__ __noinline__ void gradient_of_far_row(const rowop_distill_args& a, int64_t r, const Entries teacher, Softmax* scratch, float sum,
-                                                 float c, float scale)
+__device__ __noinline__ void gradient_of_far_row(const rowop_distill_args& a, int64_t r, void* entries, Softmax* scratch, float sum, float c,
+                                                 float scale)
 {
     const Packs<T> s(static_cast<const T*>(a.logits) + r * a.ldl, static_cast<int>(a.vocab));
     T* out = static_cast<T*>(a.dlogits) + r * a.ldd;
     const int k = static_cast<int>(a.k);
+    const Entries teacher(entries, k);
     Softmax q = Softmax::none();
+#pragma unroll 1
     for (int i = s.inside + threadIdx.x; i < s.end; i += kThreads) {
         const uint4 w[1] = {s.load(i)};
         q.add(softmax_of<T>(w, scale), scale);
@@ -157,26 +160,32 @@ __device__ __noinline__ void gradient_of_far_row(const rowop_distill_args& a, in
     // The elements before and after the whole packs.
     const int before = s.inside ? min(s.element(1), s.vocab) : 0, after = max(s.element(s.end), before);
     auto ends = [&](auto f) {
-        for (int j = threadIdx.x; j < before; j += kThreads)
+#pragma unroll 1
+    for (int j = threadIdx.x; j < before; j += kThreads)
             f(j);
-        for (int j = after + threadIdx.x; j < s.vocab; j += kThreads)
+#pragma unroll 1
+    for (int j = after + threadIdx.x; j < s.vocab; j += kThreads)
             f(j);
     };
     ends([&](int j) { q.add(to_f32(s.row[j]), scale); });
+#pragma unroll 1
     for (int i = threadIdx.x; i < k; i += kThreads)
         teacher.at_id[i] = teacher.id[i] >= 0 ? to_f32(s.row[teacher.id[i]]) : 0.0f;
     __syncwarp();
     q = cta_softmax<kThreads>(q, scale, scratch);
     const Gradient f = {c * sum / q.sum, q.max, scale};
     if (((reinterpret_cast<uint64_t>(out) ^ reinterpret_cast<uint64_t>(s.row)) & 15) == 0) {
-        for (int i = s.inside + threadIdx.x; i < s.end; i += kThreads)
+#pragma unroll 1
+    for (int i = s.inside + threadIdx.x; i < s.end; i += kThreads)
             *reinterpret_cast<uint4*>(out + s.element(i)) = gradient_of<T>(s.load(i), f);
         ends([&](int j) { out[j] = from_f32<T>(f.of(to_f32(s.row[j]))); });
     } else {
-        for (int j = threadIdx.x; j < s.vocab; j += kThreads)
+#pragma unroll 1
+    for (int j = threadIdx.x; j < s.vocab; j += kThreads)
             out[j] = from_f32<T>(f.of(to_f32(s.row[j])));
     }
     __syncthreads();
+#pragma unroll 1
     for (int n = threadIdx.x; n < k; n += kThreads) {
         const float pn = teacher.id[n] >= 0 ? teacher.of(n) : -1.0f;
         if (pn >= 0.0f)
@@ -184,12 +193,15 @@ __device__ __noinline__ void gradient_of_far_row(const rowop_distill_args& a, in
     }
 }
 
-// CTAs an SM whose registers fit: with short slices as many run.
+// CTAs an SM that the registers are to allow, for short slices: the gradient
+// alone in 16-bit types has 40 (us with | without that bound: 3000 x 5000 22.2 |
+// 23.6, 2047 x 65537 77.4 | 78.7, one row of 2048 7.0 | 6.1); the others come to
+// 48 by themselves.
 template <typename T, int MODE>
 constexpr int kSlicePerSM = MODE == kGrad && sizeof(T) == 2 ? 6 : 5;
 
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kThreads, kSlicePerSM<T, MODE>)
+__global__ void __launch_bounds__(kThreads, kSlicePerSM<T, MODE> == 6 ? 6 : 0)
     sat_distill_kernel(const __grid_constant__ rowop_distill_args a, const Slices cut)
 {
     constexpr int N = kPer16<T>;
@@ -369,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, kSlicePerSM<T, MODE>)
         if (empty)
             write_zeros();
         else if (rank == 0)
-            gradient_of_far_row<T>(a, r, teacher, scratch[1], sum[0], factor(), scale);
+            gradient_of_far_row<T>(a, r, slice + cut.bytes, scratch[1], sum[0], factor(), scale);
         return;
     }
     Softmax q = Softmax::none();
