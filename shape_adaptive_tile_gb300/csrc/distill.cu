@@ -18,7 +18,7 @@
 // Measured on a GB300, of its copy rate of 6.8 TB/s: 4096 x 131072 bf16 with its
 // gradient, an eighth of the rows masked, 361 us (5.58 TB/s, 82%); the loss of
 // 1000 x 49999 fp32 36.6 us (81%); the gradient alone of 2047 x 65537 fp16, in
-// slices, 89 us (89%); 7 x 32000, in slices, 7.3 us, a chain of latencies.
+// slices, 86 us (92%); 7 x 32000, in slices, 7.3 us, a chain of latencies.
 #include "ptx.cuh"
 #include "rows.cuh"
 
