@@ -37,9 +37,10 @@ enum Mode { kLoss, kBoth, kGrad };
 
 // The gradient alone comes from lse, whose rounding to 32 bits is a relative
 // error of up to |lse| 2^-24 in q. Rows with more than this (in their logits'
-// type, fp32: 4e-6, 16 bits: 3e-5, an eighth of fp16's rounding) have their sums
-// taken again: rows far from 0, and of the type's lowest value, which have
-// nothing of the sum in lse.
+// type, fp32: 4e-6, 16 bits: 3e-5, a sixteenth of fp16's rounding) have their
+// sums taken again: rows far from 0, and of the type's lowest value, which have
+// nothing of the sum in lse. (us where all rows are, against none: 2047 x 65537
+// fp16 180 | 83, 2048 x 65536 fp32 430 | 157, 7 x 131072 bf16 39 | 5.7.)
 template <typename T>
 constexpr float kFarLse = sizeof(T) == 4 ? 64.0f : 512.0f;
 
