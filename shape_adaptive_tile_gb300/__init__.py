@@ -30,6 +30,9 @@ EXPORTS = ("gemm_plan_create", "gemm_plan_create_config", "gemm_plan_create_ex",
            "rowop_softmax", "rowop_rmsnorm", "rowop_layernorm",
            "rowop_block_norm", "rowop_block_norm_workspace", "rowop_block_norm_backward",
            "rowop_distill", "rowop_distill_backward", "rowop_verify", "rowop_verify_workspace")
+# And every function of include/ffn.h.
+FFN_EXPORTS = ("ffn_gated", "ffn_gated_workspace", "ffn_gated_backward", "ffn_gated_backward_workspace",
+               "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_scale_bytes", "mxfp4_gemm")
 
 _lock = threading.Lock()
 _lib = None
@@ -85,7 +88,8 @@ def lib() -> ctypes.CDLL:
             L.rowop_rmsnorm.restype = i32
             L.rowop_layernorm.argtypes = [vp, i64, vp, vp, vp, i64, i64, i64, f32, vp]
             L.rowop_layernorm.restype = i32
-            for fn in (L.rowop_block_norm, L.rowop_distill, L.rowop_distill_backward, L.rowop_verify):
+            for fn in (L.rowop_block_norm, L.rowop_distill, L.rowop_distill_backward, L.rowop_verify, L.ffn_gated,
+                       L.mxfp4_quantize, L.mxfp4_dequantize, L.mxfp4_gemm):
                 fn.argtypes = [vp, vp]
                 fn.restype = i32
             L.rowop_block_norm_backward.argtypes = [vp, vp, vp]
@@ -94,6 +98,14 @@ def lib() -> ctypes.CDLL:
             L.rowop_block_norm_workspace.restype = i64
             L.rowop_verify_workspace.argtypes = [i64, i64, i64]
             L.rowop_verify_workspace.restype = i64
+            L.ffn_gated_backward.argtypes = [vp, vp, vp]
+            L.ffn_gated_backward.restype = i32
+            L.ffn_gated_workspace.argtypes = [vp]
+            L.ffn_gated_workspace.restype = i64
+            L.ffn_gated_backward_workspace.argtypes = [vp, vp]
+            L.ffn_gated_backward_workspace.restype = i64
+            L.mxfp4_scale_bytes.argtypes = [i64, i64]
+            L.mxfp4_scale_bytes.restype = i64
             L.gemm_run_noalloc.restype = i32
             L.gemm_select_config.argtypes = [i64, i64, i64, i32, i32, i32, ctypes.c_char_p, i32]
             L.gemm_select_config.restype = i32
@@ -194,13 +206,14 @@ def rowop_layernorm(X, ldx: int, gamma, beta, Y, ldy: int, rows: int, width: int
 # ---- row operators of language models (include/rowops.h) ----------------------
 
 NORMS = {"none": 0, "rms": 1, "layer": 2}
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
 
 
 class _Args(ctypes.Structure):
-    """An argument struct of include/rowops.h, filled by keyword.
+    """An argument struct of include/rowops.h or include/ffn.h, filled by keyword.
 
     Pointers may be given as tensors (kept alive by the struct) or addresses,
-    element types and norms by name; fields not given are 0 or NULL. Fill it
+    element types, norms and activations by name; fields not given are 0 or NULL. Fill it
     once and pass it to any number of calls.
     """
 
@@ -219,7 +232,7 @@ class _Args(ctypes.Structure):
             self._keep[name] = value
             value = _p(value)
         elif isinstance(value, str):
-            value = (NORMS if name.endswith("_norm") else C_TYPES)[value]
+            value = (NORMS if name.endswith("_norm") else ACTIVATIONS if name == "activation" else C_TYPES)[value]
         super().__setattr__(name, value)
 
 
@@ -243,6 +256,16 @@ DistillArgs = _struct("DistillArgs", "i64 rows vocab k; i32 logits_type teacher_
 VerifyArgs = _struct("VerifyArgs", "i64 batch drafts vocab; i32 logits_type; f32 temperature draft_temperature;"
                      "ptr target; i64 ldt; ptr draft; i64 ldq; ptr tokens lengths uniforms noise; i64 ldn;"
                      "ptr accepted out logprobs workspace; i64 workspace_bytes", "rowop_verify_args")
+
+FfnArgs = _struct("FfnArgs", "i64 rows width hidden; i32 type activation w_by_output; ptr x; i64 ldx; ptr w; i64 ldw;"
+                  "ptr h; i64 ldh; ptr preact; i64 ldp; ptr workspace; i64 workspace_bytes", "ffn_gated_args")
+FfnGrads = _struct("FfnGrads", "ptr dh; i64 lddh; ptr dx; i64 lddx; ptr dw; i64 lddw; i32 dw_type accumulate;"
+                   "ptr workspace; i64 workspace_bytes", "ffn_gated_grads")
+Mxfp4Args = _struct("Mxfp4Args", "i64 rows width; i32 type reserved; ptr values; i64 ldv; ptr codes; i64 ldc; ptr scales",
+                    "mxfp4_args")
+Mxfp4GemmArgs = _struct("Mxfp4GemmArgs", "i64 rows cols width; i32 out_type activation; f32 alpha; i32 reserved;"
+                        "ptr a_codes; i64 lda; ptr a_scales b_codes; i64 ldb; ptr b_scales up_codes; i64 ldu;"
+                        "ptr up_scales out; i64 ldo", "mxfp4_gemm_args")
 
 
 def _a(args: _Args | None) -> int | None:
@@ -286,6 +309,47 @@ def _size(n: int) -> int:
     if n < 0:
         raise GemmError(n, gemm_last_error())
     return n
+
+
+# ---- feed-forward block (include/ffn.h) ----------------------------------------
+
+
+def ffn_gated(args: FfnArgs, stream=None) -> int:
+    """Both projections, the activation and the product in one kernel (see include/ffn.h)."""
+    return lib().ffn_gated(_a(args), _p(stream))
+
+
+def ffn_gated_workspace(args: FfnArgs) -> int:
+    """Scratch bytes of ffn_gated."""
+    return _size(lib().ffn_gated_workspace(_a(args)))
+
+
+def ffn_gated_backward(args: FfnArgs, grads: FfnGrads, stream=None) -> int:
+    return lib().ffn_gated_backward(_a(args), _a(grads), _p(stream))
+
+
+def ffn_gated_backward_workspace(args: FfnArgs, grads: FfnGrads) -> int:
+    """Scratch bytes of ffn_gated_backward."""
+    return _size(lib().ffn_gated_backward_workspace(_a(args), _a(grads)))
+
+
+def mxfp4_quantize(args: Mxfp4Args, stream=None) -> int:
+    """Microscaled 4-bit codes and scales of a matrix (see include/ffn.h)."""
+    return lib().mxfp4_quantize(_a(args), _p(stream))
+
+
+def mxfp4_dequantize(args: Mxfp4Args, stream=None) -> int:
+    return lib().mxfp4_dequantize(_a(args), _p(stream))
+
+
+def mxfp4_scale_bytes(rows: int, width: int) -> int:
+    """Bytes of a microscaled matrix's scales."""
+    return _size(lib().mxfp4_scale_bytes(rows, width))
+
+
+def mxfp4_gemm(args: Mxfp4GemmArgs, stream=None) -> int:
+    """Products of microscaled matrices, gated where `up` is given (see include/ffn.h)."""
+    return lib().mxfp4_gemm(_a(args), _p(stream))
 
 
 def gemm_plan_destroy(plan: int) -> None:

@@ -28,7 +28,7 @@ STAMP = os.path.join(LIB_DIR, "libsatgemm.stamp")
 SOURCES = [f"kernels_{dt}{grp}.cu" for grp in ("", "_alt", "_trans") for dt in ("tf32", "bf16", "fp16")] + [
     "device_call.cu"] + [f"blocknorm_{d}_{dt}.cu" for d in ("backward", "forward") for dt in ("bf16", "f16", "f32")] + [
     "api.cu", "aux_kernels.cu", "dispatch.cpp", "tensor_map.cpp", "noalloc.cu", "rowops.cu", "blocknorm.cu", "distill.cu",
-    "verify.cu"]
+    "verify.cu", "ffn.cu", "ffn_tiles_half.cu", "ffn_tiles_grad.cu", "ffn_tiles_mx.cu", "mxfp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 # The GEMM kernel units: an explicit register ceiling (the launch bounds of
@@ -46,7 +46,8 @@ def _nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC))]
-    files += [os.path.join(INCLUDE, "gemm.h"), os.path.join(INCLUDE, "rowops.h"), os.path.join(INCLUDE, "gemm_device.cuh")]
+    files += [os.path.join(INCLUDE, "gemm.h"), os.path.join(INCLUDE, "rowops.h"), os.path.join(INCLUDE, "gemm_device.cuh"),
+              os.path.join(INCLUDE, "ffn.h")]
     return [f for f in files if os.path.isfile(f)]
 
 
@@ -72,17 +73,17 @@ def source_hash() -> str:
     return h.hexdigest()[:16]
 
 
-# Sources of the row operators only: no GEMM kernel includes or calls them.
-_ROWOP_ONLY = ("rowops.cu", "rowops.h", "rows.cuh", "distill.cu", "verify.cu")
+# Sources of the row and feed-forward operators only: no GEMM kernel includes or calls them.
+_ROWOP_ONLY = ("rowops.cu", "rowops.h", "rows.cuh", "distill.cu", "verify.cu", "mxfp4.cu")
 
 
 def _rowop_only(name: str) -> bool:
-    return name in _ROWOP_ONLY or name.startswith("blocknorm")
+    return name in _ROWOP_ONLY or name.startswith(("blocknorm", "ffn"))
 
 
 def gemm_source_hash() -> str:
     """SHA-256 of the sources the GEMM kernels are built from: every input but
-    the row operators' own files, comments and layout aside. A profile of a
+    the row and feed-forward operators' own files, comments and layout aside. A profile of a
     GEMM kernel stays valid as long as this is unchanged."""
     h = hashlib.sha256()
     for f in _inputs():

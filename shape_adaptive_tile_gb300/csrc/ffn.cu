@@ -1,0 +1,709 @@
+// The gated product, its gradients and the products of microscaled matrices
+// (include/ffn.h): checks of arguments, tensor maps, and the choice of a tile
+// kernel (ffn_tile.cuh).
+#include "ffn.h"
+
+#include <algorithm>
+#include <mutex>
+
+#include "ffn_tile.cuh"
+#include "rows.cuh"
+
+namespace sat {
+namespace ffn {
+
+extern const Variant kHalfTiles[], kGradTiles[], kScaledTiles[];
+extern const int kNumHalfTiles, kNumGradTiles, kNumScaledTiles;
+
+const Variant* find_variant(int mx, int epi, int cg, int bn, int p_mn, int q_mn, int swap)
+{
+    const Variant* tab[3] = {kHalfTiles, kGradTiles, kScaledTiles};
+    const int num[3] = {kNumHalfTiles, kNumGradTiles, kNumScaledTiles};
+    for (int g = 0; g < 3; ++g)
+        for (int i = 0; i < num[g]; ++i) {
+            const Variant& v = tab[g][i];
+            if (v.mx == mx && v.epi == epi && v.cg == cg && v.bn == bn && v.p_mn == p_mn && v.q_mn == q_mn && v.swap == swap)
+                return &v;
+        }
+    return nullptr;
+}
+
+}  // namespace ffn
+}  // namespace sat
+
+namespace {
+
+using namespace sat;
+using namespace sat::rows;
+using namespace sat::ffn;
+
+constexpr int64_t kMost = INT64_C(1) << 31;
+constexpr unsigned long long kTimeoutNs = 2000000000ull;
+
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+int64_t ceil_div(int64_t n, int64_t by) { return (n + by - 1) / by; }
+
+// The current device's SMs, or a status.
+int device_sms(int* sms)
+{
+    static std::atomic<int> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return fail_with(GEMM_ERR_LAUNCH, "querying the device: %s", cudaGetErrorString(e));
+    int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        int major = 0, minor = 0;
+        e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+        if (e == cudaSuccess)
+            e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+        if (e == cudaSuccess)
+            e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess)
+            return fail_with(GEMM_ERR_LAUNCH, "querying the device: %s", cudaGetErrorString(e));
+        if (major != 10 || minor != 3)
+            return fail_with(GEMM_ERR_ARCH, "device %d is compute capability %d.%d; this library is built for sm_103a only",
+                             dev, major, minor);
+        if (dev < 64)
+            known[dev].store(n, std::memory_order_relaxed);
+    }
+    *sms = n;
+    return GEMM_OK;
+}
+
+// One factor of a product: `extent` rows (or columns) of the output by k. mn:
+// extent is the contiguous one, else k is. Two pointers: two segments of k, two
+// products of a batch, or the gate's and the other weights.
+struct Factor {
+    const void* at[2];
+    int64_t ld, extent;
+    bool mn;
+    const void* scales[2];
+    int64_t ld1 = 0;  // the second one's stride, where it is another
+};
+
+struct Product {
+    int epi, mx;
+    Factor x, w;        // x gives the output's rows, w its columns
+    bool w_is_weights;  // w may be the first operand for a few rows
+    int64_t k;          // of one segment
+    int segments, batch;
+    int type;           // of 16-bit operands
+    int activation, keep, add, out_type;
+    float alpha;
+    int64_t rows, cols;  // of one output
+    void* out[3];
+    int64_t ld[3];
+    bool padded;  // the outputs' rows go on to a whole number of 16 bytes that nobody reads
+    const void* dh;
+    int64_t lddh;
+};
+
+int map_error(int rc)
+{
+    return rc == -1 ? fail_with(GEMM_ERR_LAUNCH, "cuTensorMapEncodeTiled is not available from the driver")
+                    : fail_with(GEMM_ERR_LAUNCH, "cuTensorMapEncodeTiled failed (%d)", rc);
+}
+
+CUtensorMapDataType map_type(int type)
+{
+    return type == GEMM_C_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+           : type == GEMM_C_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
+int encode_factor(CUtensorMap* map, const Product& p, const Factor& f, int i, int box_rows)
+{
+    const uint64_t extent = static_cast<uint64_t>(f.extent), k = static_cast<uint64_t>(p.k), ld = static_cast<uint64_t>(i && f.ld1 ? f.ld1 : f.ld);
+    int rc;
+    if (p.mx)
+        rc = encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, f.at[i], (k + 31) / 32 * 16, extent, ld, 128,
+                        static_cast<uint32_t>(box_rows), CU_TENSOR_MAP_SWIZZLE_128B);
+    else if (f.mn)
+        rc = encode_map(map, map_type(p.type), 2, f.at[i], extent, k, ld, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+    else
+        rc = encode_map(map, map_type(p.type), 2, f.at[i], k, extent, ld, 64, static_cast<uint32_t>(box_rows),
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+    return rc ? map_error(rc) : GEMM_OK;
+}
+
+// Scales as rows of 512 bytes, one for each tile of 128 rows x 4 blocks, read two at a time.
+int encode_scales(CUtensorMap* map, const Product& p, const Factor& f, int i)
+{
+    const int rc = encode_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, f.scales[i], 128,
+                              static_cast<uint64_t>(ceil_div(f.extent, 128) * ceil_div(p.k, 128)), 128, 128, 2,
+                              CU_TENSOR_MAP_SWIZZLE_NONE);
+    return rc ? map_error(rc) : GEMM_OK;
+}
+
+int launch_product(const Product& p, int sms, cudaStream_t stream)
+{
+    const bool gated = p.epi != kStore;
+    const int64_t bk = p.mx ? 256 : 64;
+    const int64_t num_kb = ceil_div(p.k, bk) * p.segments;
+    // A few rows: the weights are the first operand, so that no accumulator row goes unused.
+    const bool swap = p.w_is_weights && p.rows <= 64;
+    const Variant* v = nullptr;
+    int cluster = 1, grid = 0;
+    int64_t tp = 0, tq = 0;
+    if (swap) {
+        v = find_variant(p.mx, p.epi, 1, p.rows <= 16 ? 16 : p.rows <= 32 ? 32 : 64, p.w.mn, p.x.mn, 1);
+        tp = ceil_div(p.cols, 128);
+        tq = ceil_div(p.rows, v->bn);
+    } else {
+        const int64_t pairs = ceil_div(p.rows, 256) * ceil_div(p.cols, gated ? 128 : 256) * p.batch;
+        if (pairs >= sms / 2) {
+            v = find_variant(p.mx, p.epi, 2, 256, p.x.mn, p.w.mn, 0);
+            cluster = 2;
+        } else {
+            v = find_variant(p.mx, p.epi, 1, p.mx && gated ? 256 : 128, p.x.mn, p.w.mn, 0);
+        }
+        tp = ceil_div(p.rows, 128 * v->cg);
+        tq = ceil_div(p.cols, gated ? v->bn / 2 : v->bn);
+    }
+    const int64_t tiles = tp * tq * p.batch;
+    if (tiles * 16 >= kMost)
+        return fail_with(GEMM_ERR_ARG, "too many tiles");
+    TileArgs a{};
+    if (v->persistent) {
+        grid = static_cast<int>(std::min<int64_t>(tiles, sms / v->cg)) * v->cg;
+    } else {
+        // Share k among as many CTAs as fill the SMs, of four k-blocks at least, while the sums fit in the ring.
+        int64_t s = 1;
+        while (s < 8 && tiles * (s + 1) <= sms && num_kb / (s + 1) >= 4 &&
+               s * ceil_div(v->chunks, s + 1) * v->part_bytes <= v->ring_bytes)
+            ++s;
+        cluster = static_cast<int>(s);
+        grid = static_cast<int>(tiles * s);
+    }
+    a.tiles_p = static_cast<int>(tp);
+    a.tiles_q = static_cast<int>(tq);
+    a.batch = p.batch;
+    a.num_kb = static_cast<int>(num_kb);
+    a.seg_kb = static_cast<int>(num_kb / p.segments);
+    a.tail_steps = p.mx ? static_cast<int>(ceil_div(p.k - (num_kb - 1) * 256, 64)) : 4;
+    a.kb_per_rank = v->persistent ? a.num_kb : static_cast<int>(std::max<int64_t>(1, ceil_div(num_kb, cluster)));
+    a.group = v->cg == 2 ? 8 : 16;
+    a.idesc = p.mx ? idesc_mxf4(128 * v->cg, v->bn)
+                   : idesc_f32acc(p.type == GEMM_C_BF16 ? kFmtBF16 : kFmtF16, 128 * v->cg, v->bn, v->q_mn != 0, v->p_mn != 0);
+    a.alpha = p.alpha;
+    a.activation = p.activation;
+    a.out_kind = p.out_type;
+    a.add = p.add;
+    a.keep = p.keep;
+    a.rows = static_cast<int>(p.rows);
+    a.cols = static_cast<int>(p.cols);
+    a.timeout_ns = kTimeoutNs;
+    const int outs = p.epi == kStore ? p.batch : p.epi == kGrad ? 2 : p.keep ? 3 : 1;
+    TileMaps m{};
+    ScaleMaps sm{};
+    const Factor &first = swap ? p.w : p.x, &second = swap ? p.x : p.w;
+    const int qbox = std::min(64, v->bn / v->cg);
+    // The second pointers: of a gated product the weights' only; of segments or a batch both factors'.
+    const bool two_first = gated ? swap : p.segments * p.batch > 1, two_second = gated ? !swap : p.segments * p.batch > 1;
+    int rc = GEMM_OK;
+    for (int i = 0; i < 2 && !rc; ++i) {
+        if (i == 0 || two_first)
+            rc = encode_factor(&m.p[i], p, first, i, 128);
+        if (!rc && (i == 0 || two_second))
+            rc = encode_factor(&m.q[i], p, second, i, qbox);
+        if (p.mx) {
+            if (!rc && (i == 0 || two_first))
+                rc = encode_scales(&sm.p[i], p, first, i);
+            if (!rc && (i == 0 || two_second))
+                rc = encode_scales(&sm.q[i], p, second, i);
+        }
+    }
+    a.sf_rows_p = a.sf_rows_q = p.mx ? static_cast<int>(ceil_div(p.k, 128)) : 0;
+    const int es = type_bytes(p.out_type);
+    for (int i = 0; i < outs && !rc; ++i) {
+        a.out[i] = p.out[i];
+        a.ld[i] = p.ld[i];
+        if (!swap && aligned(p.out[i], 16) && p.ld[i] * es % 16 == 0) {
+            a.tma_out |= 1 << i;
+            if (p.padded || p.cols * es % 16 == 0)
+                a.tma_edge |= 1 << i;
+            const int e = encode_map(&m.o[i], map_type(p.out_type), es, p.out[i], static_cast<uint64_t>(p.cols),
+                                     static_cast<uint64_t>(p.rows), static_cast<uint64_t>(p.ld[i]), static_cast<uint32_t>(128 / es),
+                                     32, CU_TENSOR_MAP_SWIZZLE_128B);
+            rc = e ? map_error(e) : GEMM_OK;
+        }
+    }
+    if (!rc && p.epi == kGrad) {
+        const int e = encode_map(&m.o[2], map_type(p.type), 2, p.dh, static_cast<uint64_t>(p.cols), static_cast<uint64_t>(p.rows),
+                                 static_cast<uint64_t>(p.lddh), 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+        rc = e ? map_error(e) : GEMM_OK;
+    }
+    if (rc)
+        return rc;
+    const cudaError_t e = v->launch(m, p.mx ? &sm : nullptr, a, grid, cluster, stream);
+    return e == cudaSuccess ? GEMM_OK : fail_with(GEMM_ERR_LAUNCH, "launching a tile kernel: %s", cudaGetErrorString(e));
+}
+
+// ---- gated product ------------------------------------------------------------
+
+bool rows16(const void* p, int64_t ld) { return aligned(p, 16) && ld * 2 % 16 == 0; }
+
+// A copy's row stride in elements: whole 128-byte lines, an odd number of them (rows do not repeat at a power of two).
+int64_t packed_ld(int64_t n)
+{
+    const int64_t lines = ceil_div(n * 2, 128);
+    return (lines | 1) * 64;
+}
+
+// What is copied into aligned rows first, and where: byte offsets into the workspace.
+struct Copies {
+    bool x, w, dh;
+    int64_t ldx, ldw, lddh;
+    int64_t at_x, at_w, at_w2, at_dh, end;
+};
+
+Copies copies_of(const ffn_gated_args& a, const void* dh, int64_t lddh, bool uses_x, int64_t at)
+{
+    Copies k{};
+    k.x = uses_x && !rows16(a.x, a.ldx);
+    k.w = !rows16(a.w, a.ldw) || (!a.w_by_output && a.hidden % 8 != 0);
+    k.dh = dh && !rows16(dh, lddh);
+    if (k.x) {
+        k.ldx = packed_ld(a.width);
+        k.at_x = at;
+        at += a.rows * k.ldx * 2;
+    }
+    if (k.w) {
+        k.ldw = packed_ld(a.w_by_output ? a.width : a.hidden);
+        k.at_w = at;
+        k.at_w2 = at + (a.w_by_output ? a.hidden : a.width) * k.ldw * 2;
+        at += 2 * (a.w_by_output ? a.hidden : a.width) * k.ldw * 2;
+    }
+    if (k.dh) {
+        k.lddh = packed_ld(a.hidden);
+        k.at_dh = at;
+        at += a.rows * k.lddh * 2;
+    }
+    k.end = at;
+    return k;
+}
+
+int check(const ffn_gated_args* a)
+{
+    if (!a)
+        return fail_with(GEMM_ERR_ARG, "args is NULL");
+    if (a->rows < 0 || a->width < 0 || a->hidden < 0 || a->rows >= kMost || a->width >= kMost || 2 * a->hidden >= kMost)
+        return fail_with(GEMM_ERR_ARG, "sizes must be in [0, 2^31)");
+    if (a->type != GEMM_C_BF16 && a->type != GEMM_C_F16)
+        return fail_with(GEMM_ERR_ARG, "type must be bf16 or fp16");
+    if (a->activation < FFN_NONE || a->activation > FFN_RELU)
+        return fail_with(GEMM_ERR_ARG, "unknown activation %d", a->activation);
+    if (a->rows > 0 && a->width > 0 && a->hidden > 0) {
+        if (!a->x || !a->w)
+            return fail_with(GEMM_ERR_ARG, "x or w is NULL");
+        if (a->ldx < a->width || a->ldw < (a->w_by_output ? a->width : 2 * a->hidden))
+            return fail_with(GEMM_ERR_ARG, "row stride of x or w below the row");
+        if (!aligned(a->x, 2) || !aligned(a->w, 2))
+            return fail_with(GEMM_ERR_ALIGN, "x or w is not aligned to its elements");
+    }
+    if (a->rows > 0 && a->hidden > 0 && a->preact) {
+        if (a->ldp < 2 * a->hidden)
+            return fail_with(GEMM_ERR_ARG, "row stride of preact below the row");
+        if (!aligned(a->preact, 2))
+            return fail_with(GEMM_ERR_ALIGN, "preact is not aligned to its elements");
+    }
+    if (a->ldx >= kMost || a->ldw >= kMost || a->ldp >= kMost || a->ldh >= kMost)
+        return fail_with(GEMM_ERR_ARG, "row strides must be below 2^31");
+    return GEMM_OK;
+}
+
+int check_workspace(const void* at, int64_t bytes, int64_t need, const char* fn)
+{
+    if (need == 0)
+        return GEMM_OK;
+    if (!at || bytes < need)
+        return fail_with(GEMM_ERR_ARG, "workspace is NULL or below %s()", fn);
+    if (!aligned(at, 16))
+        return fail_with(GEMM_ERR_ALIGN, "workspace is not aligned to 16 bytes");
+    return GEMM_OK;
+}
+
+int cuda_rc(cudaError_t e, const char* what)
+{
+    return e == cudaSuccess ? GEMM_OK : fail_with(GEMM_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// Copies what needs it, and gives x, the weights and dh as they are read.
+int pack(const ffn_gated_args& a, const Copies& k, const void* dh, int64_t lddh, void* workspace, int sms, cudaStream_t s,
+         Factor* x, Factor* w, Factor* d)
+{
+    char* ws = static_cast<char*>(workspace);
+    const char *wp = static_cast<const char*>(a.w);
+    cudaError_t e = cudaSuccess;
+    x->at[0] = a.x;
+    x->ld = a.ldx;
+    if (k.x) {
+        e = launch_pack_rows(a.x, a.ldx * 2, ws + k.at_x, k.ldx * 2, a.rows, a.width * 2, sms, s);
+        x->at[0] = ws + k.at_x;
+        x->ld = k.ldx;
+    }
+    const int64_t half = a.w_by_output ? a.hidden * a.ldw * 2 : a.hidden * 2;  // bytes from the gate's weights to the others
+    w->at[0] = wp;
+    w->at[1] = wp + half;
+    w->ld = a.ldw;
+    if (k.w) {
+        const int64_t rows = a.w_by_output ? a.hidden : a.width, bytes = (a.w_by_output ? a.width : a.hidden) * 2;
+        for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+            e = launch_pack_rows(w->at[i], a.ldw * 2, ws + (i ? k.at_w2 : k.at_w), k.ldw * 2, rows, bytes, sms, s);
+        w->at[0] = ws + k.at_w;
+        w->at[1] = ws + k.at_w2;
+        w->ld = k.ldw;
+    }
+    d->at[0] = dh;
+    d->ld = lddh;
+    if (k.dh) {
+        if (e == cudaSuccess)
+            e = launch_pack_rows(dh, lddh * 2, ws + k.at_dh, k.lddh * 2, a.rows, a.hidden * 2, sms, s);
+        d->at[0] = ws + k.at_dh;
+        d->ld = k.lddh;
+    }
+    return cuda_rc(e, "launching a copy into aligned rows");
+}
+
+// dg and du of eight columns a thread, from the pre-activations.
+struct SlopeArgs {
+    long long rows, hidden, units;  // units: eight columns
+    const void* dh;
+    const void* preact;
+    void* dz;  // [dg du], the second half `half` elements after the first
+    long long lddh, ldp, ldz, half;
+    int activation;
+};
+
+template <typename T>
+__device__ __forceinline__ Pack<T> load_at(const T* p, long long left, bool vec)
+{
+    if (vec && left >= 8)
+        return load_pack(p);
+    Pack<T> v{};
+    for (int i = 0; i < 8 && i < left; ++i)
+        reinterpret_cast<T*>(v.w)[i] = p[i];
+    return v;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) sat_ffn_slope_kernel(const SlopeArgs a, const bool dh_vec, const bool p_vec)
+{
+    const long long unit = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    const long long r = unit / a.units, j = (unit - r * a.units) * 8;
+    if (r >= a.rows)
+        return;
+    const long long left = a.hidden - j;
+    const T* pre = static_cast<const T*>(a.preact) + r * a.ldp + j;
+    const Pack<T> d = load_at(static_cast<const T*>(a.dh) + r * a.lddh + j, left, dh_vec);
+    const Pack<T> g = load_at(pre, left, p_vec), u = load_at(pre + a.hidden, left, p_vec);
+    Pack<T> dg, du;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float dv = to_f32(reinterpret_cast<const T*>(d.w)[i]);
+        float v, slope;
+        act_grad(to_f32(reinterpret_cast<const T*>(g.w)[i]), a.activation, v, slope);
+        reinterpret_cast<T*>(dg.w)[i] = from_f32<T>(dv * to_f32(reinterpret_cast<const T*>(u.w)[i]) * slope);
+        reinterpret_cast<T*>(du.w)[i] = from_f32<T>(dv * v);
+    }
+    // Rows of dz are whole eights of columns: what lies past `hidden` is never read.
+    T* z = static_cast<T*>(a.dz) + r * a.ldz + j;
+    store_pack(z, dg);
+    store_pack(z + a.half, du);
+}
+
+template <typename T>
+cudaError_t launch_slope(const SlopeArgs& a, cudaStream_t s)
+{
+    const bool dh_vec = aligned(a.dh, 16) && a.lddh % 8 == 0;
+    const bool p_vec = aligned(a.preact, 16) && a.ldp % 8 == 0 && a.hidden % 8 == 0;
+    const long long grid = ceil_div(a.rows * a.units, 256);
+    if (grid >= kMost)
+        return cudaErrorInvalidConfiguration;
+    sat_ffn_slope_kernel<T><<<static_cast<unsigned>(grid), 256, 0, s>>>(a, dh_vec, p_vec);
+    return cudaGetLastError();
+}
+
+int check_backward(const ffn_gated_args* a, const ffn_gated_grads* g)
+{
+    const int rc = check(a);
+    if (rc)
+        return rc;
+    if (!g)
+        return fail_with(GEMM_ERR_ARG, "grads is NULL");
+    if (g->dw_type != GEMM_C_F32 && g->dw_type != a->type && g->dw)
+        return fail_with(GEMM_ERR_ARG, "dw_type must be fp32 or args->type");
+    if (g->accumulate && g->dw && g->dw_type != GEMM_C_F32)
+        return fail_with(GEMM_ERR_ARG, "accumulate needs dw in fp32");
+    if (a->rows > 0 && a->hidden > 0 && (g->dx || g->dw) && a->width > 0) {
+        if (!g->dh)
+            return fail_with(GEMM_ERR_ARG, "dh is NULL");
+        if (g->lddh < a->hidden)
+            return fail_with(GEMM_ERR_ARG, "row stride of dh below the row");
+        if (!aligned(g->dh, 2))
+            return fail_with(GEMM_ERR_ALIGN, "dh is not aligned to its elements");
+    }
+    if (g->dx && a->rows > 0 && a->width > 0 && g->lddx < a->width)
+        return fail_with(GEMM_ERR_ARG, "row stride of dx below the row");
+    if (g->dw && a->width > 0 && a->hidden > 0 && g->lddw < (a->w_by_output ? a->width : 2 * a->hidden))
+        return fail_with(GEMM_ERR_ARG, "row stride of dw below the row");
+    if (!aligned(g->dx, 2) || (g->dw && !aligned(g->dw, type_bytes(g->dw_type))))
+        return fail_with(GEMM_ERR_ALIGN, "dx or dw is not aligned to its elements");
+    if (g->lddh >= kMost || g->lddx >= kMost || g->lddw >= kMost)
+        return fail_with(GEMM_ERR_ARG, "row strides must be below 2^31");
+    return GEMM_OK;
+}
+
+// The backward pass's workspace: [dg du] with both halves' rows on 16 bytes, then copies.
+int64_t dz_ld(const ffn_gated_args& a) { return 2 * round_up(a.hidden, 8); }
+
+Copies backward_copies(const ffn_gated_args& a, const ffn_gated_grads& g)
+{
+    return copies_of(a, a.preact ? nullptr : g.dh, g.lddh, !a.preact || g.dw, round_up(a.rows * dz_ld(a) * 2, 128));
+}
+
+bool backward_empty(const ffn_gated_args& a, const ffn_gated_grads& g)
+{
+    return a.rows == 0 || a.width == 0 || a.hidden == 0 || (!g.dx && !g.dw);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t ffn_gated_workspace(const ffn_gated_args* args)
+{
+    set_last_error("");
+    const int rc = check(args);
+    if (rc)
+        return rc;
+    if (args->rows == 0 || args->width == 0 || args->hidden == 0)
+        return 0;
+    return copies_of(*args, nullptr, 0, true, 0).end;
+}
+
+int ffn_gated(const ffn_gated_args* args, void* stream)
+{
+    set_last_error("");
+    int rc = check(args);
+    if (rc || args->rows == 0 || args->hidden == 0)
+        return rc;
+    const ffn_gated_args& a = *args;
+    if (!a.h)
+        return fail_with(GEMM_ERR_ARG, "h is NULL");
+    if (a.ldh < a.hidden)
+        return fail_with(GEMM_ERR_ARG, "row stride of h below the row");
+    if (!aligned(a.h, 2))
+        return fail_with(GEMM_ERR_ALIGN, "h is not aligned to its elements");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a.width == 0) {  // a(0) 0 = 0 for every activation
+        cudaError_t e = cudaMemset2DAsync(a.h, a.ldh * 2, 0, a.hidden * 2, a.rows, s);
+        if (e == cudaSuccess && a.preact)
+            e = cudaMemset2DAsync(a.preact, a.ldp * 2, 0, a.hidden * 4, a.rows, s);
+        return cuda_rc(e, "clearing h");
+    }
+    const Copies k = copies_of(a, nullptr, 0, true, 0);
+    rc = check_workspace(a.workspace, a.workspace_bytes, k.end, "ffn_gated_workspace");
+    int sms = 0;
+    if (!rc)
+        rc = device_sms(&sms);
+    if (rc)
+        return rc;
+    Product p{};
+    Factor none{};
+    p.epi = kGated;
+    rc = pack(a, k, nullptr, 0, a.workspace, sms, s, &p.x, &p.w, &none);
+    if (rc)
+        return rc;
+    p.x.extent = a.rows;
+    p.w.extent = a.hidden;
+    p.w.mn = !a.w_by_output;
+    p.w_is_weights = true;
+    p.k = a.width;
+    p.segments = p.batch = 1;
+    p.type = p.out_type = a.type;
+    p.activation = a.activation;
+    p.keep = a.preact != nullptr;
+    p.alpha = 1.0f;
+    p.rows = a.rows;
+    p.cols = a.hidden;
+    p.out[0] = a.h;
+    p.ld[0] = a.ldh;
+    p.out[1] = a.preact;
+    p.out[2] = a.preact ? static_cast<uint16_t*>(a.preact) + a.hidden : nullptr;
+    p.ld[1] = p.ld[2] = a.ldp;
+    return launch_product(p, sms, s);
+}
+
+int64_t ffn_gated_backward_workspace(const ffn_gated_args* args, const ffn_gated_grads* grads)
+{
+    set_last_error("");
+    const int rc = check_backward(args, grads);
+    if (rc)
+        return rc;
+    return backward_empty(*args, *grads) ? 0 : backward_copies(*args, *grads).end;
+}
+
+int ffn_gated_backward(const ffn_gated_args* args, const ffn_gated_grads* grads, void* stream)
+{
+    set_last_error("");
+    int rc = check_backward(args, grads);
+    if (rc)
+        return rc;
+    const ffn_gated_args& a = *args;
+    const ffn_gated_grads& g = *grads;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (backward_empty(a, g)) {
+        cudaError_t e = cudaSuccess;
+        if (g.dx && a.rows > 0 && a.width > 0)  // hidden == 0
+            e = cudaMemset2DAsync(g.dx, g.lddx * 2, 0, a.width * 2, a.rows, s);
+        if (e == cudaSuccess && g.dw && !g.accumulate && a.width > 0 && a.hidden > 0) {  // rows == 0
+            const int64_t es = type_bytes(g.dw_type), cols = a.w_by_output ? a.width : 2 * a.hidden;
+            e = cudaMemset2DAsync(g.dw, g.lddw * es, 0, cols * es, a.w_by_output ? 2 * a.hidden : a.width, s);
+        }
+        return cuda_rc(e, "clearing the gradients");
+    }
+    const Copies k = backward_copies(a, g);
+    rc = check_workspace(g.workspace, g.workspace_bytes, k.end, "ffn_gated_backward_workspace");
+    int sms = 0;
+    if (!rc)
+        rc = device_sms(&sms);
+    if (rc)
+        return rc;
+    Factor x{}, w{}, dh{};
+    rc = pack(a, k, a.preact ? nullptr : g.dh, g.lddh, g.workspace, sms, s, &x, &w, &dh);
+    if (rc)
+        return rc;
+    const int64_t ldz = dz_ld(a), half = ldz / 2;
+    uint16_t* dz = static_cast<uint16_t*>(g.workspace);
+    x.extent = a.rows;
+    w.extent = a.hidden;
+    w.mn = !a.w_by_output;
+    Product p{};
+    p.type = p.out_type = a.type;
+    p.activation = a.activation;
+    p.alpha = 1.0f;
+    p.segments = p.batch = 1;
+    if (a.preact) {
+        SlopeArgs sl{};
+        sl.rows = a.rows;
+        sl.hidden = a.hidden;
+        sl.units = half / 8;
+        sl.dh = g.dh;
+        sl.lddh = g.lddh;
+        sl.preact = a.preact;
+        sl.ldp = a.ldp;
+        sl.dz = dz;
+        sl.ldz = ldz;
+        sl.half = half;
+        sl.activation = a.activation;
+        rc = cuda_rc(a.type == GEMM_C_BF16 ? launch_slope<__nv_bfloat16>(sl, s) : launch_slope<__half>(sl, s),
+                     "launching the activation's gradient");
+    } else {
+        p.epi = kGrad;
+        p.x = x;
+        p.w = w;
+        p.k = a.width;
+        p.rows = a.rows;
+        p.cols = a.hidden;
+        p.out[0] = dz;
+        p.out[1] = dz + half;
+        p.ld[0] = p.ld[1] = ldz;
+        p.dh = dh.at[0];
+        p.lddh = dh.ld;
+        p.padded = true;
+        rc = launch_product(p, sms, s);
+        p.padded = false;
+    }
+    p.epi = kStore;
+    if (!rc && g.dx) {
+        // [dg du] x [Wg Wu]^T: two segments of k, each as long as `hidden`.
+        p.x = Factor{{dz, dz + half}, ldz, a.rows, false, {}};
+        p.w = Factor{{w.at[0], w.at[1]}, w.ld, a.width, a.w_by_output != 0, {}};
+        p.k = a.hidden;
+        p.segments = 2;
+        p.rows = a.rows;
+        p.cols = a.width;
+        p.out[0] = g.dx;
+        p.ld[0] = g.lddx;
+        rc = launch_product(p, sms, s);
+        p.segments = 1;
+    }
+    if (!rc && g.dw) {
+        // A product for each half of dw, over the rows of x and of [dg du].
+        const Factor z{{dz, dz + half}, ldz, a.hidden, true, {}}, in{{x.at[0], x.at[0]}, x.ld, a.width, true, {}};
+        const int64_t es = type_bytes(g.dw_type);
+        p.x = a.w_by_output ? z : in;
+        p.w = a.w_by_output ? in : z;
+        p.k = a.rows;
+        p.batch = 2;
+        p.rows = p.x.extent;
+        p.cols = p.w.extent;
+        p.out_type = g.dw_type;
+        p.add = g.accumulate != 0;
+        p.out[0] = g.dw;
+        p.out[1] = static_cast<char*>(g.dw) + (a.w_by_output ? a.hidden * g.lddw : a.hidden) * es;
+        p.ld[0] = p.ld[1] = g.lddw;
+        rc = launch_product(p, sms, s);
+    }
+    return rc;
+}
+
+int mxfp4_gemm(const mxfp4_gemm_args* args, void* stream)
+{
+    set_last_error("");
+    if (!args)
+        return fail_with(GEMM_ERR_ARG, "args is NULL");
+    const mxfp4_gemm_args& a = *args;
+    if (a.rows < 0 || a.cols < 0 || a.width < 0 || a.rows >= kMost || a.cols >= kMost || a.width >= kMost)
+        return fail_with(GEMM_ERR_ARG, "sizes must be in [0, 2^31)");
+    if (!type_ok(a.out_type))
+        return fail_with(GEMM_ERR_ARG, "bad out_type");
+    if (a.activation < FFN_NONE || a.activation > FFN_RELU)
+        return fail_with(GEMM_ERR_ARG, "unknown activation %d", a.activation);
+    if (!a.up_codes && a.activation != FFN_NONE)
+        return fail_with(GEMM_ERR_ARG, "an activation needs up_codes");
+    if (a.rows == 0 || a.cols == 0)
+        return GEMM_OK;
+    const int es = type_bytes(a.out_type);
+    if (!a.out)
+        return fail_with(GEMM_ERR_ARG, "out is NULL");
+    if (a.ldo < a.cols || a.ldo >= kMost)
+        return fail_with(GEMM_ERR_ARG, "row stride of out below the row, or not below 2^31");
+    if (!aligned(a.out, es))
+        return fail_with(GEMM_ERR_ALIGN, "out is not aligned to its elements");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a.width == 0)
+        return cuda_rc(cudaMemset2DAsync(a.out, a.ldo * es, 0, a.cols * es, a.rows, s), "clearing out");
+    if (!a.a_codes || !a.a_scales || !a.b_codes || !a.b_scales || (a.up_codes && !a.up_scales))
+        return fail_with(GEMM_ERR_ARG, "codes or scales are NULL");
+    const int64_t row = ceil_div(a.width, 32) * 16;
+    if (a.lda < row || a.ldb < row || (a.up_codes && a.ldu < row) || a.lda >= kMost || a.ldb >= kMost || a.ldu >= kMost)
+        return fail_with(GEMM_ERR_ARG, "row stride of codes below the row, or not below 2^31");
+    if (!aligned(a.a_codes, 16) || !aligned(a.a_scales, 16) || !aligned(a.b_codes, 16) || !aligned(a.b_scales, 16) ||
+        !aligned(a.up_codes, 16) || !aligned(a.up_scales, 16) || a.lda % 16 || a.ldb % 16 || (a.up_codes && a.ldu % 16))
+        return fail_with(GEMM_ERR_ALIGN, "codes, their rows and scales must start on 16 bytes");
+    int sms = 0;
+    const int rc = device_sms(&sms);
+    if (rc)
+        return rc;
+    Product p{};
+    p.mx = 1;
+    p.epi = a.up_codes ? kGated : kStore;
+    p.x = Factor{{a.a_codes, nullptr}, a.lda, a.rows, false, {a.a_scales, nullptr}};
+    p.w = Factor{{a.b_codes, a.up_codes}, a.ldb, a.cols, false, {a.b_scales, a.up_scales}, a.ldu};
+    p.w_is_weights = true;
+    p.k = a.width;
+    p.segments = p.batch = 1;
+    p.activation = a.activation;
+    p.alpha = a.alpha;
+    p.out_type = a.out_type;
+    p.rows = a.rows;
+    p.cols = a.cols;
+    p.out[0] = a.out;
+    p.ld[0] = a.ldo;
+    return launch_product(p, sms, s);
+}
+
+}  // extern "C"

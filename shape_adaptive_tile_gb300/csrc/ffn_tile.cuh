@@ -1,0 +1,841 @@
+// The tile kernel of the feed-forward operators: tcgen05 products of 16-bit or
+// microscaled 4-bit operands whose epilogue is the activation and the product
+// of two projections, their gradient, or a plain store.
+//
+// Roles as in the GEMM kernel: one warp fills a ring of shared-memory stages by
+// TMA, one thread issues the MMAs, eight warps take the accumulators from
+// tensor memory to the outputs. Two kinds of launch:
+//   - persistent (one CTA or CTA pair an SM or SM pair): tiles in grouped raster
+//     order, two accumulators in turn so that a tile's epilogue runs beside the
+//     next one's products (16-bit operands; the scales of 4-bit ones leave room
+//     for one accumulator of 256 columns);
+//   - split: one tile a cluster, whose CTAs take a share of k each and add their
+//     sums through distributed shared memory in rank order. For problems of few
+//     tiles, and for a few tokens (swap: the weights are the first operand, their
+//     outputs the accumulator's rows, and the tokens its 16 to 64 columns).
+// A gated tile holds the same columns of both projections: as halves of its
+// columns (in a pair, each CTA loads one half), or, swapped, as two accumulators.
+#pragma once
+
+#include <atomic>
+
+#include "ffn_ptx.cuh"
+#include "ffn_tile.h"
+
+namespace sat {
+namespace ffn {
+
+template <bool MX_, int EPI_, int CG_, int BN_, bool P_MN_, bool Q_MN_, bool SWAP_, bool SPLIT_>
+struct TileTraits {
+    static constexpr bool MX = MX_, P_MN = P_MN_, Q_MN = Q_MN_, SWAP = SWAP_, SPLIT = SPLIT_;
+    static constexpr int EPI = EPI_, CG = CG_, BN = BN_;
+    static constexpr bool GATED = EPI != kStore;
+    static constexpr int BK = MX ? 256 : 64;              // k of one stage: rows of 128 bytes
+    static constexpr int NP = SWAP && GATED ? 2 : 1;      // first operands a stage
+    static constexpr int P_BYTES = 128 * 128;
+    static constexpr int BN_CTA = BN / CG;                // second operand's rows this CTA loads
+    static constexpr int Q_BYTES = BN_CTA * 128;
+    static constexpr int QBOX = BN_CTA < 64 ? BN_CTA : 64;  // rows (or columns, MN-major) of one box
+    // Scales of a stage: two words (of four blocks of 32) for each row: 1 KB for 128 rows.
+    static constexpr int NQT = (BN + 127) / 128;          // row tiles of the second operand's scales
+    static constexpr int SF_BYTES = MX ? 1024 * (NP + NQT) : 0;
+    static constexpr int STAGE_BYTES = NP * P_BYTES + Q_BYTES + SF_BYTES;
+    static constexpr int TX_BYTES = STAGE_BYTES;
+    static constexpr int EPI_WARPS = 8;
+    static constexpr int EPI_BYTES = SWAP ? 0 : EPI_WARPS * 4096;
+    static constexpr int BAR_BYTES = 512;
+    // Two CTAs an SM for few tokens (their prologues and ends overlap), else one.
+    static constexpr int BUDGET = (SWAP && BN <= 32 ? 113 : 227) * 1024 - 1024 - EPI_BYTES - BAR_BYTES - (SWAP && BN <= 32 ? 1024 : 0);
+    static constexpr int STAGES = BUDGET / STAGE_BYTES > 8 ? 8 : BUDGET / STAGE_BYTES;
+    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + BAR_BYTES;
+    static constexpr int THREADS = (2 + EPI_WARPS) * 32;
+    static constexpr int ACC_COLS = NP * BN;
+    static constexpr int ACCS = SPLIT || (MX && BN > 128) ? 1 : 2;
+    // Scale columns of a stage: 4 for each of two words of 128 rows.
+    static constexpr int SF_COLS = MX ? 8 * (NP + NQT) : 0;
+    static constexpr int NEED_COLS = ACCS * ACC_COLS + STAGES * SF_COLS;
+    static constexpr int TMEM_COLS = NEED_COLS <= 32 ? 32 : NEED_COLS <= 64 ? 64 : NEED_COLS <= 128 ? 128 : NEED_COLS <= 256 ? 256 : 512;
+    // Columns of one epilogue step, counted in output columns.
+    static constexpr int CHUNK = SWAP ? 16 : 64;
+    static constexpr int OUT_COLS = GATED && !SWAP ? BN / 2 : BN;  // output columns of a tile (swapped: tokens)
+    static constexpr int NCHUNK = OUT_COLS / CHUNK;
+    static constexpr int CHUNK_ACC = GATED ? 2 * CHUNK : CHUNK;    // accumulator columns of a chunk
+    static constexpr int PART_BYTES = CHUNK_ACC * 128 * 4;         // a chunk's partial sums of one CTA
+
+    static_assert(!MX || (!P_MN && !Q_MN), "4-bit operands are K-major");
+    static_assert(!SWAP || (SPLIT && CG == 1 && !Q_MN), "few tokens: split, K-major tokens");
+    static_assert(!SPLIT || CG == 1, "split tiles are 1-SM");
+    static_assert(EPI != kGrad || !SWAP, "no swapped gradient");
+    static_assert(SWAP || OUT_COLS % 64 == 0, "whole 64-column chunks");
+    static_assert(STAGES >= 2 && NEED_COLS <= 512, "ring or tensor memory");
+    static_assert((SWAP && BN <= 32 ? 2 : 1) * (SMEM_BYTES + 1024) <= 228 * 1024, "shared memory of an SM");
+};
+
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+
+// a(g)
+__device__ __forceinline__ float act(float g, int kind)
+{
+    if (kind == 1)
+        return g * sigmoid(g);
+    if (kind == 2)
+        return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
+    if (kind == 3)  // (1 + tanh y) / 2 = 1 / (1 + exp(-2 y))
+        return g * sigmoid(1.5957691216057308f * fmaf(0.044715f * g * g, g, g));
+    if (kind == 4)
+        return g > 0.0f ? g : (g != g ? g : 0.0f);
+    return g;
+}
+
+// a(g) and a'(g)
+__device__ __forceinline__ void act_grad(float g, int kind, float& a, float& d)
+{
+    if (kind == 1) {
+        const float s = sigmoid(g);
+        a = g * s;
+        d = s * fmaf(g, 1.0f - s, 1.0f);
+    } else if (kind == 2) {
+        const float c = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
+        a = g * c;
+        d = fmaf(g * 0.39894228040143268f, __expf(-0.5f * g * g), c);
+    } else if (kind == 3) {
+        const float s = sigmoid(1.5957691216057308f * fmaf(0.044715f * g * g, g, g));
+        a = g * s;
+        d = fmaf(a * (1.0f - s), 1.5957691216057308f * fmaf(0.134145f * g, g, 1.0f), s);
+    } else if (kind == 4) {
+        a = g > 0.0f ? g : (g != g ? g : 0.0f);
+        d = g > 0.0f ? 1.0f : (g != g ? g : 0.0f);
+    } else {
+        a = g;
+        d = 1.0f;
+    }
+}
+
+// Two floats rounded to bf16 (kind 1) or fp16 (kind 2), the first in the lower half.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int kind)
+{
+    uint32_t r;
+    if (kind == 1)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void unpack2(uint32_t v, int kind, float& lo, float& hi)
+{
+    if (kind == 1) {
+        lo = __uint_as_float(v << 16);
+        hi = __uint_as_float(v & 0xFFFF0000u);
+    } else {
+        const __half2 h = *reinterpret_cast<const __half2*>(&v);
+        const float2 f = __half22float2(h);
+        lo = f.x;
+        hi = f.y;
+    }
+}
+
+struct Tile {
+    int tp, tq, z;
+};
+
+// Tile t in groups of `group` tile rows, rows fastest inside a group: CTAs that
+// run together share a few rows of the first operand and a few of the second.
+__device__ __forceinline__ Tile tile_of(int t, const TileArgs& a)
+{
+    Tile w;
+    const int per_z = a.tiles_p * a.tiles_q;
+    w.z = t / per_z;
+    t -= w.z * per_z;
+    const int per = a.group * a.tiles_q;
+    const int g = t / per, r = t - g * per, first = g * a.group;
+    const int gs = min(a.group, a.tiles_p - first);
+    w.tp = first + r % gs;
+    w.tq = r / gs;
+    return w;
+}
+
+template <class T>
+__device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMaps* scales, const TileArgs& args)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* const gbase = smem_raw + (base - raw);
+    const uint32_t sP = base, sQ = sP + T::STAGES * T::NP * T::P_BYTES, sS = sQ + T::STAGES * T::Q_BYTES;
+    const uint32_t epi = base + T::STAGES * T::STAGE_BYTES;
+    const uint32_t bars = epi + T::EPI_BYTES;
+    uint8_t* const gbars = gbase + T::STAGES * T::STAGE_BYTES + T::EPI_BYTES;
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (T::STAGES + s); };
+    auto tfull_bar = [&](int a) { return bars + 8u * (2 * T::STAGES + a); };
+    auto tempty_bar = [&](int a) { return bars + 8u * (2 * T::STAGES + 2 + a); };
+    const uint32_t drain_bar = bars + 8u * (2 * T::STAGES + 4);
+    const uint32_t tmem_ready_bar = bars + 8u * (2 * T::STAGES + 5);
+    auto load_bar = [&](int w) { return bars + 8u * (2 * T::STAGES + 6 + w); };  // kGrad: an epilogue warp's dh
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbars + 8 * (2 * T::STAGES + 14));
+    volatile int* const abort_flag = reinterpret_cast<volatile int*>(gbars + 8 * (2 * T::STAGES + 14) + 4);
+    static_assert(8 * (2 * T::STAGES + 15) <= T::BAR_BYTES, "barrier area");
+
+    const uint32_t rank = T::CG == 2 || T::SPLIT ? cluster_ctarank() : 0u;
+    const bool leader = T::SPLIT || rank == 0;  // of the MMA's CTA pair
+
+    if (warp == 0) {
+        if (lane < T::STAGES) {
+            mbar_init(full_bar(lane), 1);
+            mbar_init(empty_bar(lane), 1);
+        } else if (lane < T::STAGES + 2) {
+            mbar_init(tfull_bar(lane - T::STAGES), 1);
+            mbar_init(tempty_bar(lane - T::STAGES), T::EPI_WARPS * T::CG);
+        } else if (lane == T::STAGES + 2) {
+            mbar_init(drain_bar, 1);
+            mbar_init(tmem_ready_bar, 1);
+            *abort_flag = 0;
+        } else if (lane >= 16 && lane < 24) {
+            mbar_init(load_bar(lane - 16), 1);
+        }
+        fence_mbar_init();
+    }
+    static_assert(T::STAGES + 3 <= 16, "one lane a barrier");
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&maps.p[0]);
+        tma_prefetch_desc(&maps.q[0]);
+    }
+    __syncthreads();
+    if constexpr (T::CG == 2)
+        cluster_sync();
+    uint32_t tmem_base = 0;
+    if (warp >= 1) {
+        if (warp == 1) {
+            tmem_alloc<T::CG>(smem_u32(tmem_slot), T::TMEM_COLS);
+            tmem_relinquish<T::CG>();
+        }
+        tc_fence_before();
+        named_bar_sync(1, (1 + T::EPI_WARPS) * 32);
+        tc_fence_after();
+        tmem_base = *tmem_slot;
+        if (T::CG == 2 && !leader && warp == 1 && lane == 0)
+            mbar_arrive_cluster(map_to_cta(tmem_ready_bar, 0));
+    }
+    const WaitCtl wc{abort_flag, nullptr, args.timeout_ns};
+    constexpr bool kClu = T::CG == 2;
+
+    // Persistent: tiles t0, t0 + step, ... Split: the cluster's one tile, this
+    // CTA's k-blocks [kb0, kb1).
+    const int tiles = args.batch * args.tiles_p * args.tiles_q;
+    const int split = T::SPLIT ? max(1, (args.num_kb + args.kb_per_rank - 1) / args.kb_per_rank) : 1;  // CTAs with a share
+    const int csize = T::SPLIT ? static_cast<int>(gridDim.x) / tiles : 1;
+    const int t0 = T::SPLIT ? static_cast<int>(blockIdx.x) / csize : static_cast<int>(blockIdx.x) / T::CG;
+    const int step = T::SPLIT ? tiles : static_cast<int>(gridDim.x) / T::CG;
+    const int kb0 = T::SPLIT ? min(args.num_kb, static_cast<int>(rank) * args.kb_per_rank) : 0;
+    const int kb1 = T::SPLIT ? min(args.num_kb, kb0 + args.kb_per_rank) : args.num_kb;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            const uint32_t full0 = T::CG == 2 ? map_to_cta(full_bar(0), 0) : full_bar(0);
+            int wave = 0;
+            for (int t = t0; ok && t < tiles; t += step, ++wave) {
+                const Tile w = tile_of(t, args);
+                const int p0 = w.tp * (128 * T::CG) + (T::CG == 2 ? static_cast<int>(rank) * 128 : 0);
+                const int q0 = w.tq * (T::GATED && !T::SWAP ? T::BN / 2 : T::BN);
+                for (int i = 0; i < kb1 - kb0; ++i) {
+                    // Alternate waves run through k in opposite directions: each starts on what the last left in L2.
+                    const int kb = !T::SPLIT && (wave & 1) ? kb1 - 1 - i : kb0 + i;
+                    if (!wait_bar<false>(empty_bar(stage), phase ^ 1u, wc, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = full0 + 8u * stage;
+                    if (T::CG == 1 || leader)
+                        mbar_arrive_expect_tx(full_bar(stage), T::CG * T::TX_BYTES);
+                    auto load = [&](uint32_t dst, const CUtensorMap* m, int x, int y) {
+                        if constexpr (T::CG == 1)
+                            tma_load_2d(dst, m, fb, x, y);
+                        else
+                            tma_load_2d_pair(dst, m, fb, x, y);
+                    };
+                    const int seg = kb >= args.seg_kb ? 1 : 0;
+                    const int zi = seg | w.z;
+                    const int kb_in = kb - seg * args.seg_kb;
+                    const int k0 = kb_in * (T::MX ? 128 : 64);  // 4-bit maps count bytes
+#pragma unroll
+                    for (int n = 0; n < T::NP; ++n) {
+                        const CUtensorMap* m = &maps.p[T::NP == 2 ? n : zi];
+                        const uint32_t dst = sP + (stage * T::NP + n) * T::P_BYTES;
+                        if constexpr (T::P_MN) {
+                            load(dst, m, p0, k0);
+                            load(dst + 8192, m, p0 + 64, k0);
+                        } else {
+                            load(dst, m, k0, p0);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < T::BN_CTA / T::QBOX; ++j) {
+                        // Which part of the tile's columns box j of this CTA is: gated tiles have the gate's columns
+                        // first, then the other's.
+                        const int col = static_cast<int>(rank) * (T::CG == 2 ? T::BN_CTA : 0) + j * T::QBOX;
+                        const int half = T::GATED && !T::SWAP && col >= T::BN / 2 ? 1 : 0;
+                        const CUtensorMap* m = &maps.q[T::GATED ? half : zi];
+                        const int q = q0 + col - half * (T::BN / 2);
+                        const uint32_t dst = sQ + stage * T::Q_BYTES + j * (T::QBOX * 128);
+                        if constexpr (T::Q_MN)
+                            load(dst, m, q, k0);
+                        else
+                            load(dst, m, k0, q);
+                    }
+                    if constexpr (T::MX) {
+                        const uint32_t dst = sS + stage * T::SF_BYTES;
+#pragma unroll
+                        for (int n = 0; n < T::NP; ++n)
+                            load(dst + n * 1024, &scales->p[n], 0, (p0 >> 7) * args.sf_rows_p + kb * 2);
+#pragma unroll
+                        for (int j = 0; j < T::NQT; ++j) {
+                            const int half = T::GATED && !T::SWAP && j * 128 >= T::BN / 2 ? 1 : 0;
+                            const int q = q0 + j * 128 - half * (T::BN / 2);
+                            load(dst + (T::NP + j) * 1024, &scales->q[T::GATED ? half : 0], 0,
+                                 (q >> 7) * args.sf_rows_q + kb * 2);
+                        }
+                    }
+                    if (++stage == T::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (ok) {  // until every stage filled above has been read
+                for (int i = 0; i < T::STAGES; ++i) {
+                    if (!wait_bar<false>(empty_bar(stage), phase ^ 1u, wc, 0))
+                        break;
+                    if (++stage == T::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ----------------------------------------------------------------- MMA
+        if (leader && lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            bool ok = true, issued = false;
+            if constexpr (T::CG == 2)
+                ok = wait_bar<true>(tmem_ready_bar, 0, wc, 0);
+            int wave = 0;
+            for (int t = t0; ok && t < tiles; t += step, ++wave) {
+                if (kb1 <= kb0)
+                    break;
+                if (!wait_bar<kClu>(tempty_bar(acc), acc_phase ^ 1u, wc, 0)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem_base + static_cast<uint32_t>(acc * T::ACC_COLS);
+                for (int i = 0; i < kb1 - kb0; ++i) {
+                    const int kb = !T::SPLIT && (wave & 1) ? kb1 - 1 - i : kb0 + i;
+                    if (!wait_bar<false>(full_bar(stage), phase, wc, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t b0 = sQ + stage * T::Q_BYTES;
+                    const uint32_t sf0 = tmem_base + T::ACCS * T::ACC_COLS + stage * T::SF_COLS;
+                    if constexpr (T::MX) {
+                        // The stage's scales to columns of their own: two words of each 128 rows of the first operand(s),
+                        // then for each word all row tiles of the second.
+                        const uint32_t src = sS + stage * T::SF_BYTES;
+#pragma unroll
+                        for (int wd = 0; wd < 2; ++wd) {
+#pragma unroll
+                            for (int n = 0; n < T::NP; ++n)
+                                tmem_cp_scales<T::CG>(sf0 + n * 8 + wd * 4, src + n * 1024 + wd * 512);
+#pragma unroll
+                            for (int j = 0; j < T::NQT; ++j)
+                                tmem_cp_scales<T::CG>(sf0 + T::NP * 8 + wd * 4 * T::NQT + j * 4,
+                                                      src + (T::NP + j) * 1024 + wd * 512);
+                        }
+                    }
+                    const int steps = T::MX && kb == args.num_kb - 1 ? args.tail_steps : 4;
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        if (T::MX && ks >= steps)
+                            break;
+                        const uint64_t bd = T::Q_MN ? sdesc(b0 + ks * 2048, 8192, 1024, kLayoutSW128)
+                                                    : sdesc(b0 + ks * 32, 16, 1024, kLayoutSW128);
+                        const uint32_t go = (i != 0 || ks != 0) ? 1u : 0u;
+#pragma unroll
+                        for (int n = 0; n < T::NP; ++n) {
+                            const uint32_t a0 = sP + (stage * T::NP + n) * T::P_BYTES;
+                            const uint64_t ad = T::P_MN ? sdesc(a0 + ks * 2048, 8192, 1024, kLayoutSW128)
+                                                        : sdesc(a0 + ks * 32, 16, 1024, kLayoutSW128);
+                            if constexpr (T::MX)
+                                mma_mxf4<T::CG>(d + n * T::BN, ad, bd, args.idesc | ((ks & 1) ? kScaleIdUpper : 0u),
+                                                sf0 + n * 8 + (ks >> 1) * 4,
+                                                sf0 + T::NP * 8 + (ks >> 1) * 4 * T::NQT, go);
+                            else
+                                mma_ss<T::CG, false>(d + n * T::BN, ad, bd, args.idesc, go);
+                        }
+                    }
+                    issued = true;
+                    if constexpr (T::CG == 1)
+                        mma_commit(empty_bar(stage));
+                    else
+                        mma_commit_pair(empty_bar(stage), 0x3);
+                    if (++stage == T::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok)
+                    break;
+                if constexpr (T::CG == 1)
+                    mma_commit(tfull_bar(acc));
+                else
+                    mma_commit_pair(tfull_bar(acc), 0x3);
+                if (++acc == T::ACCS) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            }
+            if (!ok && issued) {
+                // Let issued MMAs finish before tensor memory is freed.
+                if constexpr (T::CG == 1)
+                    mma_commit(drain_bar);
+                else
+                    mma_commit_pair(drain_bar, 0x1);
+                const uint64_t began = globaltimer_ns();
+                while (!mbar_try_wait<kClu>(drain_bar, 0) && globaltimer_ns() - began <= args.timeout_ns) {
+                }
+            }
+        }
+    }
+
+    // -------------------------------------------------------------- epilogue
+    const int ew = warp - 2, sub = warp & 3, half = ew >> 2;
+    bool ok = true;  // false: a wait gave up, and what is written from then on is NaN
+    uint32_t acc_cols = 0;  // this tile's accumulator, at this warp's lanes
+    // GC accumulator columns from `col` on, of row sub * 32 + lane; in a split tile with the other CTAs' sums added,
+    // in rank order after this CTA's own. part: their place in the partial sums (in groups of GC columns).
+    auto add_parts = [&](uint32_t* r, int n4, int chunk, int colgroup, int groups) {
+        if constexpr (T::SPLIT) {
+            const int per = (T::NCHUNK + split - 1) / split;  // chunks a CTA may own
+            for (int s = 0; s < split - 1; ++s) {
+                const uint32_t src = base + static_cast<uint32_t>((s * per + chunk / split) * T::PART_BYTES) +
+                                     static_cast<uint32_t>(colgroup * (T::PART_BYTES / groups) + (sub * 32 + lane) * 16);
+#pragma unroll
+                for (int q = 0; q < n4; ++q) {
+                    float a, b, c, d;
+                    ld_shared_v4(src + q * 2048, a, b, c, d);
+                    r[4 * q] = __float_as_uint(__uint_as_float(r[4 * q]) + a);
+                    r[4 * q + 1] = __float_as_uint(__uint_as_float(r[4 * q + 1]) + b);
+                    r[4 * q + 2] = __float_as_uint(__uint_as_float(r[4 * q + 2]) + c);
+                    r[4 * q + 3] = __float_as_uint(__uint_as_float(r[4 * q + 3]) + d);
+                }
+            }
+        }
+    };
+    auto own = [&](int chunk) { return !T::SPLIT || chunk % split == static_cast<int>(rank); };
+
+    if constexpr (T::SPLIT) {
+        // All CTAs' products are done (their rings are free), then every CTA sends the chunks that others own to these.
+        if (warp >= 2) {
+            if (kb1 > kb0)
+                ok = wait_bar<false>(tfull_bar(0), 0, wc, 0);
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            tc_fence_after();
+            acc_cols = tmem_base + (static_cast<uint32_t>(sub * 32) << 16);
+        }
+        if (csize > 1) {
+            __syncthreads();
+            cluster_sync();
+            if (warp >= 2 && kb1 > kb0) {
+                const int per = (T::NCHUNK + split - 1) / split;
+                for (int c = half; c < T::NCHUNK; c += 2) {
+                    if (own(c))
+                        continue;
+                    const int to = c % split;
+                    const int slot = static_cast<int>(rank) < to ? static_cast<int>(rank) : static_cast<int>(rank) - 1;
+                    const uint32_t dst0 = map_to_cta(base, static_cast<uint32_t>(to)) +
+                                          static_cast<uint32_t>((slot * per + c / split) * T::PART_BYTES) +
+                                          static_cast<uint32_t>((sub * 32 + lane) * 16);
+                    constexpr int GC = T::SWAP ? 16 : 32, GROUPS = T::CHUNK_ACC / GC;
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g) {
+                        // Gated chunks: the gate's columns, then the other's.
+                        const int col = T::GATED ? (g < GROUPS / 2 ? c * T::CHUNK + g * GC
+                                                                   : (T::SWAP ? T::BN : T::BN / 2) + c * T::CHUNK +
+                                                                         (g - GROUPS / 2) * GC)
+                                                 : c * T::CHUNK + g * GC;
+                        uint32_t r[GC];
+                        if constexpr (GC == 16)
+                            tmem_ld_32x32b_x16(acc_cols + col, r);
+                        else
+                            tmem_ld_32x32b_x32(acc_cols + col, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int q = 0; q < GC / 4; ++q)
+                            st_cluster_v4(dst0 + g * (T::PART_BYTES / GROUPS) + q * 2048, ok ? r[4 * q] : 0x7FFFFFFFu,
+                                          ok ? r[4 * q + 1] : 0x7FFFFFFFu, ok ? r[4 * q + 2] : 0x7FFFFFFFu,
+                                          ok ? r[4 * q + 3] : 0x7FFFFFFFu);
+                    }
+                }
+            }
+            __syncthreads();
+            cluster_sync();
+        }
+    }
+
+    if (warp >= 2) {
+        const uint32_t sb = epi + ew * 4096;
+        const uint32_t tempty0 = T::CG == 2 ? map_to_cta(tempty_bar(0), 0) : tempty_bar(0);
+        int acc = 0;
+        uint32_t acc_phase = 0, load_phase = 0;
+        const int kind = args.out_kind, activation = args.activation;
+        const float alpha = args.alpha;
+        const bool any = args.num_kb > 0;
+
+        // Hands the staged 32 rows x 128 bytes (in the stores' swizzle) to out[i]: rows row0 .., columns col0 ...
+        auto put = [&](int i, int row0, int col0) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            // (A box that reaches past the last column overwrites the rest of that 16-byte piece with zeros.)
+            if (((args.tma_out >> i) & 1) && (col0 + (kind == 0 ? 32 : 64) <= args.cols || ((args.tma_edge >> i) & 1))) {
+                if (lane == 0 && row0 < args.rows && col0 < args.cols) {
+                    if (T::EPI == kStore && args.add)
+                        tma_add_2d(&maps.o[i], sb, col0, row0);
+                    else
+                        tma_store_2d(&maps.o[i], sb, col0, row0);
+                    bulk_commit();
+                }
+                return;
+            }
+            // Rows that bulk stores cannot address: element by element, a row at a time.
+            const int rows = min(32, args.rows - row0);
+            if (kind == 0) {
+                float* o = static_cast<float*>(args.out[i]) + static_cast<long long>(row0) * args.ld[i] + col0 + lane;
+                if (col0 + lane < args.cols)
+                    for (int r = 0; r < rows; ++r, o += args.ld[i]) {
+                        const float v = __uint_as_float(
+                            ld_shared_u32(sb + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2))));
+                        *o = T::EPI == kStore && args.add ? *o + v : v;
+                    }
+            } else {
+                uint16_t* o = static_cast<uint16_t*>(args.out[i]) + static_cast<long long>(row0) * args.ld[i] + col0 + 2 * lane;
+                const int left = args.cols - col0 - 2 * lane;
+                for (int r = 0; r < rows; ++r, o += args.ld[i]) {
+                    const uint32_t v = ld_shared_u32(sb + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2)));
+                    if (left > 0)
+                        o[0] = static_cast<uint16_t>(v);
+                    if (left > 1)
+                        o[1] = static_cast<uint16_t>(v >> 16);
+                }
+            }
+            __syncwarp();
+        };
+        // The staging buffer is free: the last store has read it.
+        auto take = [&] {
+            if (lane == 0)
+                bulk_wait_read<0>();
+            __syncwarp();
+        };
+        const uint32_t my_row = sb + static_cast<uint32_t>(lane * 128);
+        auto piece = [&](int q) { return my_row + static_cast<uint32_t>((q ^ (lane & 7)) << 4); };
+
+        for (int t = t0; t < tiles; t += step) {
+            const Tile w = tile_of(t, args);
+            const int row0 = w.tp * (128 * T::CG) + (T::CG == 2 ? static_cast<int>(rank) * 128 : 0) + sub * 32;
+            const int col0 = w.tq * T::OUT_COLS;
+            if constexpr (!T::SPLIT) {
+                if constexpr (T::EPI == kGrad) {
+                    // dh comes into the staging buffer while the products run.
+                    take();
+                    if (lane == 0 && half < T::NCHUNK && row0 < args.rows && col0 + half * 64 < args.cols) {
+                        mbar_arrive_expect_tx(load_bar(ew), 4096);
+                        tma_load_2d(sb, &maps.o[2], load_bar(ew), col0 + half * 64, row0);
+                    }
+                }
+                if (any && ok)
+                    ok = wait_bar<false>(tfull_bar(acc), acc_phase, wc, 0);
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                tc_fence_after();
+                acc_cols = tmem_base + (static_cast<uint32_t>(sub * 32) << 16) + static_cast<uint32_t>(acc * T::ACC_COLS);
+            }
+            // One group of accumulator columns, scaled; NaN where a wait gave up, 0 where there is nothing to add up.
+            auto fetch32 = [&](float (&v)[32], int col, int chunk, int group) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(acc_cols + col, r);
+                tmem_wait_ld();
+                add_parts(r, 8, chunk, group, T::CHUNK_ACC / 32);
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    v[j] = !ok ? __uint_as_float(0x7FFFFFFFu) : any ? alpha * __uint_as_float(r[j]) : 0.0f;
+            };
+            auto release = [&] {
+                if constexpr (!T::SPLIT) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (T::CG == 1)
+                            mbar_arrive(tempty0 + 8u * acc);
+                        else
+                            mbar_arrive_cluster(tempty0 + 8u * acc);
+                    }
+                }
+            };
+
+            if constexpr (T::SWAP) {
+                // This lane's accumulator row is output column f, its columns are tokens.
+                const int f = row0 + lane;
+                for (int c = half; c < T::NCHUNK; c += 2) {
+                    if (!own(c))
+                        continue;
+                    const int tok0 = col0 + c * 16;
+                    uint32_t g[16], u[16];
+                    tmem_ld_32x32b_x16(acc_cols + c * 16, g);
+                    if constexpr (T::GATED)
+                        tmem_ld_32x32b_x16(acc_cols + T::BN + c * 16, u);
+                    tmem_wait_ld();
+                    add_parts(g, 4, c, 0, T::CHUNK_ACC / 16);
+                    if constexpr (T::GATED)
+                        add_parts(u, 4, c, 1, T::CHUNK_ACC / 16);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        if (f >= args.cols || tok0 + j >= args.rows)
+                            continue;
+                        float gv = !ok ? __uint_as_float(0x7FFFFFFFu) : any ? alpha * __uint_as_float(g[j]) : 0.0f;
+                        const long long row = tok0 + j;
+                        if constexpr (T::GATED) {
+                            const float uv = !ok ? gv : any ? alpha * __uint_as_float(u[j]) : 0.0f;
+                            if (args.keep) {
+                                c_store(static_cast<float*>(args.out[1]), kind, row * args.ld[1] + f, gv);
+                                c_store(static_cast<float*>(args.out[2]), kind, row * args.ld[2] + f, uv);
+                            }
+                            gv = act(gv, activation) * uv;
+                        }
+                        c_store(static_cast<float*>(args.out[0]), kind, row * args.ld[0] + f, gv);
+                    }
+                }
+            } else if constexpr (T::EPI == kStore) {
+#pragma unroll 1
+                for (int c = half; c < T::NCHUNK; c += 2) {
+                    if (!own(c))
+                        continue;
+                    if (kind == 0) {
+#pragma unroll 1
+                        for (int g = 0; g < 2; ++g) {
+                            float v[32];
+                            fetch32(v, c * 64 + g * 32, c, g);
+                            if (c + 2 >= T::NCHUNK && g == 1)
+                                release();
+                            take();
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                st_shared_v4(piece(q), v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                            put(w.z, row0, col0 + c * 64 + g * 32);
+                        }
+                    } else {
+                        take();
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            float v[32];
+                            fetch32(v, c * 64 + g * 32, c, g);
+                            if (c + 2 >= T::NCHUNK && g == 1)
+                                release();
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                st_shared_v4u(piece(g * 4 + q), pack2(v[8 * q], v[8 * q + 1], kind),
+                                              pack2(v[8 * q + 2], v[8 * q + 3], kind), pack2(v[8 * q + 4], v[8 * q + 5], kind),
+                                              pack2(v[8 * q + 6], v[8 * q + 7], kind));
+                        }
+                        put(w.z, row0, col0 + c * 64);
+                    }
+                }
+                if constexpr (T::NCHUNK < 2) {
+                    if (half >= T::NCHUNK)
+                        release();
+                }
+            } else {
+                // Gated tiles: 64 output columns a warp (128-column tiles) or, of 64-column tiles, the first four warps.
+                static_assert(T::NCHUNK <= 2, "a chunk a warp");
+                if (half >= T::NCHUNK || !own(half)) {
+                    release();
+                } else {
+                    const int c = half, cc = col0 + c * 64;
+                    uint32_t hw[32];  // kGrad: this row's 64 values of dh
+                    if constexpr (T::EPI == kGrad) {
+                        if (T::SPLIT) {
+                            take();
+                            if (lane == 0 && row0 < args.rows && cc < args.cols) {
+                                mbar_arrive_expect_tx(load_bar(ew), 4096);
+                                tma_load_2d(sb, &maps.o[2], load_bar(ew), cc, row0);
+                            }
+                        }
+                        if (row0 < args.rows && cc < args.cols) {
+                            if (!wait_bar<false>(load_bar(ew), load_phase, wc, 0))
+                                ok = false;
+                            load_phase ^= 1u;
+                        }
+                        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            ld_shared_v4u(piece(q), hw[4 * q], hw[4 * q + 1], hw[4 * q + 2], hw[4 * q + 3]);
+                        __syncwarp();
+                    }
+                    // kGated: first (and, with the pre-activations wanted, second) h, then gate and up; kGrad: dg in the
+                    // buffer, du kept in hw until dg has been read.
+                    const int outs = T::EPI == kGated && args.keep ? 3 : 1;
+#pragma unroll 1
+                    for (int o = 0; o < outs; ++o) {
+                        if (!(T::EPI == kGrad))
+                            take();
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            float gv[32], uv[32];
+                            if (T::EPI == kGrad || o != 2)
+                                fetch32(gv, c * 64 + g * 32, c, g);
+                            if (T::EPI == kGrad || o != 1)
+                                fetch32(uv, T::BN / 2 + c * 64 + g * 32, c, 2 + g);
+                            if (g == 1 && o == outs - 1)
+                                release();
+                            if constexpr (T::EPI == kGrad) {
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) {
+                                    float d0, d1, a0, a1, s0, s1;
+                                    unpack2(hw[g * 16 + j], kind, d0, d1);
+                                    act_grad(gv[2 * j], activation, a0, s0);
+                                    act_grad(gv[2 * j + 1], activation, a1, s1);
+                                    hw[g * 16 + j] = pack2(d0 * a0, d1 * a1, kind);
+                                    gv[2 * j] = d0 * uv[2 * j] * s0;
+                                    gv[2 * j + 1] = d1 * uv[2 * j + 1] * s1;
+                                }
+                            } else if (o == 0) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    gv[j] = act(gv[j], activation) * uv[j];
+                            } else if (o == 2) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    gv[j] = uv[j];
+                            }
+                            if constexpr (T::MX) {
+                                if (kind == 0) {  // (fp32 outputs: of products of 4-bit operands only)
+                                    if (g == 1)
+                                        take();
+#pragma unroll
+                                    for (int q = 0; q < 8; ++q)
+                                        st_shared_v4(piece(q), gv[4 * q], gv[4 * q + 1], gv[4 * q + 2], gv[4 * q + 3]);
+                                    put(0, row0, cc + g * 32);
+                                    continue;
+                                }
+                            }
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                st_shared_v4u(piece(g * 4 + q), pack2(gv[8 * q], gv[8 * q + 1], kind),
+                                              pack2(gv[8 * q + 2], gv[8 * q + 3], kind), pack2(gv[8 * q + 4], gv[8 * q + 5], kind),
+                                              pack2(gv[8 * q + 6], gv[8 * q + 7], kind));
+                        }
+                        if (!T::MX || kind != 0)
+                            put(o, row0, cc);
+                    }
+                    if constexpr (T::EPI == kGrad) {
+                        take();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            st_shared_v4u(piece(q), hw[4 * q], hw[4 * q + 1], hw[4 * q + 2], hw[4 * q + 3]);
+                        put(1, row0, cc);
+                    }
+                }
+            }
+            if (++acc == T::ACCS) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+        if (!T::SWAP && lane == 0) {
+            bulk_wait<0>();
+            fence_proxy_async_global();
+        }
+        __syncwarp();
+    }
+
+    // ------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (T::CG == 2)
+        cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc<T::CG>(tmem_base, T::TMEM_COLS);
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(T::THREADS, T::SWAP && T::BN <= 32 ? 2 : 1)
+    sat_ffn_tile_kernel(const __grid_constant__ TileMaps maps, const TileArgs args)
+{
+    tile_kernel<T>(maps, nullptr, args);
+}
+
+template <class T>
+__global__ void __launch_bounds__(T::THREADS, T::SWAP && T::BN <= 32 ? 2 : 1)
+    sat_ffn_scaled_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ ScaleMaps scales, const TileArgs args)
+{
+    tile_kernel<T>(maps, &scales, args);
+}
+
+template <class T>
+cudaError_t launch_tiles(const TileMaps& maps, const ScaleMaps* scales, const TileArgs& args, int grid, int cluster,
+                         cudaStream_t stream)
+{
+    const void* fn;
+    if constexpr (T::MX)
+        fn = reinterpret_cast<const void*>(sat_ffn_scaled_tile_kernel<T>);
+    else
+        fn = reinterpret_cast<const void*>(sat_ffn_tile_kernel<T>);
+    // Once for each device.
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(T::THREADS);
+    cfg.dynamicSmemBytes = T::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    if constexpr (T::MX)
+        return cudaLaunchKernelEx(&cfg, sat_ffn_scaled_tile_kernel<T>, maps, *scales, args);
+    else
+        return cudaLaunchKernelEx(&cfg, sat_ffn_tile_kernel<T>, maps, args);
+}
+
+template <class T>
+constexpr Variant variant()
+{
+    return Variant{T::MX, T::EPI, T::CG, T::BN, T::P_MN, T::Q_MN, T::SWAP, !T::SPLIT,
+                   T::STAGES * T::STAGE_BYTES, T::NCHUNK, T::PART_BYTES, &launch_tiles<T>};
+}
+
+}  // namespace ffn
+}  // namespace sat
