@@ -48,13 +48,12 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64
                      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
 }
 
-// 32 rows of 16 bytes, consecutive in shared memory (512 bytes), to 4 columns
-// of lanes 0-31, repeated in the lanes of all four warps (of both CTAs of a
-// pair, each from its own shared memory at that address).
+// 32 rows of 16 bytes, consecutive in shared memory (512 bytes; d describes
+// them), to 4 columns of lanes 0-31, repeated in the lanes of all four warps (of
+// both CTAs of a pair, each from its own shared memory at that address).
 template <int CG>
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t saddr)
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t d)
 {
-    const uint64_t d = sdesc(saddr, 16, 128, 0);  // unswizzled, 8-row groups 128 bytes apart
     if constexpr (CG == 1)
         asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d));
     else
@@ -68,6 +67,19 @@ __device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, uint32_t src,
                      reinterpret_cast<uint64_t>(map)),
                  "r"(src), "r"(x), "r"(y)
                  : "memory");
+}
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // 16 bytes to a shared::cluster address (this CTA's or a peer's).

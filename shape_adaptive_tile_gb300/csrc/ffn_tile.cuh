@@ -51,6 +51,7 @@ struct TileTraits {
     static constexpr int THREADS = (2 + EPI_WARPS) * 32;
     static constexpr int ACC_COLS = NP * BN;
     static constexpr int ACCS = SPLIT || (MX && BN > 128) ? 1 : 2;
+    static constexpr bool DRAIN = MX && !SPLIT;  // one accumulator, taken to registers at once
     // Scale columns of a stage: 4 for each of two words of 128 rows.
     static constexpr int SF_COLS = MX ? 8 * (NP + NQT) : 0;
     static constexpr int NEED_COLS = ACCS * ACC_COLS + STAGES * SF_COLS;
@@ -65,6 +66,7 @@ struct TileTraits {
     static_assert(!MX || (!P_MN && !Q_MN), "4-bit operands are K-major");
     static_assert(!SWAP || (SPLIT && CG == 1 && !Q_MN), "few tokens: split, K-major tokens");
     static_assert(!SPLIT || CG == 1, "split tiles are 1-SM");
+    static_assert(!DRAIN || BN == 256, "half the tile's columns a warp");
     static_assert(EPI != kGrad || !SWAP, "no swapped gradient");
     static_assert(SWAP || OUT_COLS % 64 == 0, "whole 64-column chunks");
     static_assert(STAGES >= 2 && NEED_COLS <= 512, "ring or tensor memory");
@@ -135,6 +137,48 @@ __device__ __forceinline__ void unpack2(uint32_t v, int kind, float& lo, float& 
     }
 }
 
+// A bounded wait of a whole warp (or of the threads that call it). After two
+// seconds the CTA's abort flag is raised (a pair's other CTA's too): all waits
+// then end at once, the loops run to their ends on whatever is there, and the
+// epilogue writes NaN. The clock is read only after a few tries: a ring whose
+// stages are used up as fast as they come waits at every one of them.
+struct Waiter {
+    uint32_t abort;       // shared address of the flag
+    uint32_t peer_abort;  // the same of the pair's other CTA, or of this one
+    unsigned long long timeout_ns;
+
+    __device__ __forceinline__ bool aborted() const { return ld_shared_u32(abort) != 0; }
+};
+
+template <bool kCluster>
+static __device__ __noinline__ void wait_long(uint32_t bar, uint32_t parity, const Waiter w)
+{
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait<kCluster>(bar, parity))
+                return;
+        if (w.aborted())
+            return;
+        if (globaltimer_ns() - t0 > w.timeout_ns) {
+            st_shared_u32(w.abort, 1u);
+            if (w.peer_abort != w.abort)
+                st_cluster_u32(w.peer_abort, 1u);
+            return;
+        }
+    }
+}
+
+template <bool kCluster>
+__device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, const Waiter& w)
+{
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait<kCluster>(bar, parity))
+            return;
+    wait_long<kCluster>(bar, parity, w);
+}
+
 struct Tile {
     int tp, tq, z;
 };
@@ -159,7 +203,10 @@ template <class T>
 __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMaps* scales, const TileArgs& args)
 {
     extern __shared__ uint8_t smem_raw[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (From one lane: the compiler then knows it to be the same in all, and keeps what the producer and the MMA warp
+    // compute in uniform registers, as their instructions want it. With a lane's own values a stage cost that warp some
+    // 1000 cycles, twice what the products of a 4-bit stage take.)
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* const gbase = smem_raw + (base - raw);
@@ -171,12 +218,11 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
     auto empty_bar = [&](int s) { return bars + 8u * (T::STAGES + s); };
     auto tfull_bar = [&](int a) { return bars + 8u * (2 * T::STAGES + a); };
     auto tempty_bar = [&](int a) { return bars + 8u * (2 * T::STAGES + 2 + a); };
-    const uint32_t drain_bar = bars + 8u * (2 * T::STAGES + 4);
-    const uint32_t tmem_ready_bar = bars + 8u * (2 * T::STAGES + 5);
-    auto load_bar = [&](int w) { return bars + 8u * (2 * T::STAGES + 6 + w); };  // kGrad: an epilogue warp's dh
-    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbars + 8 * (2 * T::STAGES + 14));
-    volatile int* const abort_flag = reinterpret_cast<volatile int*>(gbars + 8 * (2 * T::STAGES + 14) + 4);
-    static_assert(8 * (2 * T::STAGES + 15) <= T::BAR_BYTES, "barrier area");
+    const uint32_t tmem_ready_bar = bars + 8u * (2 * T::STAGES + 4);
+    auto load_bar = [&](int w) { return bars + 8u * (2 * T::STAGES + 5 + w); };  // kGrad: an epilogue warp's dh
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbars + 8 * (2 * T::STAGES + 13));
+    const uint32_t abort_at = bars + 8u * (2 * T::STAGES + 13) + 4;
+    static_assert(8 * (2 * T::STAGES + 14) <= T::BAR_BYTES, "barrier area");
 
     const uint32_t rank = T::CG == 2 || T::SPLIT ? cluster_ctarank() : 0u;
     const bool leader = T::SPLIT || rank == 0;  // of the MMA's CTA pair
@@ -189,9 +235,8 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
             mbar_init(tfull_bar(lane - T::STAGES), 1);
             mbar_init(tempty_bar(lane - T::STAGES), T::EPI_WARPS * T::CG);
         } else if (lane == T::STAGES + 2) {
-            mbar_init(drain_bar, 1);
             mbar_init(tmem_ready_bar, 1);
-            *abort_flag = 0;
+            st_shared_u32(abort_at, 0u);
         } else if (lane >= 16 && lane < 24) {
             mbar_init(load_bar(lane - 16), 1);
         }
@@ -214,11 +259,11 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
         tc_fence_before();
         named_bar_sync(1, (1 + T::EPI_WARPS) * 32);
         tc_fence_after();
-        tmem_base = *tmem_slot;
+        tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
         if (T::CG == 2 && !leader && warp == 1 && lane == 0)
             mbar_arrive_cluster(map_to_cta(tmem_ready_bar, 0));
     }
-    const WaitCtl wc{abort_flag, nullptr, args.timeout_ns};
+    const Waiter wc{abort_at, T::CG == 2 ? map_to_cta(abort_at, rank ^ 1u) : abort_at, args.timeout_ns};
     constexpr bool kClu = T::CG == 2;
 
     // Persistent: tiles t0, t0 + step, ... Split: the cluster's one tile, this
@@ -233,24 +278,24 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            const uint32_t full0 = T::CG == 2 ? map_to_cta(full_bar(0), 0) : full_bar(0);
-            int wave = 0;
-            for (int t = t0; ok && t < tiles; t += step, ++wave) {
-                const Tile w = tile_of(t, args);
-                const int p0 = w.tp * (128 * T::CG) + (T::CG == 2 ? static_cast<int>(rank) * 128 : 0);
-                const int q0 = w.tq * (T::GATED && !T::SWAP ? T::BN / 2 : T::BN);
-                for (int i = 0; i < kb1 - kb0; ++i) {
-                    // Alternate waves run through k in opposite directions: each starts on what the last left in L2.
-                    const int kb = !T::SPLIT && (wave & 1) ? kb1 - 1 - i : kb0 + i;
-                    if (!wait_bar<false>(empty_bar(stage), phase ^ 1u, wc, 0)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t fb = full0 + 8u * stage;
+        const bool one = elect_one();
+        int stage = 0, wave = 0;
+        uint32_t phase = 0;
+        const uint32_t full0 = T::CG == 2 ? map_to_cta(full_bar(0), 0) : full_bar(0);
+        for (int t = t0; t < tiles; t += step, ++wave) {
+            const Tile w = tile_of(t, args);
+            const int p0 = w.tp * (128 * T::CG) + (T::CG == 2 ? static_cast<int>(rank) * 128 : 0);
+            const int q0 = w.tq * (T::GATED && !T::SWAP ? T::BN / 2 : T::BN);
+            for (int i = 0; i < kb1 - kb0; ++i) {
+                // Alternate waves run through k in opposite directions: each starts on what the last left in L2.
+                const int kb = !T::SPLIT && (wave & 1) ? kb1 - 1 - i : kb0 + i;
+                wait_for<false>(empty_bar(stage), phase ^ 1u, wc);
+                __syncwarp();
+                const int seg = kb >= args.seg_kb ? 1 : 0;
+                const int zi = seg | w.z;
+                const int k0 = (kb - seg * args.seg_kb) * (T::MX ? 128 : 64);  // 4-bit maps count bytes
+                const uint32_t fb = full0 + 8u * stage;
+                if (one) {
                     if (T::CG == 1 || leader)
                         mbar_arrive_expect_tx(full_bar(stage), T::CG * T::TX_BYTES);
                     auto load = [&](uint32_t dst, const CUtensorMap* m, int x, int y) {
@@ -259,10 +304,6 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                         else
                             tma_load_2d_pair(dst, m, fb, x, y);
                     };
-                    const int seg = kb >= args.seg_kb ? 1 : 0;
-                    const int zi = seg | w.z;
-                    const int kb_in = kb - seg * args.seg_kb;
-                    const int k0 = kb_in * (T::MX ? 128 : 64);  // 4-bit maps count bytes
 #pragma unroll
                     for (int n = 0; n < T::NP; ++n) {
                         const CUtensorMap* m = &maps.p[T::NP == 2 ? n : zi];
@@ -279,9 +320,9 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                         // Which part of the tile's columns box j of this CTA is: gated tiles have the gate's columns
                         // first, then the other's.
                         const int col = static_cast<int>(rank) * (T::CG == 2 ? T::BN_CTA : 0) + j * T::QBOX;
-                        const int half = T::GATED && !T::SWAP && col >= T::BN / 2 ? 1 : 0;
-                        const CUtensorMap* m = &maps.q[T::GATED ? half : zi];
-                        const int q = q0 + col - half * (T::BN / 2);
+                        const int second = T::GATED && !T::SWAP && col >= T::BN / 2 ? 1 : 0;
+                        const CUtensorMap* m = &maps.q[T::GATED ? second : zi];
+                        const int q = q0 + col - second * (T::BN / 2);
                         const uint32_t dst = sQ + stage * T::Q_BYTES + j * (T::QBOX * 128);
                         if constexpr (T::Q_MN)
                             load(dst, m, q, k0);
@@ -295,131 +336,134 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                             load(dst + n * 1024, &scales->p[n], 0, (p0 >> 7) * args.sf_rows_p + kb * 2);
 #pragma unroll
                         for (int j = 0; j < T::NQT; ++j) {
-                            const int half = T::GATED && !T::SWAP && j * 128 >= T::BN / 2 ? 1 : 0;
-                            const int q = q0 + j * 128 - half * (T::BN / 2);
-                            load(dst + (T::NP + j) * 1024, &scales->q[T::GATED ? half : 0], 0,
+                            const int second = T::GATED && !T::SWAP && j * 128 >= T::BN / 2 ? 1 : 0;
+                            const int q = q0 + j * 128 - second * (T::BN / 2);
+                            load(dst + (T::NP + j) * 1024, &scales->q[T::GATED ? second : 0], 0,
                                  (q >> 7) * args.sf_rows_q + kb * 2);
                         }
                     }
-                    if (++stage == T::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
                 }
-            }
-            if (ok) {  // until every stage filled above has been read
-                for (int i = 0; i < T::STAGES; ++i) {
-                    if (!wait_bar<false>(empty_bar(stage), phase ^ 1u, wc, 0))
-                        break;
-                    if (++stage == T::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                __syncwarp();
+                if (++stage == T::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
         }
+        // Until every stage filled above has been read.
+        for (int i = 0; i < T::STAGES; ++i) {
+            wait_for<false>(empty_bar(stage), phase ^ 1u, wc);
+            if (++stage == T::STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        __syncwarp();
     } else if (warp == 1) {
         // ----------------------------------------------------------------- MMA
-        if (leader && lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            int acc = 0;
+        if (leader) {
+            const bool one = elect_one();
+            int stage = 0, acc = 0;
             uint32_t acc_phase = 0;
-            bool ok = true, issued = false;
             if constexpr (T::CG == 2)
-                ok = wait_bar<true>(tmem_ready_bar, 0, wc, 0);
-            int wave = 0;
-            for (int t = t0; ok && t < tiles; t += step, ++wave) {
-                if (kb1 <= kb0)
-                    break;
-                if (!wait_bar<kClu>(tempty_bar(acc), acc_phase ^ 1u, wc, 0)) {
-                    ok = false;
-                    break;
-                }
+                wait_for<true>(tmem_ready_bar, 0, wc);
+            // The scales of a stage go to tensor memory (to columns of that stage's own) before the products of the stage
+            // before it, so that no product waits for them: two words of each 128 rows of the first operand(s), then for
+            // each word all row tiles of the second.
+            const int per_tile = kb1 - kb0;
+            const int mine = per_tile > 0 && t0 < tiles ? ((tiles - t0 + step - 1) / step) * per_tile : 0;
+            int next = 0, next_stage = 0;  // the first block whose data has not been waited for, and its stage
+            uint32_t next_phase = 0;
+            auto arrive = [&] {
+                wait_for<false>(full_bar(next_stage), next_phase, wc);
+                __syncwarp();
                 tc_fence_after();
-                const uint32_t d = tmem_base + static_cast<uint32_t>(acc * T::ACC_COLS);
-                for (int i = 0; i < kb1 - kb0; ++i) {
-                    const int kb = !T::SPLIT && (wave & 1) ? kb1 - 1 - i : kb0 + i;
-                    if (!wait_bar<false>(full_bar(stage), phase, wc, 0)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t b0 = sQ + stage * T::Q_BYTES;
-                    const uint32_t sf0 = tmem_base + T::ACCS * T::ACC_COLS + stage * T::SF_COLS;
-                    if constexpr (T::MX) {
-                        // The stage's scales to columns of their own: two words of each 128 rows of the first operand(s),
-                        // then for each word all row tiles of the second.
-                        const uint32_t src = sS + stage * T::SF_BYTES;
+                if constexpr (T::MX) {
+                    const uint32_t src = sS + next_stage * T::SF_BYTES;
+                    const uint64_t sd = sdesc(src, 16, 128, 0);  // unswizzled, 8-row groups 128 bytes apart
+                    const uint32_t sf0 = tmem_base + T::ACCS * T::ACC_COLS + next_stage * T::SF_COLS;
+                    if (one) {
 #pragma unroll
                         for (int wd = 0; wd < 2; ++wd) {
 #pragma unroll
                             for (int n = 0; n < T::NP; ++n)
-                                tmem_cp_scales<T::CG>(sf0 + n * 8 + wd * 4, src + n * 1024 + wd * 512);
+                                tmem_cp_scales<T::CG>(sf0 + n * 8 + wd * 4, sd + n * 64 + wd * 32);
 #pragma unroll
                             for (int j = 0; j < T::NQT; ++j)
                                 tmem_cp_scales<T::CG>(sf0 + T::NP * 8 + wd * 4 * T::NQT + j * 4,
-                                                      src + (T::NP + j) * 1024 + wd * 512);
+                                                      sd + (T::NP + j) * 64 + wd * 32);
                         }
                     }
-                    const int steps = T::MX && kb == args.num_kb - 1 ? args.tail_steps : 4;
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) {
-                        if (T::MX && ks >= steps)
-                            break;
-                        const uint64_t bd = T::Q_MN ? sdesc(b0 + ks * 2048, 8192, 1024, kLayoutSW128)
-                                                    : sdesc(b0 + ks * 32, 16, 1024, kLayoutSW128);
-                        const uint32_t go = (i != 0 || ks != 0) ? 1u : 0u;
-#pragma unroll
-                        for (int n = 0; n < T::NP; ++n) {
-                            const uint32_t a0 = sP + (stage * T::NP + n) * T::P_BYTES;
-                            const uint64_t ad = T::P_MN ? sdesc(a0 + ks * 2048, 8192, 1024, kLayoutSW128)
-                                                        : sdesc(a0 + ks * 32, 16, 1024, kLayoutSW128);
-                            if constexpr (T::MX)
-                                mma_mxf4<T::CG>(d + n * T::BN, ad, bd, args.idesc | ((ks & 1) ? kScaleIdUpper : 0u),
-                                                sf0 + n * 8 + (ks >> 1) * 4,
-                                                sf0 + T::NP * 8 + (ks >> 1) * 4 * T::NQT, go);
-                            else
-                                mma_ss<T::CG, false>(d + n * T::BN, ad, bd, args.idesc, go);
-                        }
-                    }
-                    issued = true;
-                    if constexpr (T::CG == 1)
-                        mma_commit(empty_bar(stage));
-                    else
-                        mma_commit_pair(empty_bar(stage), 0x3);
-                    if (++stage == T::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    __syncwarp();
                 }
-                if (!ok)
-                    break;
-                if constexpr (T::CG == 1)
-                    mma_commit(tfull_bar(acc));
-                else
-                    mma_commit_pair(tfull_bar(acc), 0x3);
+                ++next;
+                if (++next_stage == T::STAGES) {
+                    next_stage = 0;
+                    next_phase ^= 1u;
+                }
+            };
+            const uint64_t adesc = T::P_MN ? sdesc(sP, 8192, 1024, kLayoutSW128) : sdesc(sP, 16, 1024, kLayoutSW128);
+            const uint64_t bdesc = T::Q_MN ? sdesc(sQ, 8192, 1024, kLayoutSW128) : sdesc(sQ, 16, 1024, kLayoutSW128);
+            int wave = 0, done = 0;
+            for (int t = t0; done < mine; t += step, ++wave) {
+                wait_for<kClu>(tempty_bar(acc), acc_phase ^ 1u, wc);
+                __syncwarp();
+                tc_fence_after();
+                const uint32_t d = tmem_base + static_cast<uint32_t>(acc * T::ACC_COLS);
+                for (int i = 0; i < per_tile; ++i, ++done) {
+                    const int kb = !T::SPLIT && (wave & 1) ? kb1 - 1 - i : kb0 + i;
+                    while (next < mine && next <= done + (T::MX ? 1 : 0))
+                        arrive();
+                    // (Start addresses are the descriptors' low bits, in units of 16 bytes.)
+                    const uint64_t bd0 = bdesc + static_cast<uint32_t>(stage * (T::Q_BYTES / 16));
+                    const uint64_t ad0 = adesc + static_cast<uint32_t>(stage * (T::NP * T::P_BYTES / 16));
+                    const uint32_t sf0 = tmem_base + T::ACCS * T::ACC_COLS + stage * T::SF_COLS;
+                    const int steps = T::MX && kb == args.num_kb - 1 ? args.tail_steps : 4;
+                    if (one) {
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) {
+                            if (T::MX && ks >= steps)
+                                break;
+                            const uint64_t bd = bd0 + ks * (T::Q_MN ? 128 : 2);
+                            const uint32_t go = (i != 0 || ks != 0) ? 1u : 0u;
+#pragma unroll
+                            for (int n = 0; n < T::NP; ++n) {
+                                const uint64_t ad = ad0 + n * (T::P_BYTES / 16) + ks * (T::P_MN ? 128 : 2);
+                                if constexpr (T::MX)
+                                    mma_mxf4<T::CG>(d + n * T::BN, ad, bd, args.idesc | ((ks & 1) ? kScaleIdUpper : 0u),
+                                                    sf0 + n * 8 + (ks >> 1) * 4,
+                                                    sf0 + T::NP * 8 + (ks >> 1) * 4 * T::NQT, go);
+                                else
+                                    mma_ss<T::CG, false>(d + n * T::BN, ad, bd, args.idesc, go);
+                            }
+                        }
+                        if constexpr (T::CG == 1)
+                            mma_commit(empty_bar(stage));
+                        else
+                            mma_commit_pair(empty_bar(stage), 0x3);
+                        if (i == per_tile - 1) {
+                            if constexpr (T::CG == 1)
+                                mma_commit(tfull_bar(acc));
+                            else
+                                mma_commit_pair(tfull_bar(acc), 0x3);
+                        }
+                    }
+                    __syncwarp();
+                    if (++stage == T::STAGES)
+                        stage = 0;
+                }
                 if (++acc == T::ACCS) {
                     acc = 0;
                     acc_phase ^= 1u;
                 }
             }
-            if (!ok && issued) {
-                // Let issued MMAs finish before tensor memory is freed.
-                if constexpr (T::CG == 1)
-                    mma_commit(drain_bar);
-                else
-                    mma_commit_pair(drain_bar, 0x1);
-                const uint64_t began = globaltimer_ns();
-                while (!mbar_try_wait<kClu>(drain_bar, 0) && globaltimer_ns() - began <= args.timeout_ns) {
-                }
-            }
         }
+        __syncwarp();
     }
 
     // -------------------------------------------------------------- epilogue
     const int ew = warp - 2, sub = warp & 3, half = ew >> 2;
-    bool ok = true;  // false: a wait gave up, and what is written from then on is NaN
+    bool ok = true;  // false: a wait gave up, and what is written is NaN
     uint32_t acc_cols = 0;  // this tile's accumulator, at this warp's lanes
     // GC accumulator columns from `col` on, of row sub * 32 + lane; in a split tile with the other CTAs' sums added,
     // in rank order after this CTA's own. part: their place in the partial sums (in groups of GC columns).
@@ -447,8 +491,8 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
         // All CTAs' products are done (their rings are free), then every CTA sends the chunks that others own to these.
         if (warp >= 2) {
             if (kb1 > kb0)
-                ok = wait_bar<false>(tfull_bar(0), 0, wc, 0);
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                wait_for<false>(tfull_bar(0), 0, wc);
+            ok = __all_sync(0xffffffffu, !wc.aborted());
             tc_fence_after();
             acc_cols = tmem_base + (static_cast<uint32_t>(sub * 32) << 16);
         }
@@ -561,9 +605,9 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                         tma_load_2d(sb, &maps.o[2], load_bar(ew), col0 + half * 64, row0);
                     }
                 }
-                if (any && ok)
-                    ok = wait_bar<false>(tfull_bar(acc), acc_phase, wc, 0);
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (any)
+                    wait_for<false>(tfull_bar(acc), acc_phase, wc);
+                ok = __all_sync(0xffffffffu, !wc.aborted());
                 tc_fence_after();
                 acc_cols = tmem_base + (static_cast<uint32_t>(sub * 32) << 16) + static_cast<uint32_t>(acc * T::ACC_COLS);
             }
@@ -590,7 +634,57 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                 }
             };
 
-            if constexpr (T::SWAP) {
+            if constexpr (T::DRAIN) {
+                // One accumulator: this warp's columns go to registers at once, and the next tile's products begin while
+                // these are worked on. Half the tile's columns a warp: 64 of each factor of a gated tile, else two
+                // chunks of 64.
+                float v[4][32];
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    tmem_ld_32x32b_x32(acc_cols + (T::GATED ? (g >> 1) * (T::BN / 2) + half * 64 + (g & 1) * 32
+                                                            : half * 128 + g * 32),
+                                       reinterpret_cast<uint32_t(&)[32]>(v[g]));
+                tmem_wait_ld();
+                release();
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[g][j] = ok ? alpha * v[g][j] : __uint_as_float(0x7FFFFFFFu);
+                if constexpr (T::GATED) {
+#pragma unroll
+                    for (int g = 0; g < 2; ++g)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[g][j] = act(v[g][j], activation) * v[g + 2][j];
+                }
+                constexpr int GROUPS = T::GATED ? 2 : 4;
+                const int first = col0 + half * GROUPS * 32;
+                if (kind == 0) {
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g) {
+                        take();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            st_shared_v4(piece(q), v[g][4 * q], v[g][4 * q + 1], v[g][4 * q + 2], v[g][4 * q + 3]);
+                        put(0, row0, first + g * 32);
+                    }
+                } else {
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g) {
+                        if (g % 2 == 0)
+                            take();
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            st_shared_v4u(piece((g & 1) * 4 + q), pack2(v[g][8 * q], v[g][8 * q + 1], kind),
+                                          pack2(v[g][8 * q + 2], v[g][8 * q + 3], kind),
+                                          pack2(v[g][8 * q + 4], v[g][8 * q + 5], kind),
+                                          pack2(v[g][8 * q + 6], v[g][8 * q + 7], kind));
+                        if (g % 2 == 1)
+                            put(0, row0, first + (g - 1) * 32);
+                    }
+                }
+            } else if constexpr (T::SWAP) {
                 // This lane's accumulator row is output column f, its columns are tokens.
                 const int f = row0 + lane;
                 for (int c = half; c < T::NCHUNK; c += 2) {
@@ -678,11 +772,10 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                             }
                         }
                         if (row0 < args.rows && cc < args.cols) {
-                            if (!wait_bar<false>(load_bar(ew), load_phase, wc, 0))
-                                ok = false;
+                            wait_for<false>(load_bar(ew), load_phase, wc);
                             load_phase ^= 1u;
                         }
-                        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                        ok = __all_sync(0xffffffffu, !wc.aborted());
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
                             ld_shared_v4u(piece(q), hw[4 * q], hw[4 * q + 1], hw[4 * q + 2], hw[4 * q + 3]);
