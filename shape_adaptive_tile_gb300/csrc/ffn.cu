@@ -399,14 +399,16 @@ __global__ void __launch_bounds__(256) sat_ffn_slope_kernel(const SlopeArgs a, c
     const Pack<T> d = load_at(static_cast<const T*>(a.dh) + r * a.lddh + j, left, dh_vec);
     const Pack<T> g = load_at(pre, left, p_vec), u = load_at(pre + a.hidden, left, p_vec);
     Pack<T> dg, du;
+    with_act(a.activation, [&](auto k) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float dv = to_f32(reinterpret_cast<const T*>(d.w)[i]);
-        float v, slope;
-        act_grad(to_f32(reinterpret_cast<const T*>(g.w)[i]), a.activation, v, slope);
-        reinterpret_cast<T*>(dg.w)[i] = from_f32<T>(dv * to_f32(reinterpret_cast<const T*>(u.w)[i]) * slope);
-        reinterpret_cast<T*>(du.w)[i] = from_f32<T>(dv * v);
-    }
+        for (int i = 0; i < 8; ++i) {
+            const float dv = to_f32(reinterpret_cast<const T*>(d.w)[i]);
+            float v, slope;
+            act_grad<decltype(k)::value>(to_f32(reinterpret_cast<const T*>(g.w)[i]), v, slope);
+            reinterpret_cast<T*>(dg.w)[i] = from_f32<T>(dv * to_f32(reinterpret_cast<const T*>(u.w)[i]) * slope);
+            reinterpret_cast<T*>(du.w)[i] = from_f32<T>(dv * v);
+        }
+    });
     // Rows of dz are whole eights of columns: what lies past `hidden` is never read.
     T* z = static_cast<T*>(a.dz) + r * a.ldz + j;
     store_pack(z, dg);

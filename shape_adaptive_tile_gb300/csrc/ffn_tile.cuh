@@ -18,6 +18,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "ffn_ptx.cuh"
 #include "ffn_tile.h"
@@ -75,41 +76,85 @@ struct TileTraits {
 
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
-// a(g)
-__device__ __forceinline__ float act(float g, int kind)
-{
-    if (kind == 1)
-        return g * sigmoid(g);
-    if (kind == 2)
-        return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
-    if (kind == 3)  // (1 + tanh y) / 2 = 1 / (1 + exp(-2 y))
-        return g * sigmoid(1.5957691216057308f * fmaf(0.044715f * g * g, g, g));
-    if (kind == 4)
-        return g > 0.0f ? g : (g != g ? g : 0.0f);
-    return g;
-}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int kind);
 
-// a(g) and a'(g)
-__device__ __forceinline__ void act_grad(float g, int kind, float& a, float& d)
+// a(g) and a'(g) of the activation KIND (ffn_activation_t).
+template <int KIND>
+__device__ __forceinline__ void act_grad(float g, float& a, float& d)
 {
-    if (kind == 1) {
+    if constexpr (KIND == 1) {
         const float s = sigmoid(g);
         a = g * s;
         d = s * fmaf(g, 1.0f - s, 1.0f);
-    } else if (kind == 2) {
+    } else if constexpr (KIND == 2) {
         const float c = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
         a = g * c;
         d = fmaf(g * 0.39894228040143268f, __expf(-0.5f * g * g), c);
-    } else if (kind == 3) {
+    } else if constexpr (KIND == 3) {  // (1 + tanh y) / 2 = 1 / (1 + exp(-2 y))
         const float s = sigmoid(1.5957691216057308f * fmaf(0.044715f * g * g, g, g));
         a = g * s;
         d = fmaf(a * (1.0f - s), 1.5957691216057308f * fmaf(0.134145f * g, g, 1.0f), s);
-    } else if (kind == 4) {
+    } else if constexpr (KIND == 4) {
         a = g > 0.0f ? g : (g != g ? g : 0.0f);
         d = g > 0.0f ? 1.0f : (g != g ? g : 0.0f);
     } else {
         a = g;
         d = 1.0f;
+    }
+}
+
+// f(std::integral_constant<int, kind>): the choice is made once for a whole
+// loop over values. Made for each of 64 unrolled values instead, the code ran
+// to tens of kilobytes, whose fetching took a single tile's epilogue 9 us.
+template <class F>
+__device__ __forceinline__ void with_act(int kind, F f)
+{
+    if (kind == 1)
+        f(std::integral_constant<int, 1>{});
+    else if (kind == 2)
+        f(std::integral_constant<int, 2>{});
+    else if (kind == 3)
+        f(std::integral_constant<int, 3>{});
+    else if (kind == 4)
+        f(std::integral_constant<int, 4>{});
+    else
+        f(std::integral_constant<int, 0>{});
+}
+
+// g = a(g) u
+template <int N>
+__device__ __forceinline__ void gate(float (&g)[N], const float (&u)[N], int kind)
+{
+    with_act(kind, [&](auto k) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            float a, d;
+            act_grad<decltype(k)::value>(g[j], a, d);
+            g[j] = a * u[j];
+        }
+    });
+}
+
+// N elements of one kind, `step` apart (16-bit kinds rounded to nearest even), for those of index below n.
+template <int N>
+__device__ __forceinline__ void store_column(void* at, int kind, long long first, long long step, int n, const float (&v)[N])
+{
+    if (kind == 0) {
+        float* o = static_cast<float*>(at) + first;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j < n)
+                o[j * step] = v[j];
+    } else {
+        uint16_t* o = static_cast<uint16_t*>(at) + first;
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+            const uint32_t w = pack2(v[j], v[j + 1], kind);
+            if (j < n)
+                o[j * step] = static_cast<uint16_t>(w);
+            if (j + 1 < n)
+                o[(j + 1) * step] = static_cast<uint16_t>(w >> 16);
+        }
     }
 }
 
@@ -177,6 +222,84 @@ __device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, const Wa
         if (mbar_try_wait<kCluster>(bar, parity))
             return;
     wait_long<kCluster>(bar, parity, w);
+}
+
+// 16-bit rows start, start + STEP, ... of a staged chunk, all of which start on
+// a word (ODD false) or all between two words (ODD): then a lane's second
+// element and the next lane's first make a word, and the row's first element and
+// its last go by themselves.
+template <bool ODD, int STEP>
+__device__ __forceinline__ void store_words(uint32_t sb, uint16_t* out, long long ld, int start, int rows, int n)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t at[8 / STEP], next[8 / STEP];
+#pragma unroll
+    for (int i = 0; i < 8 / STEP; ++i) {
+        const int r = (start + i * STEP) & 7;
+        at[i] = sb + r * 128 + ((((lane >> 2) ^ r) << 4) | ((lane & 3) << 2));
+        const int l1 = min(lane + 1, 31);
+        next[i] = sb + r * 128 + ((((l1 >> 2) ^ r) << 4) | ((l1 & 3) << 2));
+    }
+    const int e = 2 * lane + (ODD ? 1 : 0);  // first element of this lane's word
+    const bool word = e + 1 < n, tail = e == n - 1, head = ODD && lane == 0 && n > 0;
+    const long long step = static_cast<long long>(STEP) * ld;
+    uint16_t* o = out + start * ld;
+#pragma unroll 1
+    for (int r0 = start; r0 < rows; r0 += 8) {
+#pragma unroll
+        for (int i = 0; i < 8 / STEP; ++i) {
+            const uint32_t v = ld_shared_u32(at[i]);
+            const uint32_t w = ODD ? __funnelshift_r(v, ld_shared_u32(next[i]), 16) : v;
+            at[i] += 1024;
+            next[i] += 1024;
+            if (r0 + i * STEP < rows) {
+                if (word)
+                    *reinterpret_cast<uint32_t*>(o + e) = w;
+                if (tail)
+                    o[e] = static_cast<uint16_t>(w);
+                if (head)
+                    o[0] = static_cast<uint16_t>(v);
+            }
+            o += step;
+        }
+    }
+}
+
+// Staged rows (32 of 128 bytes, in the stores' swizzle) that bulk stores cannot
+// address, to `at` + first + r ld: `rows` rows of `left` elements or fewer. A
+// function of its own: its code stays out of the way of the others'.
+static __device__ __noinline__ void store_rows(uint32_t sb, void* at, long long first, long long ld, int kind, int rows,
+                                               int left, bool add)
+{
+    const int lane = threadIdx.x & 31;
+    if (kind == 0) {
+        float* o = static_cast<float*>(at) + first + lane;
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += 8, o += 8 * ld) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = __uint_as_float(ld_shared_u32(sb + (r0 + i) * 128 + ((((lane >> 2) ^ i) << 4) | ((lane & 3) << 2))));
+                if (add && r0 + i < rows && lane < left)
+                    v[i] += o[i * ld];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (r0 + i < rows && lane < left)
+                    o[i * ld] = v[i];
+        }
+        return;
+    }
+    uint16_t* o = static_cast<uint16_t*>(at) + first;
+    const int n = min(64, left), odd = static_cast<int>(reinterpret_cast<uintptr_t>(o) >> 1 & 1);
+    if (ld & 1) {
+        store_words<false, 2>(sb, o, ld, odd, rows, n);
+        store_words<true, 2>(sb, o, ld, 1 - odd, rows, n);
+    } else if (odd) {
+        store_words<true, 1>(sb, o, ld, 0, rows, n);
+    } else {
+        store_words<false, 1>(sb, o, ld, 0, rows, n);
+    }
 }
 
 struct Tile {
@@ -560,27 +683,8 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                 }
                 return;
             }
-            // Rows that bulk stores cannot address: element by element, a row at a time.
-            const int rows = min(32, args.rows - row0);
-            if (kind == 0) {
-                float* o = static_cast<float*>(args.out[i]) + static_cast<long long>(row0) * args.ld[i] + col0 + lane;
-                if (col0 + lane < args.cols)
-                    for (int r = 0; r < rows; ++r, o += args.ld[i]) {
-                        const float v = __uint_as_float(
-                            ld_shared_u32(sb + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2))));
-                        *o = T::EPI == kStore && args.add ? *o + v : v;
-                    }
-            } else {
-                uint16_t* o = static_cast<uint16_t*>(args.out[i]) + static_cast<long long>(row0) * args.ld[i] + col0 + 2 * lane;
-                const int left = args.cols - col0 - 2 * lane;
-                for (int r = 0; r < rows; ++r, o += args.ld[i]) {
-                    const uint32_t v = ld_shared_u32(sb + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2)));
-                    if (left > 0)
-                        o[0] = static_cast<uint16_t>(v);
-                    if (left > 1)
-                        o[1] = static_cast<uint16_t>(v >> 16);
-                }
-            }
+            store_rows(sb, args.out[i], static_cast<long long>(row0) * args.ld[i] + col0, args.ld[i], kind,
+                       min(32, args.rows - row0), args.cols - col0, T::EPI == kStore && args.add);
             __syncwarp();
         };
         // The staging buffer is free: the last store has read it.
@@ -652,11 +756,8 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                     for (int j = 0; j < 32; ++j)
                         v[g][j] = ok ? alpha * v[g][j] : __uint_as_float(0x7FFFFFFFu);
                 if constexpr (T::GATED) {
-#pragma unroll
-                    for (int g = 0; g < 2; ++g)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[g][j] = act(v[g][j], activation) * v[g + 2][j];
+                    gate(v[0], v[2], activation);
+                    gate(v[1], v[3], activation);
                 }
                 constexpr int GROUPS = T::GATED ? 2 : 4;
                 const int first = col0 + half * GROUPS * 32;
@@ -691,30 +792,28 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                     if (!own(c))
                         continue;
                     const int tok0 = col0 + c * 16;
-                    uint32_t g[16], u[16];
-                    tmem_ld_32x32b_x16(acc_cols + c * 16, g);
-                    if constexpr (T::GATED)
-                        tmem_ld_32x32b_x16(acc_cols + T::BN + c * 16, u);
-                    tmem_wait_ld();
-                    add_parts(g, 4, c, 0, T::CHUNK_ACC / 16);
-                    if constexpr (T::GATED)
-                        add_parts(u, 4, c, 1, T::CHUNK_ACC / 16);
+                    uint32_t r[16];
+                    float g[16], u[16];
+                    auto take16 = [&](float (&v)[16], int col, int group) {
+                        tmem_ld_32x32b_x16(acc_cols + col, r);
+                        tmem_wait_ld();
+                        add_parts(r, 4, c, group, T::CHUNK_ACC / 16);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if (f >= args.cols || tok0 + j >= args.rows)
-                            continue;
-                        float gv = !ok ? __uint_as_float(0x7FFFFFFFu) : any ? alpha * __uint_as_float(g[j]) : 0.0f;
-                        const long long row = tok0 + j;
-                        if constexpr (T::GATED) {
-                            const float uv = !ok ? gv : any ? alpha * __uint_as_float(u[j]) : 0.0f;
-                            if (args.keep) {
-                                c_store(static_cast<float*>(args.out[1]), kind, row * args.ld[1] + f, gv);
-                                c_store(static_cast<float*>(args.out[2]), kind, row * args.ld[2] + f, uv);
-                            }
-                            gv = act(gv, activation) * uv;
+                        for (int j = 0; j < 16; ++j)
+                            v[j] = !ok ? __uint_as_float(0x7FFFFFFFu) : any ? alpha * __uint_as_float(r[j]) : 0.0f;
+                    };
+                    take16(g, c * 16, 0);
+                    if constexpr (T::GATED)
+                        take16(u, T::BN + c * 16, 1);
+                    const int n = f < args.cols ? args.rows - tok0 : 0;
+                    if constexpr (T::GATED) {
+                        if (args.keep) {
+                            store_column(args.out[1], kind, tok0 * args.ld[1] + f, args.ld[1], n, g);
+                            store_column(args.out[2], kind, tok0 * args.ld[2] + f, args.ld[2], n, u);
                         }
-                        c_store(static_cast<float*>(args.out[0]), kind, row * args.ld[0] + f, gv);
+                        gate(g, u, activation);
                     }
+                    store_column(args.out[0], kind, tok0 * args.ld[0] + f, args.ld[0], n, g);
                 }
             } else if constexpr (T::EPI == kStore) {
 #pragma unroll 1
@@ -798,20 +897,20 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                             if (g == 1 && o == outs - 1)
                                 release();
                             if constexpr (T::EPI == kGrad) {
+                                with_act(activation, [&](auto k) {
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) {
-                                    float d0, d1, a0, a1, s0, s1;
-                                    unpack2(hw[g * 16 + j], kind, d0, d1);
-                                    act_grad(gv[2 * j], activation, a0, s0);
-                                    act_grad(gv[2 * j + 1], activation, a1, s1);
-                                    hw[g * 16 + j] = pack2(d0 * a0, d1 * a1, kind);
-                                    gv[2 * j] = d0 * uv[2 * j] * s0;
-                                    gv[2 * j + 1] = d1 * uv[2 * j + 1] * s1;
-                                }
+                                    for (int j = 0; j < 16; ++j) {
+                                        float d0, d1, a0, a1, s0, s1;
+                                        unpack2(hw[g * 16 + j], kind, d0, d1);
+                                        act_grad<decltype(k)::value>(gv[2 * j], a0, s0);
+                                        act_grad<decltype(k)::value>(gv[2 * j + 1], a1, s1);
+                                        hw[g * 16 + j] = pack2(d0 * a0, d1 * a1, kind);
+                                        gv[2 * j] = d0 * uv[2 * j] * s0;
+                                        gv[2 * j + 1] = d1 * uv[2 * j + 1] * s1;
+                                    }
+                                });
                             } else if (o == 0) {
-#pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    gv[j] = act(gv[j], activation) * uv[j];
+                                gate(gv, uv, activation);
                             } else if (o == 2) {
 #pragma unroll
                                 for (int j = 0; j < 32; ++j)
