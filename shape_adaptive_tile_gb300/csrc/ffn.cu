@@ -329,41 +329,98 @@ int cuda_rc(cudaError_t e, const char* what)
     return e == cudaSuccess ? GEMM_OK : fail_with(GEMM_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// Up to four matrices copied into rows that start on 16 bytes: 16 bytes a
+// thread, from the words that hold them. Columns past a row's end are 0.
+struct Copy {
+    const uint8_t* from;
+    uint8_t* to;
+    long long ld, ld_to, bytes;  // of rows: bytes apart, in them
+    long long pieces, end;       // 16-byte pieces of a row, and of this matrix and those before it
+};
+struct CopyArgs {
+    Copy m[4];
+    int n;
+};
+
+__global__ void __launch_bounds__(256) sat_ffn_copy_kernel(const __grid_constant__ CopyArgs a)
+{
+    launch_dependents();
+    wait_for_earlier();
+    long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    int k = 0;
+    while (k < a.n && i >= a.m[k].end)
+        ++k;
+    if (k == a.n)
+        return;
+    const Copy& m = a.m[k];
+    if (k > 0)
+        i -= a.m[k - 1].end;
+    const long long r = i / m.pieces, at = (i - r * m.pieces) * 16;
+    const uint8_t* from = m.from + r * m.ld + at;
+    const long long left = m.bytes - at;  // > 0
+    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 2);
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(from - odd);
+    uint32_t w[5];
+#pragma unroll
+    for (int j = 0; j < 5; ++j)  // (a word that holds a byte of the row is read whole)
+        w[j] = 4 * j - odd < left && (j < 4 || odd) ? words[j] : 0u;
+    uint32_t out[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        out[j] = odd ? __funnelshift_r(w[j], w[j + 1], 16) : w[j];
+        if (left < 4 * j + 4)
+            out[j] = left > 4 * j ? out[j] & 0xFFFFu : 0u;
+    }
+    *reinterpret_cast<uint4*>(m.to + r * m.ld_to + at) = make_uint4(out[0], out[1], out[2], out[3]);
+}
+
 // Copies what needs it, and gives x, the weights and dh as they are read.
-int pack(const ffn_gated_args& a, const Copies& k, const void* dh, int64_t lddh, void* workspace, int sms, cudaStream_t s,
-         Factor* x, Factor* w, Factor* d)
+int pack(const ffn_gated_args& a, const Copies& k, const void* dh, int64_t lddh, void* workspace, cudaStream_t s, Factor* x,
+         Factor* w, Factor* d)
 {
     char* ws = static_cast<char*>(workspace);
-    const char *wp = static_cast<const char*>(a.w);
-    cudaError_t e = cudaSuccess;
+    CopyArgs c{};
+    auto add = [&](const void* from, int64_t ld, int64_t to, int64_t ld_to, int64_t rows, int64_t width) {
+        Copy& m = c.m[c.n];
+        m.from = static_cast<const uint8_t*>(from);
+        m.to = reinterpret_cast<uint8_t*>(ws + to);
+        m.ld = ld * 2;
+        m.ld_to = ld_to * 2;
+        m.bytes = width * 2;
+        m.pieces = ceil_div(m.bytes, 16);
+        m.end = (c.n ? c.m[c.n - 1].end : 0) + rows * m.pieces;
+        ++c.n;
+        return static_cast<const void*>(m.to);
+    };
     x->at[0] = a.x;
     x->ld = a.ldx;
     if (k.x) {
-        e = launch_pack_rows(a.x, a.ldx * 2, ws + k.at_x, k.ldx * 2, a.rows, a.width * 2, sms, s);
-        x->at[0] = ws + k.at_x;
+        x->at[0] = add(a.x, a.ldx, k.at_x, k.ldx, a.rows, a.width);
         x->ld = k.ldx;
     }
     const int64_t half = a.w_by_output ? a.hidden * a.ldw * 2 : a.hidden * 2;  // bytes from the gate's weights to the others
-    w->at[0] = wp;
-    w->at[1] = wp + half;
+    w->at[0] = a.w;
+    w->at[1] = static_cast<const char*>(a.w) + half;
     w->ld = a.ldw;
     if (k.w) {
-        const int64_t rows = a.w_by_output ? a.hidden : a.width, bytes = (a.w_by_output ? a.width : a.hidden) * 2;
-        for (int i = 0; i < 2 && e == cudaSuccess; ++i)
-            e = launch_pack_rows(w->at[i], a.ldw * 2, ws + (i ? k.at_w2 : k.at_w), k.ldw * 2, rows, bytes, sms, s);
-        w->at[0] = ws + k.at_w;
-        w->at[1] = ws + k.at_w2;
+        for (int i = 0; i < 2; ++i)
+            w->at[i] = add(w->at[i], a.ldw, i ? k.at_w2 : k.at_w, k.ldw, a.w_by_output ? a.hidden : a.width,
+                           a.w_by_output ? a.width : a.hidden);
         w->ld = k.ldw;
     }
     d->at[0] = dh;
     d->ld = lddh;
     if (k.dh) {
-        if (e == cudaSuccess)
-            e = launch_pack_rows(dh, lddh * 2, ws + k.at_dh, k.lddh * 2, a.rows, a.hidden * 2, sms, s);
-        d->at[0] = ws + k.at_dh;
+        d->at[0] = add(dh, lddh, k.at_dh, k.lddh, a.rows, a.hidden);
         d->ld = k.lddh;
     }
-    return cuda_rc(e, "launching a copy into aligned rows");
+    if (c.n == 0)
+        return GEMM_OK;
+    const int64_t grid = ceil_div(c.m[c.n - 1].end, 256);
+    if (grid >= kMost)
+        return fail_with(GEMM_ERR_ARG, "too much to copy into aligned rows");
+    return cuda_rc(launch_early(sat_ffn_copy_kernel, static_cast<unsigned>(grid), 256, 0, 1, s, c),
+                   "launching a copy into aligned rows");
 }
 
 // dg and du of eight columns a thread, from the pre-activations.
@@ -376,20 +433,30 @@ struct SlopeArgs {
     int activation;
 };
 
+// Eight elements, or the `left` that there are; off 16 bytes from the words that hold them.
 template <typename T>
 __device__ __forceinline__ Pack<T> load_at(const T* p, long long left, bool vec)
 {
     if (vec && left >= 8)
         return load_pack(p);
-    Pack<T> v{};
-    for (int i = 0; i < 8 && i < left; ++i)
-        reinterpret_cast<T*>(v.w)[i] = p[i];
+    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1 & 1);
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(p - odd);
+    uint32_t w[5];
+#pragma unroll
+    for (int j = 0; j < 5; ++j)
+        w[j] = 2 * j - odd < left && (j < 4 || odd) ? words[j] : 0u;
+    Pack<T> v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)  // (what is past the last element is not looked at)
+        v.w[j] = odd ? __funnelshift_r(w[j], w[j + 1], 16) : w[j];
     return v;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(256) sat_ffn_slope_kernel(const SlopeArgs a, const bool dh_vec, const bool p_vec)
 {
+    launch_dependents();
+    wait_for_earlier();
     const long long unit = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
     const long long r = unit / a.units, j = (unit - r * a.units) * 8;
     if (r >= a.rows)
@@ -423,8 +490,7 @@ cudaError_t launch_slope(const SlopeArgs& a, cudaStream_t s)
     const long long grid = ceil_div(a.rows * a.units, 256);
     if (grid >= kMost)
         return cudaErrorInvalidConfiguration;
-    sat_ffn_slope_kernel<T><<<static_cast<unsigned>(grid), 256, 0, s>>>(a, dh_vec, p_vec);
-    return cudaGetLastError();
+    return launch_early(sat_ffn_slope_kernel<T>, static_cast<unsigned>(grid), 256, 0, 1, s, a, dh_vec, p_vec);
 }
 
 int check_backward(const ffn_gated_args* a, const ffn_gated_grads* g)
@@ -515,7 +581,7 @@ int ffn_gated(const ffn_gated_args* args, void* stream)
     Product p{};
     Factor none{};
     p.epi = kGated;
-    rc = pack(a, k, nullptr, 0, a.workspace, sms, s, &p.x, &p.w, &none);
+    rc = pack(a, k, nullptr, 0, a.workspace, s, &p.x, &p.w, &none);
     if (rc)
         return rc;
     p.x.extent = a.rows;
@@ -574,7 +640,7 @@ int ffn_gated_backward(const ffn_gated_args* args, const ffn_gated_grads* grads,
     if (rc)
         return rc;
     Factor x{}, w{}, dh{};
-    rc = pack(a, k, a.preact ? nullptr : g.dh, g.lddh, g.workspace, sms, s, &x, &w, &dh);
+    rc = pack(a, k, a.preact ? nullptr : g.dh, g.lddh, g.workspace, s, &x, &w, &dh);
     if (rc)
         return rc;
     const int64_t ldz = dz_ld(a), half = ldz / 2;

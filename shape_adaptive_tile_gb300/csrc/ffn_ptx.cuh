@@ -69,6 +69,11 @@ __device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, uint32_t src,
                  : "memory");
 }
 
+// Programmatic launches: the next kernel of the stream may begin its set-up
+// now; and everything that earlier kernels wrote is there.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_earlier() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one()
 {

@@ -52,7 +52,7 @@ struct TileTraits {
     static constexpr int THREADS = (2 + EPI_WARPS) * 32;
     static constexpr int ACC_COLS = NP * BN;
     static constexpr int ACCS = SPLIT || (MX && BN > 128) ? 1 : 2;
-    static constexpr bool DRAIN = MX && !SPLIT;  // one accumulator, taken to registers at once
+    static constexpr bool DRAIN = !SPLIT && (MX || EPI == kGated);  // an accumulator is taken to registers at once
     // Scale columns of a stage: 4 for each of two words of 128 rows.
     static constexpr int SF_COLS = MX ? 8 * (NP + NQT) : 0;
     static constexpr int NEED_COLS = ACCS * ACC_COLS + STAGES * SF_COLS;
@@ -72,6 +72,9 @@ struct TileTraits {
     static_assert(SWAP || OUT_COLS % 64 == 0, "whole 64-column chunks");
     static_assert(STAGES >= 2 && NEED_COLS <= 512, "ring or tensor memory");
     static_assert((SWAP && BN <= 32 ? 2 : 1) * (SMEM_BYTES + 1024) <= 228 * 1024, "shared memory of an SM");
+    // CTAs of two launches may meet on an SM, and the later one's wait for the earlier one's end: whatever fits there
+    // together has to find its tensor memory together. Kernels of more than 151 KB meet none of 75.5 KB or more (with 1 KB of the system's each).
+    static_assert(SMEM_BYTES > 151 * 1024 || (SMEM_BYTES >= 75 * 1024 + 512 && TMEM_COLS <= 128), "tensor memory of an SM");
 };
 
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
@@ -87,9 +90,21 @@ __device__ __forceinline__ void act_grad(float g, float& a, float& d)
         a = g * s;
         d = s * fmaf(g, 1.0f - s, 1.0f);
     } else if constexpr (KIND == 2) {
-        const float c = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
+        // The normal distribution's integral by Abramowitz and Stegun, Handbook of Mathematical Functions, 26.2.17:
+        // 1 - phi(x) (b1 t + ... + b5 t^5) with t = 1 / (1 + 0.2316419 x) for x >= 0, off by at most 7.5e-8. Below 0 it is
+        // the product itself, without a difference. The derivative wants phi too. Half the instructions of erff, which
+        // bounded the epilogue.
+        const float x = fabsf(g);
+        const float t = __fdividef(1.0f, fmaf(0.2316419f, x, 1.0f));
+        const float phi = 0.39894228040143268f * __expf(-0.5f * g * g);
+        float q = fmaf(1.330274429f, t, -1.821255978f);
+        q = fmaf(q, t, 1.781477937f);
+        q = fmaf(q, t, -0.356563782f);
+        q = fmaf(q, t, 0.319381530f);
+        q *= t * phi;
+        const float c = g < 0.0f ? q : 1.0f - q;
         a = g * c;
-        d = fmaf(g * 0.39894228040143268f, __expf(-0.5f * g * g), c);
+        d = fmaf(g, phi, c);
     } else if constexpr (KIND == 3) {  // (1 + tanh y) / 2 = 1 / (1 + exp(-2 y))
         const float s = sigmoid(1.5957691216057308f * fmaf(0.044715f * g * g, g, g));
         a = g * s;
@@ -246,21 +261,28 @@ __device__ __forceinline__ void store_words(uint32_t sb, uint16_t* out, long lon
     uint16_t* o = out + start * ld;
 #pragma unroll 1
     for (int r0 = start; r0 < rows; r0 += 8) {
+        uint32_t v[8 / STEP], w[8 / STEP];
 #pragma unroll
         for (int i = 0; i < 8 / STEP; ++i) {
-            const uint32_t v = ld_shared_u32(at[i]);
-            const uint32_t w = ODD ? __funnelshift_r(v, ld_shared_u32(next[i]), 16) : v;
+            v[i] = ld_shared_u32(at[i]);
+            w[i] = ODD ? ld_shared_u32(next[i]) : 0u;
             at[i] += 1024;
             next[i] += 1024;
+        }
+#pragma unroll
+        for (int i = 0; i < 8 / STEP; ++i, o += step) {
+            if (ODD)
+                w[i] = __funnelshift_r(v[i], w[i], 16);
+            else
+                w[i] = v[i];
             if (r0 + i * STEP < rows) {
                 if (word)
-                    *reinterpret_cast<uint32_t*>(o + e) = w;
+                    *reinterpret_cast<uint32_t*>(o + e) = w[i];
                 if (tail)
-                    o[e] = static_cast<uint16_t>(w);
+                    o[e] = static_cast<uint16_t>(w[i]);
                 if (head)
-                    o[0] = static_cast<uint16_t>(v);
+                    o[0] = static_cast<uint16_t>(v[i]);
             }
-            o += step;
         }
     }
 }
@@ -347,6 +369,7 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
     const uint32_t abort_at = bars + 8u * (2 * T::STAGES + 13) + 4;
     static_assert(8 * (2 * T::STAGES + 14) <= T::BAR_BYTES, "barrier area");
 
+    launch_dependents();
     const uint32_t rank = T::CG == 2 || T::SPLIT ? cluster_ctarank() : 0u;
     const bool leader = T::SPLIT || rank == 0;  // of the MMA's CTA pair
 
@@ -386,6 +409,7 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
         if (T::CG == 2 && !leader && warp == 1 && lane == 0)
             mbar_arrive_cluster(map_to_cta(tmem_ready_bar, 0));
     }
+    wait_for_earlier();
     const Waiter wc{abort_at, T::CG == 2 ? map_to_cta(abort_at, rank ^ 1u) : abort_at, args.timeout_ns};
     constexpr bool kClu = T::CG == 2;
 
@@ -739,9 +763,9 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
             };
 
             if constexpr (T::DRAIN) {
-                // One accumulator: this warp's columns go to registers at once, and the next tile's products begin while
-                // these are worked on. Half the tile's columns a warp: 64 of each factor of a gated tile, else two
-                // chunks of 64.
+                // This warp's columns go to registers at once, and the accumulator back to the MMA warp (of one accumulator
+                // the next tile's products begin now). Half the tile's columns a warp: 64 of each factor of a gated tile,
+                // else two chunks of 64.
                 float v[4][32];
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
@@ -754,14 +778,30 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                 for (int g = 0; g < 4; ++g)
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        v[g][j] = ok ? alpha * v[g][j] : __uint_as_float(0x7FFFFFFFu);
+                        v[g][j] = !ok ? __uint_as_float(0x7FFFFFFFu) : any ? alpha * v[g][j] : 0.0f;
+                auto stage16 = [&](const float (&x)[32], int at) {  // 32 values of this row as 16-bit columns from `at` on
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        st_shared_v4u(piece(at / 8 + q), pack2(x[8 * q], x[8 * q + 1], kind), pack2(x[8 * q + 2], x[8 * q + 3], kind),
+                                      pack2(x[8 * q + 4], x[8 * q + 5], kind), pack2(x[8 * q + 6], x[8 * q + 7], kind));
+                };
+                constexpr int GROUPS = T::GATED ? 2 : 4;
+                const int first = col0 + half * GROUPS * 32;
                 if constexpr (T::GATED) {
+                    if (!T::MX && args.keep) {
+                        take();
+                        stage16(v[0], 0);
+                        stage16(v[1], 32);
+                        put(1, row0, first);
+                        take();
+                        stage16(v[2], 0);
+                        stage16(v[3], 32);
+                        put(2, row0, first);
+                    }
                     gate(v[0], v[2], activation);
                     gate(v[1], v[3], activation);
                 }
-                constexpr int GROUPS = T::GATED ? 2 : 4;
-                const int first = col0 + half * GROUPS * 32;
-                if (kind == 0) {
+                if (T::MX && kind == 0) {
 #pragma unroll
                     for (int g = 0; g < GROUPS; ++g) {
                         take();
@@ -772,17 +812,11 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                     }
                 } else {
 #pragma unroll
-                    for (int g = 0; g < GROUPS; ++g) {
-                        if (g % 2 == 0)
-                            take();
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            st_shared_v4u(piece((g & 1) * 4 + q), pack2(v[g][8 * q], v[g][8 * q + 1], kind),
-                                          pack2(v[g][8 * q + 2], v[g][8 * q + 3], kind),
-                                          pack2(v[g][8 * q + 4], v[g][8 * q + 5], kind),
-                                          pack2(v[g][8 * q + 6], v[g][8 * q + 7], kind));
-                        if (g % 2 == 1)
-                            put(0, row0, first + (g - 1) * 32);
+                    for (int g = 0; g < GROUPS; g += 2) {
+                        take();
+                        stage16(v[g], 0);
+                        stage16(v[g + 1], 32);
+                        put(0, row0, first + g * 32);
                     }
                 }
             } else if constexpr (T::SWAP) {
@@ -1004,22 +1038,12 @@ cudaError_t launch_tiles(const TileMaps& maps, const ScaleMaps* scales, const Ti
         if (dev < 64)
             ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(T::THREADS);
-    cfg.dynamicSmemBytes = T::SMEM_BYTES;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
     if constexpr (T::MX)
-        return cudaLaunchKernelEx(&cfg, sat_ffn_scaled_tile_kernel<T>, maps, *scales, args);
+        return launch_early(sat_ffn_scaled_tile_kernel<T>, static_cast<unsigned>(grid), T::THREADS, T::SMEM_BYTES,
+                            static_cast<unsigned>(cluster), stream, maps, *scales, args);
     else
-        return cudaLaunchKernelEx(&cfg, sat_ffn_tile_kernel<T>, maps, args);
+        return launch_early(sat_ffn_tile_kernel<T>, static_cast<unsigned>(grid), T::THREADS, T::SMEM_BYTES,
+                            static_cast<unsigned>(cluster), stream, maps, args);
 }
 
 template <class T>

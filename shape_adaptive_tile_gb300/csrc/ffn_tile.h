@@ -58,6 +58,29 @@ struct Variant {
                           cudaStream_t stream);
 };
 
+// A launch that may begin its set-up (up to wait_for_earlier) while the kernel
+// before it in the stream ends.
+template <class... Args>
+cudaError_t launch_early(void (*kernel)(Args...), unsigned grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t stream,
+                         Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // The variant, or nullptr (ffn_tiles_*.cu).
 const Variant* find_variant(int mx, int epi, int cg, int bn, int p_mn, int q_mn, int swap);
 

@@ -2,6 +2,8 @@
 #include <cuda_fp4.h>
 
 #include "ffn.h"
+#include "ffn_ptx.cuh"
+#include "ffn_tile.h"
 #include "rows.cuh"
 
 namespace {
@@ -56,6 +58,27 @@ __device__ __forceinline__ Pack<T> load8(const T* row, long long j, long long wi
     return v;
 }
 
+// The bits of the largest magnitude as an fp32 number: of 16-bit types two values at a time.
+__device__ __forceinline__ uint32_t magnitude(const Pack<float>& p)
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        top = max(top, p.w[k] & 0x7FFFFFFFu);
+    return top;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t magnitude(const Pack<T>& p)
+{
+    uint32_t two = p.w[0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int k = 1; k < 4; ++k)
+        two = __vmaxu2(two, p.w[k] & 0x7FFF7FFFu);
+    const uint16_t top = static_cast<uint16_t>(max(two & 0xFFFFu, two >> 16));
+    return __float_as_uint(to_f32(*reinterpret_cast<const T*>(&top)));
+}
+
 // Eight columns of four rows a thread, all loads in flight at once: four
 // threads a block of 32, sixteen a word of scales. A block's largest magnitude
 // is compared as bits (past the infinity come the NaN); its exponent field is
@@ -63,6 +86,8 @@ __device__ __forceinline__ Pack<T> load8(const T* row, long long j, long long wi
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) sat_mxfp4_quantize_kernel(const __grid_constant__ Args a)
 {
+    launch_dependents();
+    wait_for_earlier();
     const Place p = place(a);
     const long long j = p.unit * 8ll;
     Pack<T> in[4];
@@ -76,12 +101,10 @@ __global__ void __launch_bounds__(kThreads) sat_mxfp4_quantize_kernel(const __gr
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         float v[8];
-        uint32_t top = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 8; ++k)
             v[k] = to_f32(reinterpret_cast<const T*>(in[u].w)[k]);
-            top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
-        }
+        uint32_t top = magnitude(in[u]);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const uint32_t field = top >> 23;
@@ -109,6 +132,8 @@ __global__ void __launch_bounds__(kThreads) sat_mxfp4_quantize_kernel(const __gr
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) sat_mxfp4_dequantize_kernel(const __grid_constant__ Args a)
 {
+    launch_dependents();
+    wait_for_earlier();
     const Place p = place(a);
     if (!p.in || (p.unit >> 2) >= a.blocks)
         return;
@@ -188,14 +213,13 @@ cudaError_t launch(const mxfp4_args& a, cudaStream_t s)
     const long long grid = (k.sets + rows - 1) / rows * k.chunks;
     if (grid >= (INT64_C(1) << 31))
         return cudaErrorInvalidConfiguration;
-    const unsigned g = static_cast<unsigned>(grid);
     const bool vec = packs(a.values, a.ldv, a.type);
+    void (*kernel)(Args);
     if constexpr (kQuantize)
-        vec ? sat_mxfp4_quantize_kernel<T, true><<<g, kThreads, 0, s>>>(k) : sat_mxfp4_quantize_kernel<T, false><<<g, kThreads, 0, s>>>(k);
+        kernel = vec ? sat_mxfp4_quantize_kernel<T, true> : sat_mxfp4_quantize_kernel<T, false>;
     else
-        vec ? sat_mxfp4_dequantize_kernel<T, true><<<g, kThreads, 0, s>>>(k)
-            : sat_mxfp4_dequantize_kernel<T, false><<<g, kThreads, 0, s>>>(k);
-    return cudaGetLastError();
+        kernel = vec ? sat_mxfp4_dequantize_kernel<T, true> : sat_mxfp4_dequantize_kernel<T, false>;
+    return ffn::launch_early(kernel, static_cast<unsigned>(grid), kThreads, 0, 1, s, k);
 }
 
 template <bool kQuantize>
