@@ -136,46 +136,97 @@ int encode_scales(CUtensorMap* map, const Product& p, const Factor& f, int i)
     return rc ? map_error(rc) : GEMM_OK;
 }
 
+// A launch: its variant, tiles, and the CTAs that share a tile's k (or make a pair).
+struct Choice {
+    const Variant* v;
+    int64_t tp, tq;
+    int cluster;
+    double us;
+};
+
+// How long a kind of tile takes, in us: a launch with its first loads and last
+// stores, a tile's own overhead, a k-block, and adding up a shared tile's sums.
+// Measured on a GB300 over 65 to 2048 rows and 64 to 16384 of k, of which these
+// give the times to 10% or so, 20% at worst. What they decide: of 515 x 1008 by
+// 4016 of k, 13 us as 40 tiles of 128 x 128 shared by 3 CTAs against 25 as 12
+// pairs' tiles; of 2048 x 2048 by 4096, 24 us as 64 pairs' tiles against 37; gated,
+// 1024 x 1024 of 1024 outputs, 9.2 us as 128 single tiles against 10.5.
+struct Cost {
+    double launch, tile, block, join;
+};
+
+Cost cost_of(int mx, bool gated, int cg)
+{
+    if (cg == 2)
+        return mx ? Cost{5.0, 2.2, 0.28, 0.0} : Cost{6.5, 1.1, 0.26, 0.0};
+    if (mx)
+        return gated ? Cost{1.0, 2.3, 0.69, 6.0} : Cost{1.4, 3.8, 0.32, 2.0};
+    return Cost{2.0, 4.0, 0.20, 2.5};
+}
+
+Choice tiles_of(const Product& p, const Variant* v, int sms)
+{
+    const bool gated = p.epi != kStore;
+    Choice c{v, 0, 0, v->cg, 0.0};
+    if (v->swap) {
+        c.tp = ceil_div(p.cols, 128);
+        c.tq = ceil_div(p.rows, v->bn);
+    } else {
+        c.tp = ceil_div(p.rows, 128 * v->cg);
+        c.tq = ceil_div(p.cols, gated ? v->bn / 2 : v->bn);
+    }
+    const int64_t tiles = c.tp * c.tq * p.batch, num_kb = ceil_div(p.k, p.mx ? 256 : 64) * p.segments;
+    if (v->swap) {
+        // Every SM wants a CTA: all of them together keep the memory busy. Of 4-bit weights two, as their rings are short
+        // (8192 x 8192 gated by one token: 16.4 us as 256 CTAs, 23.1 as 128; 16-bit weights lose 1 to 3%). At least four
+        // k-blocks a CTA, and the sums have to fit in the ring.
+        const int64_t ctas = p.mx && v->bn <= 32 ? 2 * sms : sms;
+        int64_t s = 1;
+        while (s < 8 && tiles * (s + 1) <= ctas && num_kb / (s + 1) >= 4 &&
+               s * ceil_div(v->chunks, s + 1) * v->part_bytes <= v->ring_bytes)
+            ++s;
+        c.cluster = static_cast<int>(s);
+        return c;
+    }
+    const Cost t = cost_of(p.mx, gated, v->cg);
+    if (v->persistent) {
+        c.us = t.launch + ceil_div(tiles, sms / v->cg) * (t.tile + t.block * num_kb);
+        return c;
+    }
+    for (int64_t s = 1; s <= 8 && s <= std::max<int64_t>(1, num_kb / 4); ++s) {
+        if ((s - 1) * ceil_div(v->chunks, s) * v->part_bytes > v->ring_bytes)
+            break;
+        const double us = t.launch + ceil_div(tiles * s, sms) * (t.tile + t.block * ceil_div(num_kb, s) + (s > 1 ? t.join : 0.0));
+        if (s == 1 || us < c.us) {
+            c.cluster = static_cast<int>(s);
+            c.us = us;
+        }
+    }
+    return c;
+}
+
 int launch_product(const Product& p, int sms, cudaStream_t stream)
 {
     const bool gated = p.epi != kStore;
-    const int64_t bk = p.mx ? 256 : 64;
-    const int64_t num_kb = ceil_div(p.k, bk) * p.segments;
+    const int64_t num_kb = ceil_div(p.k, p.mx ? 256 : 64) * p.segments;
     // A few rows: the weights are the first operand, so that no accumulator row goes unused.
     const bool swap = p.w_is_weights && p.rows <= 64;
-    const Variant* v = nullptr;
-    int cluster = 1, grid = 0;
-    int64_t tp = 0, tq = 0;
+    Choice c;
     if (swap) {
-        v = find_variant(p.mx, p.epi, 1, p.rows <= 16 ? 16 : p.rows <= 32 ? 32 : 64, p.w.mn, p.x.mn, 1);
-        tp = ceil_div(p.cols, 128);
-        tq = ceil_div(p.rows, v->bn);
+        c = tiles_of(p, find_variant(p.mx, p.epi, 1, p.rows <= 16 ? 16 : p.rows <= 32 ? 32 : 64, p.w.mn, p.x.mn, 1), sms);
     } else {
-        const int64_t pairs = ceil_div(p.rows, 256) * ceil_div(p.cols, gated ? 128 : 256) * p.batch;
-        if (pairs >= sms / 2) {
-            v = find_variant(p.mx, p.epi, 2, 256, p.x.mn, p.w.mn, 0);
-            cluster = 2;
-        } else {
-            v = find_variant(p.mx, p.epi, 1, p.mx && gated ? 256 : 128, p.x.mn, p.w.mn, 0);
-        }
-        tp = ceil_div(p.rows, 128 * v->cg);
-        tq = ceil_div(p.cols, gated ? v->bn / 2 : v->bn);
+        c = tiles_of(p, find_variant(p.mx, p.epi, 2, 256, p.x.mn, p.w.mn, 0), sms);
+        const Choice one = tiles_of(p, find_variant(p.mx, p.epi, 1, p.mx && gated ? 256 : 128, p.x.mn, p.w.mn, 0), sms);
+        if (one.us < c.us)
+            c = one;
     }
-    const int64_t tiles = tp * tq * p.batch;
+    const Variant* v = c.v;
+    const int cluster = c.cluster;
+    const int64_t tp = c.tp, tq = c.tq, tiles = tp * tq * p.batch;
     if (tiles * 16 >= kMost)
         return fail_with(GEMM_ERR_ARG, "too many tiles");
+    const int grid = static_cast<int>(v->persistent ? std::min<int64_t>(tiles, sms / v->cg) * v->cg : tiles * cluster);
     TileArgs a{};
-    if (v->persistent) {
-        grid = static_cast<int>(std::min<int64_t>(tiles, sms / v->cg)) * v->cg;
-    } else {
-        // Share k among as many CTAs as fill the SMs, of four k-blocks at least, while the sums fit in the ring.
-        int64_t s = 1;
-        while (s < 8 && tiles * (s + 1) <= sms && num_kb / (s + 1) >= 4 &&
-               s * ceil_div(v->chunks, s + 1) * v->part_bytes <= v->ring_bytes)
-            ++s;
-        cluster = static_cast<int>(s);
-        grid = static_cast<int>(tiles * s);
-    }
     a.tiles_p = static_cast<int>(tp);
     a.tiles_q = static_cast<int>(tq);
     a.batch = p.batch;
