@@ -94,6 +94,7 @@ struct Product {
     int64_t rows, cols;  // of one output
     void* out[3];
     int64_t ld[3];
+    bool beside;  // needs nothing of the kernel before it
     bool padded;  // the outputs' rows go on to a whole number of 16 bytes that nobody reads
     const void* dh;
     int64_t lddh;
@@ -242,6 +243,7 @@ int launch_product(const Product& p, int sms, cudaStream_t stream)
     a.out_kind = p.out_type;
     a.add = p.add;
     a.keep = p.keep;
+    a.beside = p.beside;
     a.rows = static_cast<int>(p.rows);
     a.cols = static_cast<int>(p.cols);
     a.timeout_ns = kTimeoutNs;
@@ -395,8 +397,8 @@ struct CopyArgs {
 
 __global__ void __launch_bounds__(256) sat_ffn_copy_kernel(const __grid_constant__ CopyArgs a)
 {
-    launch_dependents();
     wait_for_earlier();
+    launch_dependents();
     long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
     int k = 0;
     while (k < a.n && i >= a.m[k].end)
@@ -481,7 +483,7 @@ struct SlopeArgs {
     const void* preact;
     void* dz;  // [dg du], the second half `half` elements after the first
     long long lddh, ldp, ldz, half;
-    int activation;
+    int activation, beside;
 };
 
 // Eight elements, or the `left` that there are; off 16 bytes from the words that hold them.
@@ -506,12 +508,15 @@ __device__ __forceinline__ Pack<T> load_at(const T* p, long long left, bool vec)
 template <typename T>
 __global__ void __launch_bounds__(256) sat_ffn_slope_kernel(const SlopeArgs a, const bool dh_vec, const bool p_vec)
 {
+    if (!a.beside)
+        wait_for_earlier();
     launch_dependents();
-    wait_for_earlier();
     const long long unit = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
     const long long r = unit / a.units, j = (unit - r * a.units) * 8;
-    if (r >= a.rows)
+    if (r >= a.rows) {
+        wait_for_earlier();
         return;
+    }
     const long long left = a.hidden - j;
     const T* pre = static_cast<const T*>(a.preact) + r * a.ldp + j;
     const Pack<T> d = load_at(static_cast<const T*>(a.dh) + r * a.lddh + j, left, dh_vec);
@@ -531,6 +536,7 @@ __global__ void __launch_bounds__(256) sat_ffn_slope_kernel(const SlopeArgs a, c
     T* z = static_cast<T*>(a.dz) + r * a.ldz + j;
     store_pack(z, dg);
     store_pack(z + a.half, du);
+    wait_for_earlier();
 }
 
 template <typename T>
@@ -717,6 +723,7 @@ int ffn_gated_backward(const ffn_gated_args* args, const ffn_gated_grads* grads,
         sl.ldz = ldz;
         sl.half = half;
         sl.activation = a.activation;
+        sl.beside = k.x || k.w;  // the copies are of x and w
         rc = cuda_rc(a.type == GEMM_C_BF16 ? launch_slope<__nv_bfloat16>(sl, s) : launch_slope<__half>(sl, s),
                      "launching the activation's gradient");
     } else {
@@ -757,6 +764,7 @@ int ffn_gated_backward(const ffn_gated_args* args, const ffn_gated_grads* grads,
         p.w = a.w_by_output ? in : z;
         p.k = a.rows;
         p.batch = 2;
+        p.beside = g.dx != nullptr;  // dx and dw both come from [dg du], which is there when the kernel of dx begins
         p.rows = p.x.extent;
         p.cols = p.w.extent;
         p.out_type = g.dw_type;

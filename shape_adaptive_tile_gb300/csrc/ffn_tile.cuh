@@ -369,7 +369,6 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
     const uint32_t abort_at = bars + 8u * (2 * T::STAGES + 13) + 4;
     static_assert(8 * (2 * T::STAGES + 14) <= T::BAR_BYTES, "barrier area");
 
-    launch_dependents();
     const uint32_t rank = T::CG == 2 || T::SPLIT ? cluster_ctarank() : 0u;
     const bool leader = T::SPLIT || rank == 0;  // of the MMA's CTA pair
 
@@ -409,7 +408,9 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
         if (T::CG == 2 && !leader && warp == 1 && lane == 0)
             mbar_arrive_cluster(map_to_cta(tmem_ready_bar, 0));
     }
-    wait_for_earlier();
+    if (!args.beside)
+        wait_for_earlier();
+    launch_dependents();
     const Waiter wc{abort_at, T::CG == 2 ? map_to_cta(abort_at, rank ^ 1u) : abort_at, args.timeout_ns};
     constexpr bool kClu = T::CG == 2;
 
@@ -768,10 +769,9 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                 // else two chunks of 64.
                 float v[4][32];
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    tmem_ld_32x32b_x32(acc_cols + (T::GATED ? (g >> 1) * (T::BN / 2) + half * 64 + (g & 1) * 32
-                                                            : half * 128 + g * 32),
-                                       reinterpret_cast<uint32_t(&)[32]>(v[g]));
+                for (int g = 0; g < 4; g += 2)
+                    tmem_ld_32x32b_x64(acc_cols + (T::GATED ? (g >> 1) * (T::BN / 2) + half * 64 : half * 128 + g * 32),
+                                       reinterpret_cast<uint32_t(&)[64]>(v[g]));
                 tmem_wait_ld();
                 release();
 #pragma unroll
@@ -991,6 +991,8 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
         __syncwarp();
     }
 
+    if (args.beside)
+        wait_for_earlier();  // this kernel's end is the end of the one before, too
     // ------------------------------------------------------------- teardown
     tc_fence_before();
     __syncthreads();

@@ -45,12 +45,42 @@ __device__ __forceinline__ Place place(const Args& a)
     return p;
 }
 
+// Eight elements of row[j ..]; past the width 0. Rows that start off 16 bytes:
+// by the 16-byte pieces around them where these lie in the row, shifted into
+// place (the shift is the same in all of a row's threads).
 template <typename T, bool kVec>
 __device__ __forceinline__ Pack<T> load8(const T* row, long long j, long long width)
 {
     if (kVec && j + 8 <= width)
         return load_pack(row + j);
     Pack<T> v{};
+    if constexpr (!kVec) {
+        constexpr int P = 16 / sizeof(T), N = sizeof(T) == 4 ? 3 : 2;
+        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row + j)) & 15u;
+        const int back = static_cast<int>(off / sizeof(T));
+        if (j >= back && j - back + N * P <= width) {
+            const uint4* from = reinterpret_cast<const uint4*>(row + j - back);
+            uint32_t w[4 * N + 3] = {};
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint4 q = __ldg(from + i);
+                w[4 * i] = q.x;
+                w[4 * i + 1] = q.y;
+                w[4 * i + 2] = q.z;
+                w[4 * i + 3] = q.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 4 * N; ++i)
+                w[i] = off & 8 ? w[i + 2] : w[i];
+#pragma unroll
+            for (int i = 0; i < 4 * N; ++i)
+                w[i] = off & 4 ? w[i + 1] : w[i];
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(2 * sizeof(T)); ++i)
+                v.w[i] = sizeof(T) == 2 && (off & 2) ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+            return v;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (j + i < width)
@@ -58,36 +88,38 @@ __device__ __forceinline__ Pack<T> load8(const T* row, long long j, long long wi
     return v;
 }
 
-// The bits of the largest magnitude as an fp32 number: of 16-bit types two values at a time.
-__device__ __forceinline__ uint32_t magnitude(const Pack<float>& p)
+// The exponent field, as an fp32 number's, of the largest magnitude: 255 with an infinity or a NaN among the values.
+__device__ __forceinline__ uint32_t largest_field(const Pack<float>& p)
 {
     uint32_t top = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         top = max(top, p.w[k] & 0x7FFFFFFFu);
-    return top;
+    return top >> 23;
 }
 
 template <typename T>
-__device__ __forceinline__ uint32_t magnitude(const Pack<T>& p)
+__device__ __forceinline__ uint32_t largest_field(const Pack<T>& p)  // 16-bit types: two values at a time
 {
     uint32_t two = p.w[0] & 0x7FFF7FFFu;
 #pragma unroll
     for (int k = 1; k < 4; ++k)
         two = __vmaxu2(two, p.w[k] & 0x7FFF7FFFu);
     const uint16_t top = static_cast<uint16_t>(max(two & 0xFFFFu, two >> 16));
-    return __float_as_uint(to_f32(*reinterpret_cast<const T*>(&top)));
+    return __float_as_uint(to_f32(*reinterpret_cast<const T*>(&top))) >> 23;
 }
 
 // Eight columns of four rows a thread, all loads in flight at once: four
-// threads a block of 32, sixteen a word of scales. A block's largest magnitude
-// is compared as bits (past the infinity come the NaN); its exponent field is
-// the logarithm rounded down.
+// threads a block of 32, sixteen a word of scales. The exponent field of a
+// block's largest magnitude is its logarithm rounded down (bits compare as
+// magnitudes do); the four rows' fields share a word, whose bytes are compared
+// and exchanged together: 4 shuffles for 32 values a thread instead of 16.
+// Bounded by the reads; 8192 x 8192 bf16: see the table of cases.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) sat_mxfp4_quantize_kernel(const __grid_constant__ Args a)
 {
-    launch_dependents();
     wait_for_earlier();
+    launch_dependents();
     const Place p = place(a);
     const long long j = p.unit * 8ll;
     Pack<T> in[4];
@@ -97,59 +129,108 @@ __global__ void __launch_bounds__(kThreads) sat_mxfp4_quantize_kernel(const __gr
             in[u] = load8<T, kVec>(static_cast<const T*>(a.values) + (p.row + 32 * u) * a.ldv, j, a.width);
         else
             in[u] = Pack<T>{};
-    uint32_t words[4];
+    uint32_t fields = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        fields |= largest_field(in[u]) << (8 * u);
+    fields = __vmaxu4(fields, __shfl_xor_sync(0xffffffffu, fields, 1));
+    fields = __vmaxu4(fields, __shfl_xor_sync(0xffffffffu, fields, 2));
+    // exponent + 127 of each row's block: two less, not below 0, and 255 for what is not finite.
+    const uint32_t bytes = __vsubus4(fields, 0x02020202u) | __vcmpeq4(fields, 0xFFFFFFFFu);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-        float v[8];
+        const uint32_t byte = bytes >> (8 * u) & 255u;
+        const float by = __uint_as_float((254u - byte) << 23);  // 2^-exponent, always a normal number (of 255: not used)
+        uint32_t w = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            v[k] = to_f32(reinterpret_cast<const T*>(in[u].w)[k]);
-        uint32_t top = magnitude(in[u]);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const uint32_t field = top >> 23;
-        const bool bad = field == 255;
-        const uint32_t byte = bad ? 255u : field > 2 ? field - 2 : 0u;        // exponent + 127
-        const float by = __uint_as_float(bad ? 0u : (254u - byte) << 23);     // 2^-exponent, always a normal number
-        if (p.in && p.row + 32 * u < a.rows && (p.unit >> 2) < a.blocks) {
-            uint32_t w = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 f = bad ? make_float2(0.0f, 0.0f) : make_float2(v[2 * k] * by, v[2 * k + 1] * by);
-                w |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(f, __NV_E2M1, cudaRoundNearest)) << (8 * k);
-            }
-            *reinterpret_cast<uint32_t*>(a.codes + (p.row + 32 * u) * a.ldc + p.unit * 4) = w;
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = make_float2(to_f32(reinterpret_cast<const T*>(in[u].w)[2 * k]) * by,
+                                         to_f32(reinterpret_cast<const T*>(in[u].w)[2 * k + 1]) * by);
+            w |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(f, __NV_E2M1, cudaRoundNearest)) << (8 * k);
         }
-        uint32_t word = byte << (8 * (threadIdx.x / 4 % 4));
-        word |= __shfl_xor_sync(0xffffffffu, word, 4);
-        word |= __shfl_xor_sync(0xffffffffu, word, 8);
-        words[u] = word;  // 0 for rows past the last one
+        if (p.in && p.row + 32 * u < a.rows && (p.unit >> 2) < a.blocks)
+            *reinterpret_cast<uint32_t*>(a.codes + (p.row + 32 * u) * a.ldc + p.unit * 4) = byte == 255 ? 0u : w;
     }
-    if (p.in && threadIdx.x % 16 == 0)
-        a.scales[p.at] = make_uint4(words[0], words[1], words[2], words[3]);
+    // The bytes of four blocks x four rows, each block's in one group of lanes, turned: group g gets row g's word.
+    const int g = threadIdx.x >> 2 & 3;
+    uint32_t other = __shfl_xor_sync(0xffffffffu, bytes, 4);
+    uint32_t word = __byte_perm(bytes, other, g & 1 ? 0x3715 : 0x6240);
+    other = __shfl_xor_sync(0xffffffffu, word, 8);
+    word = __byte_perm(word, other, g & 2 ? 0x3276 : 0x5410);
+    if (p.in && (threadIdx.x & 3) == 0)
+        reinterpret_cast<uint32_t*>(a.scales + p.at)[g] = word;  // 0 for rows past the last one
+}
+
+// Eight elements a thread to row[j ..], of rows that start off 16 bytes (all of a
+// warp's threads; `in`: this one has elements). A thread writes the 16-byte
+// pieces that begin among its elements, the last of them with the next lane's;
+// elements at the row's or the warp's ends, in no such piece, go one by one.
+// (All one by one, 8192 x 8191 bf16 took 174 us instead of 36.)
+template <typename T>
+__device__ __forceinline__ void store_shifted(T* row, long long j, long long width, const Pack<T>& v, bool in, bool same_as_next,
+                                              bool same_as_last)
+{
+    constexpr int P = 16 / sizeof(T), W = 2 * sizeof(T), PIECES = W / 4;
+    uint32_t w[W + 4 + 3] = {};
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        w[i] = v.w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[W + i] = __shfl_down_sync(0xffffffffu, v.w[i], 1);
+    if (!in)
+        return;
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row + j)) & 15u, skip = (16u - off) & 15u;
+    const int first = static_cast<int>(skip / sizeof(T));  // element that the first piece begins with
+#pragma unroll
+    for (int i = 0; i < W + 4; ++i)
+        w[i] = skip & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < W + 4; ++i)
+        w[i] = skip & 4 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        w[i] = sizeof(T) == 2 && (skip & 2) ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+    int done = first;  // elements from `first` on that pieces take
+#pragma unroll
+    for (int k = 0; k < PIECES; ++k) {
+        const bool mine = first + (k + 1) * P <= 8;
+        if (j + first + (k + 1) * P <= width && (mine || same_as_next)) {
+            *reinterpret_cast<uint4*>(row + j + first + k * P) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            done = first + (k + 1) * P;
+        }
+    }
+    const bool head = first > 0 && !(same_as_last && j + first <= width);  // no piece of the last lane's reaches in here
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if ((i < first ? head : i >= done) && j + i < width)
+            row[j + i] = reinterpret_cast<const T*>(v.w)[i];
 }
 
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) sat_mxfp4_dequantize_kernel(const __grid_constant__ Args a)
 {
-    launch_dependents();
     wait_for_earlier();
+    launch_dependents();
     const Place p = place(a);
-    if (!p.in || (p.unit >> 2) >= a.blocks)
+    const bool in = p.in && (p.unit >> 2) < a.blocks;
+    if (kVec && !in)
         return;
     const long long j = p.unit * 8ll;
-    const uint4 s4 = a.scales[p.at];
+    const uint4 s4 = in ? a.scales[p.at] : make_uint4(0, 0, 0, 0);
     const uint32_t words[4] = {s4.x, s4.y, s4.z, s4.w};
     uint32_t codes[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-        codes[u] = p.row + 32 * u < a.rows
+        codes[u] = in && p.row + 32 * u < a.rows
                        ? *reinterpret_cast<const uint32_t*>(a.codes + (p.row + 32 * u) * a.ldc + p.unit * 4)
                        : 0u;
+    // Whether the neighbouring lanes have the row's next and last eight columns.
+    const int lane = threadIdx.x & 31, in_row = threadIdx.x % a.per_row;
+    const bool same_as_next = lane < 31 && in_row + 1 < a.per_row, same_as_last = lane > 0 && in_row > 0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-        if (p.row + 32 * u >= a.rows)
-            return;
+        const bool here = in && p.row + 32 * u < a.rows;
         const uint32_t byte = words[u] >> (8 * (p.unit / 4 % 4)) & 255u;
         // 2^(byte - 127): of byte 0 it is below the normal numbers.
         const float by = __uint_as_float(byte == 255 ? 0x7FFFFFFFu : byte ? byte << 23 : 0x00400000u);
@@ -163,9 +244,11 @@ __global__ void __launch_bounds__(kThreads) sat_mxfp4_dequantize_kernel(const __
             reinterpret_cast<T*>(out.w)[2 * k] = from_f32<T>(f.x * by);
             reinterpret_cast<T*>(out.w)[2 * k + 1] = from_f32<T>(f.y * by);
         }
-        if (kVec && j + 8 <= a.width) {
+        if constexpr (!kVec) {
+            store_shifted(row, j, a.width, out, here, same_as_next, same_as_last);
+        } else if (here && j + 8 <= a.width) {
             store_pack(row + j, out);
-        } else {
+        } else if (here) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 if (j + k < a.width)
