@@ -241,8 +241,9 @@ __device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, const Wa
 
 // 16-bit rows start, start + STEP, ... of a staged chunk, all of which start on
 // a word (ODD false) or all between two words (ODD): then a lane's second
-// element and the next lane's first make a word, and the row's first element and
-// its last go by themselves.
+// element and the next lane's first make a word. (A store costs the same some four
+// cycles of the SM whatever it moves, so the rows' ends are left to two stores
+// for all rows together.)
 template <bool ODD, int STEP>
 __device__ __forceinline__ void store_words(uint32_t sb, uint16_t* out, long long ld, int start, int rows, int n)
 {
@@ -256,7 +257,7 @@ __device__ __forceinline__ void store_words(uint32_t sb, uint16_t* out, long lon
         next[i] = sb + r * 128 + ((((l1 >> 2) ^ r) << 4) | ((l1 & 3) << 2));
     }
     const int e = 2 * lane + (ODD ? 1 : 0);  // first element of this lane's word
-    const bool word = e + 1 < n, tail = e == n - 1, head = ODD && lane == 0 && n > 0;
+    const bool word = e + 1 < n;
     const long long step = static_cast<long long>(STEP) * ld;
     uint16_t* o = out + start * ld;
 #pragma unroll 1
@@ -275,14 +276,8 @@ __device__ __forceinline__ void store_words(uint32_t sb, uint16_t* out, long lon
                 w[i] = __funnelshift_r(v[i], w[i], 16);
             else
                 w[i] = v[i];
-            if (r0 + i * STEP < rows) {
-                if (word)
-                    *reinterpret_cast<uint32_t*>(o + e) = w[i];
-                if (tail)
-                    o[e] = static_cast<uint16_t>(w[i]);
-                if (head)
-                    o[0] = static_cast<uint16_t>(v[i]);
-            }
+            if (r0 + i * STEP < rows && word)
+                *reinterpret_cast<uint32_t*>(o + e) = w[i];
         }
     }
 }
@@ -314,6 +309,19 @@ static __device__ __noinline__ void store_rows(uint32_t sb, void* at, long long 
     }
     uint16_t* o = static_cast<uint16_t*>(at) + first;
     const int n = min(64, left), odd = static_cast<int>(reinterpret_cast<uintptr_t>(o) >> 1 & 1);
+    // A lane a row: the first element of rows that start between two words, and the last where it is not in a word.
+    if (lane < rows && n > 0) {
+        const int mine = (odd + (static_cast<int>(ld) & 1) * lane) & 1;
+        auto element = [&](int c) {
+            const uint32_t w = ld_shared_u32(sb + lane * 128 + (((c >> 3) ^ (lane & 7)) << 4) + ((c & 6) << 1));
+            return static_cast<uint16_t>(c & 1 ? w >> 16 : w);
+        };
+        const uint16_t first_one = element(0), last_one = element(n - 1);
+        if (mine)
+            o[lane * ld] = first_one;
+        if ((n ^ mine) & 1)
+            o[lane * ld + n - 1] = last_one;
+    }
     if (ld & 1) {
         store_words<false, 2>(sb, o, ld, odd, rows, n);
         store_words<true, 2>(sb, o, ld, 1 - odd, rows, n);
