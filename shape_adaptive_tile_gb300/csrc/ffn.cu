@@ -38,7 +38,6 @@ using namespace sat::rows;
 using namespace sat::ffn;
 
 constexpr int64_t kMost = INT64_C(1) << 31;
-constexpr unsigned long long kTimeoutNs = 2000000000ull;
 
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 int64_t ceil_div(int64_t n, int64_t by) { return (n + by - 1) / by; }
@@ -94,7 +93,7 @@ struct Product {
     int64_t rows, cols;  // of one output
     void* out[3];
     int64_t ld[3];
-    bool beside;  // needs nothing of the kernel before it
+    bool beside, next_beside;  // needs nothing of the kernel before it; nor does the next one of this
     bool padded;  // the outputs' rows go on to a whole number of 16 bytes that nobody reads
     const void* dh;
     int64_t lddh;
@@ -244,9 +243,9 @@ int launch_product(const Product& p, int sms, cudaStream_t stream)
     a.add = p.add;
     a.keep = p.keep;
     a.beside = p.beside;
+    a.next_beside = p.next_beside;
     a.rows = static_cast<int>(p.rows);
     a.cols = static_cast<int>(p.cols);
-    a.timeout_ns = kTimeoutNs;
     const int outs = p.epi == kStore ? p.batch : p.epi == kGrad ? 2 : p.keep ? 3 : 1;
     TileMaps m{};
     ScaleMaps sm{};
@@ -508,9 +507,9 @@ __device__ __forceinline__ Pack<T> load_at(const T* p, long long left, bool vec)
 template <typename T>
 __global__ void __launch_bounds__(256) sat_ffn_slope_kernel(const SlopeArgs a, const bool dh_vec, const bool p_vec)
 {
+    launch_dependents();  // (the next one waits)
     if (!a.beside)
         wait_for_earlier();
-    launch_dependents();
     const long long unit = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
     const long long r = unit / a.units, j = (unit - r * a.units) * 8;
     if (r >= a.rows) {
@@ -753,8 +752,10 @@ int ffn_gated_backward(const ffn_gated_args* args, const ffn_gated_grads* grads,
         p.cols = a.width;
         p.out[0] = g.dx;
         p.ld[0] = g.lddx;
+        p.next_beside = g.dw != nullptr;
         rc = launch_product(p, sms, s);
         p.segments = 1;
+        p.next_beside = false;
     }
     if (!rc && g.dw) {
         // A product for each half of dw, over the rows of x and of [dg du].

@@ -197,46 +197,63 @@ __device__ __forceinline__ void unpack2(uint32_t v, int kind, float& lo, float& 
     }
 }
 
-// A bounded wait of a whole warp (or of the threads that call it). After two
-// seconds the CTA's abort flag is raised (a pair's other CTA's too): all waits
-// then end at once, the loops run to their ends on whatever is there, and the
-// epilogue writes NaN. The clock is read only after a few tries: a ring whose
-// stages are used up as fast as they come waits at every one of them.
+// Waits are bounded: a whole warp's, each of at most kWaitNs. Who gives up raises
+// the CTA's abort flag (and a pair's other CTA's), and every wait that is not over
+// then gives up too. Nothing more is loaded, multiplied or released after that, so
+// no stage is filled and no barrier armed out of turn; outputs whose sums have not
+// come are NaN; and the CTA ends only after the limit again (2 ms at least), when
+// whatever was on its way has landed. The clock is read only after a few tries: a
+// ring whose stages are used up as fast as they come waits at every one of them.
+#ifndef SAT_FFN_WAIT_NS
+#define SAT_FFN_WAIT_NS 2000000000ull
+#endif
+constexpr unsigned long long kWaitNs = SAT_FFN_WAIT_NS;
+constexpr int kWaitTries = kWaitNs > 0 ? 64 : 0, kWaitRound = kWaitNs > 0 ? 32 : 1;
+
 struct Waiter {
     uint32_t abort;       // shared address of the flag
     uint32_t peer_abort;  // the same of the pair's other CTA, or of this one
-    unsigned long long timeout_ns;
 
     __device__ __forceinline__ bool aborted() const { return ld_shared_u32(abort) != 0; }
 };
 
+// Of a whole warp: true or false in all lanes.
 template <bool kCluster>
-static __device__ __noinline__ void wait_long(uint32_t bar, uint32_t parity, const Waiter w)
+static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, const Waiter w)
 {
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
-        for (int i = 0; i < 32; ++i)
-            if (mbar_try_wait<kCluster>(bar, parity))
-                return;
-        if (w.aborted())
-            return;
-        if (globaltimer_ns() - t0 > w.timeout_ns) {
+        bool there = false;
+        for (int i = 0; i < kWaitRound && !there; ++i)
+            there = kWaitNs > 0 ? mbar_try_wait<kCluster>(bar, parity) : mbar_test_wait<kCluster>(bar, parity);
+        if (__all_sync(0xffffffffu, there))
+            return true;
+        if (__any_sync(0xffffffffu, w.aborted()))
+            return false;
+        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 >= kWaitNs)) {
             st_shared_u32(w.abort, 1u);
             if (w.peer_abort != w.abort)
                 st_cluster_u32(w.peer_abort, 1u);
-            return;
+            return false;
         }
     }
 }
 
 template <bool kCluster>
-__device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, const Waiter& w)
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, const Waiter& w)
 {
+    bool there = false;
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait<kCluster>(bar, parity))
-            return;
-    wait_long<kCluster>(bar, parity, w);
+    for (int i = 0; i < kWaitTries && !there; ++i)
+        there = mbar_try_wait<kCluster>(bar, parity);
+    return __all_sync(0xffffffffu, there) || wait_long<kCluster>(bar, parity, w);
+}
+
+static __device__ __noinline__ void wait_again()
+{
+    const uint64_t t0 = globaltimer_ns(), ns = kWaitNs > 2000000ull ? kWaitNs : 2000000ull;
+    while (globaltimer_ns() - t0 < ns)
+        __nanosleep(1000);
 }
 
 // 16-bit rows start, start + STEP, ... of a staged chunk, all of which start on
@@ -332,6 +349,19 @@ static __device__ __noinline__ void store_rows(uint32_t sb, void* at, long long 
     }
 }
 
+// NaN in `rows` rows and `cols` columns of out[i] from (row0, col0) on, where they are in the output.
+static __device__ __noinline__ void store_nan(const TileArgs& a, int i, int row0, int rows, int col0, int cols)
+{
+    for (int r = row0; r < min(row0 + rows, a.rows); ++r)
+        for (int c = col0 + (threadIdx.x & 31); c < min(col0 + cols, a.cols); c += 32) {
+            const long long at = static_cast<long long>(r) * a.ld[i] + c;
+            if (a.out_kind == 0)
+                static_cast<uint32_t*>(a.out[i])[at] = 0x7FFFFFFFu;
+            else
+                static_cast<uint16_t*>(a.out[i])[at] = 0x7FFFu;  // a NaN of bf16 as of fp16
+        }
+}
+
 struct Tile {
     int tp, tq, z;
 };
@@ -350,6 +380,34 @@ __device__ __forceinline__ Tile tile_of(int t, const TileArgs& a)
     w.tp = first + r % gs;
     w.tq = r / gs;
     return w;
+}
+
+// The producer's or the MMA warp's end after a wait that gave up: all that is left
+// of the kernel for it, so that the loops above need no way out (with one, the
+// compiler takes what follows a wait for code of single lanes, 40% slower).
+template <class T>
+static __device__ __noinline__ void end_warp(uint32_t tmem_base, int csize, int beside)
+{
+    __syncwarp();
+    if (T::SPLIT && csize > 1) {
+        for (int i = 0; i < 2; ++i) {
+            __syncthreads();
+            cluster_sync();
+        }
+    }
+    wait_again();
+    if (beside)
+        wait_for_earlier();
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (T::CG == 2)
+        cluster_sync();
+    if (threadIdx.x >> 5 == 1) {
+        tc_fence_after();
+        tmem_dealloc<T::CG>(tmem_base, T::TMEM_COLS);
+    }
+    asm volatile("exit;");
 }
 
 template <class T>
@@ -416,10 +474,15 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
         if (T::CG == 2 && !leader && warp == 1 && lane == 0)
             mbar_arrive_cluster(map_to_cta(tmem_ready_bar, 0));
     }
+    // The next kernel may start its set-up once this one's CTAs all have their tensor memory, or, where it will not wait
+    // itself (next_beside), once all that came before this one is over.
+    if (!args.next_beside && warp == 1)
+        launch_dependents();
     if (!args.beside)
         wait_for_earlier();
-    launch_dependents();
-    const Waiter wc{abort_at, T::CG == 2 ? map_to_cta(abort_at, rank ^ 1u) : abort_at, args.timeout_ns};
+    if (args.next_beside)
+        launch_dependents();
+    const Waiter wc{abort_at, T::CG == 2 ? map_to_cta(abort_at, rank ^ 1u) : abort_at};
     constexpr bool kClu = T::CG == 2;
 
     // Persistent: tiles t0, t0 + step, ... Split: the cluster's one tile, this
@@ -431,6 +494,11 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
     const int step = T::SPLIT ? tiles : static_cast<int>(gridDim.x) / T::CG;
     const int kb0 = T::SPLIT ? min(args.num_kb, static_cast<int>(rank) * args.kb_per_rank) : 0;
     const int kb1 = T::SPLIT ? min(args.num_kb, kb0 + args.kb_per_rank) : args.num_kb;
+
+    auto give_up = [&] {
+        end_warp<T>(tmem_base, csize, args.beside);
+        __builtin_unreachable();
+    };
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -445,8 +513,8 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
             for (int i = 0; i < kb1 - kb0; ++i) {
                 // Alternate waves run through k in opposite directions: each starts on what the last left in L2.
                 const int kb = !T::SPLIT && (wave & 1) ? kb1 - 1 - i : kb0 + i;
-                wait_for<false>(empty_bar(stage), phase ^ 1u, wc);
-                __syncwarp();
+                if (!wait_for<false>(empty_bar(stage), phase ^ 1u, wc))
+                    give_up();
                 const int seg = kb >= args.seg_kb ? 1 : 0;
                 const int zi = seg | w.z;
                 const int k0 = (kb - seg * args.seg_kb) * (T::MX ? 128 : 64);  // 4-bit maps count bytes
@@ -508,7 +576,8 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
         }
         // Until every stage filled above has been read.
         for (int i = 0; i < T::STAGES; ++i) {
-            wait_for<false>(empty_bar(stage), phase ^ 1u, wc);
+            if (!wait_for<false>(empty_bar(stage), phase ^ 1u, wc))
+                give_up();
             if (++stage == T::STAGES) {
                 stage = 0;
                 phase ^= 1u;
@@ -521,8 +590,10 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
             const bool one = elect_one();
             int stage = 0, acc = 0;
             uint32_t acc_phase = 0;
-            if constexpr (T::CG == 2)
-                wait_for<true>(tmem_ready_bar, 0, wc);
+            if constexpr (T::CG == 2) {
+                if (!wait_for<true>(tmem_ready_bar, 0, wc))
+                    give_up();
+            }
             // The scales of a stage go to tensor memory (to columns of that stage's own) before the products of the stage
             // before it, so that no product waits for them: two words of each 128 rows of the first operand(s), then for
             // each word all row tiles of the second.
@@ -531,8 +602,8 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
             int next = 0, next_stage = 0;  // the first block whose data has not been waited for, and its stage
             uint32_t next_phase = 0;
             auto arrive = [&] {
-                wait_for<false>(full_bar(next_stage), next_phase, wc);
-                __syncwarp();
+                if (!wait_for<false>(full_bar(next_stage), next_phase, wc))
+                    give_up();
                 tc_fence_after();
                 if constexpr (T::MX) {
                     const uint32_t src = sS + next_stage * T::SF_BYTES;
@@ -561,9 +632,9 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
             const uint64_t adesc = T::P_MN ? sdesc(sP, 8192, 1024, kLayoutSW128) : sdesc(sP, 16, 1024, kLayoutSW128);
             const uint64_t bdesc = T::Q_MN ? sdesc(sQ, 8192, 1024, kLayoutSW128) : sdesc(sQ, 16, 1024, kLayoutSW128);
             int wave = 0, done = 0;
-            for (int t = t0; done < mine; t += step, ++wave) {
-                wait_for<kClu>(tempty_bar(acc), acc_phase ^ 1u, wc);
-                __syncwarp();
+            while (done < mine) {
+                if (!wait_for<kClu>(tempty_bar(acc), acc_phase ^ 1u, wc))
+                    give_up();
                 tc_fence_after();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(acc * T::ACC_COLS);
                 for (int i = 0; i < per_tile; ++i, ++done) {
@@ -608,6 +679,7 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                     if (++stage == T::STAGES)
                         stage = 0;
                 }
+                ++wave;
                 if (++acc == T::ACCS) {
                     acc = 0;
                     acc_phase ^= 1u;
@@ -619,7 +691,7 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
 
     // -------------------------------------------------------------- epilogue
     const int ew = warp - 2, sub = warp & 3, half = ew >> 2;
-    bool ok = true;  // false: a wait gave up, and what is written is NaN
+    bool ok = true;  // false: a wait gave up, and the outputs are NaN from then on
     uint32_t acc_cols = 0;  // this tile's accumulator, at this warp's lanes
     // GC accumulator columns from `col` on, of row sub * 32 + lane; in a split tile with the other CTAs' sums added,
     // in rank order after this CTA's own. part: their place in the partial sums (in groups of GC columns).
@@ -647,8 +719,7 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
         // All CTAs' products are done (their rings are free), then every CTA sends the chunks that others own to these.
         if (warp >= 2) {
             if (kb1 > kb0)
-                wait_for<false>(tfull_bar(0), 0, wc);
-            ok = __all_sync(0xffffffffu, !wc.aborted());
+                ok = wait_for<false>(tfull_bar(0), 0, wc);
             tc_fence_after();
             acc_cols = tmem_base + (static_cast<uint32_t>(sub * 32) << 16);
         }
@@ -699,7 +770,6 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
         uint32_t acc_phase = 0, load_phase = 0;
         const int kind = args.out_kind, activation = args.activation;
         const float alpha = args.alpha;
-        const bool any = args.num_kb > 0;
 
         // Hands the staged 32 rows x 128 bytes (in the stores' swizzle) to out[i]: rows row0 .., columns col0 ...
         auto put = [&](int i, int row0, int col0) {
@@ -729,7 +799,8 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
         const uint32_t my_row = sb + static_cast<uint32_t>(lane * 128);
         auto piece = [&](int q) { return my_row + static_cast<uint32_t>((q ^ (lane & 7)) << 4); };
 
-        for (int t = t0; t < tiles; t += step) {
+        int t = t0;
+        for (; t < tiles; t += step) {
             const Tile w = tile_of(t, args);
             const int row0 = w.tp * (128 * T::CG) + (T::CG == 2 ? static_cast<int>(rank) * 128 : 0) + sub * 32;
             const int col0 = w.tq * T::OUT_COLS;
@@ -737,18 +808,17 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                 if constexpr (T::EPI == kGrad) {
                     // dh comes into the staging buffer while the products run.
                     take();
-                    if (lane == 0 && half < T::NCHUNK && row0 < args.rows && col0 + half * 64 < args.cols) {
+                    if (ok && lane == 0 && half < T::NCHUNK && row0 < args.rows && col0 + half * 64 < args.cols) {
                         mbar_arrive_expect_tx(load_bar(ew), 4096);
                         tma_load_2d(sb, &maps.o[2], load_bar(ew), col0 + half * 64, row0);
                     }
                 }
-                if (any)
-                    wait_for<false>(tfull_bar(acc), acc_phase, wc);
-                ok = __all_sync(0xffffffffu, !wc.aborted());
+                if (ok)
+                    ok = wait_for<false>(tfull_bar(acc), acc_phase, wc);
                 tc_fence_after();
                 acc_cols = tmem_base + (static_cast<uint32_t>(sub * 32) << 16) + static_cast<uint32_t>(acc * T::ACC_COLS);
             }
-            // One group of accumulator columns, scaled; NaN where a wait gave up, 0 where there is nothing to add up.
+            // One group of accumulator columns, scaled.
             auto fetch32 = [&](float (&v)[32], int col, int chunk, int group) {
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(acc_cols + col, r);
@@ -756,7 +826,7 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                 add_parts(r, 8, chunk, group, T::CHUNK_ACC / 32);
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                    v[j] = !ok ? __uint_as_float(0x7FFFFFFFu) : any ? alpha * __uint_as_float(r[j]) : 0.0f;
+                    v[j] = alpha * __uint_as_float(r[j]);
             };
             auto release = [&] {
                 if constexpr (!T::SPLIT) {
@@ -771,22 +841,25 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                 }
             };
 
+            if (!ok)
+                break;
             if constexpr (T::DRAIN) {
                 // This warp's columns go to registers at once, and the accumulator back to the MMA warp (of one accumulator
                 // the next tile's products begin now). Half the tile's columns a warp: 64 of each factor of a gated tile,
                 // else two chunks of 64.
                 float v[4][32];
 #pragma unroll
-                for (int g = 0; g < 4; g += 2)
-                    tmem_ld_32x32b_x64(acc_cols + (T::GATED ? (g >> 1) * (T::BN / 2) + half * 64 : half * 128 + g * 32),
-                                       reinterpret_cast<uint32_t(&)[64]>(v[g]));
+                for (int g = 0; g < 4; ++g)
+                    tmem_ld_32x32b_x32(acc_cols + (T::GATED ? (g >> 1) * (T::BN / 2) + half * 64 + (g & 1) * 32
+                                                            : half * 128 + g * 32),
+                                       reinterpret_cast<uint32_t(&)[32]>(v[g]));
                 tmem_wait_ld();
                 release();
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        v[g][j] = !ok ? __uint_as_float(0x7FFFFFFFu) : any ? alpha * v[g][j] : 0.0f;
+                        v[g][j] = alpha * v[g][j];
                 auto stage16 = [&](const float (&x)[32], int at) {  // 32 values of this row as 16-bit columns from `at` on
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
@@ -809,7 +882,7 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                     gate(v[0], v[2], activation);
                     gate(v[1], v[3], activation);
                 }
-                if (T::MX && kind == 0) {
+                if (T::MX && kind == 0) {  // (fp32 outputs: of 4-bit operands only)
 #pragma unroll
                     for (int g = 0; g < GROUPS; ++g) {
                         take();
@@ -842,7 +915,7 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                         add_parts(r, 4, c, group, T::CHUNK_ACC / 16);
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            v[j] = !ok ? __uint_as_float(0x7FFFFFFFu) : any ? alpha * __uint_as_float(r[j]) : 0.0f;
+                            v[j] = alpha * __uint_as_float(r[j]);
                     };
                     take16(g, c * 16, 0);
                     if constexpr (T::GATED)
@@ -913,10 +986,11 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                             }
                         }
                         if (row0 < args.rows && cc < args.cols) {
-                            wait_for<false>(load_bar(ew), load_phase, wc);
+                            ok = wait_for<false>(load_bar(ew), load_phase, wc);
                             load_phase ^= 1u;
                         }
-                        ok = __all_sync(0xffffffffu, !wc.aborted());
+                        if (!ok)
+                            break;
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
                             ld_shared_v4u(piece(q), hw[4 * q], hw[4 * q + 1], hw[4 * q + 2], hw[4 * q + 3]);
@@ -992,6 +1066,21 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                 acc_phase ^= 1u;
             }
         }
+        for (; t < tiles; t += step) {  // a wait gave up: this warp's outputs of the tiles that are left
+            const Tile w = tile_of(t, args);
+            const int row0 = w.tp * (128 * T::CG) + (T::CG == 2 ? static_cast<int>(rank) * 128 : 0) + sub * 32;
+            const int outs = T::EPI == kGrad ? 2 : T::EPI == kGated && args.keep ? 3 : 1;
+            for (int o = 0; o < outs; ++o)
+                for (int c = half; c < T::NCHUNK; c += 2) {
+                    if (!own(c))
+                        continue;
+                    const int col = w.tq * T::OUT_COLS + c * T::CHUNK;
+                    if (T::SWAP)
+                        store_nan(args, o, col, T::CHUNK, row0, 32);
+                    else
+                        store_nan(args, T::EPI == kStore ? w.z : o, row0, 32, col, T::CHUNK);
+                }
+        }
         if (!T::SWAP && lane == 0) {
             bulk_wait<0>();
             fence_proxy_async_global();
@@ -999,6 +1088,8 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
         __syncwarp();
     }
 
+    if (__any_sync(0xffffffffu, wc.aborted()))
+        wait_again();
     if (args.beside)
         wait_for_earlier();  // this kernel's end is the end of the one before, too
     // ------------------------------------------------------------- teardown

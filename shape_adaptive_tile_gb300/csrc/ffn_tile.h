@@ -33,12 +33,12 @@ struct TileArgs {
     int keep;      // kGated: the pre-activations are wanted
     int rows, cols;  // of one output matrix
     int beside;      // this kernel needs nothing of the one before it in the stream, and may run beside it
+    int next_beside; // so may the next one beside this
     void* out[3];    // kStore: batch 0 and 1; kGated: h, gate, up; kGrad: dg, du
     long long ld[3];
     int tma_out;     // bit i: out[i] is written by bulk tensor stores through o[i],
     int tma_edge;    // boxes that reach past the last column too
     int sf_rows_p, sf_rows_q;  // scale rows (512 bytes) of a row tile, i.e. ceil(K / 128); 0 where unscaled
-    unsigned long long timeout_ns;
 };
 
 struct TileMaps {
@@ -60,10 +60,10 @@ struct Variant {
 };
 
 // A launch that may begin its set-up (up to wait_for_earlier) while the kernel
-// before it in the stream ends. Each kernel launched this way lets the next one
-// begin (launch_dependents) once it has waited itself, so that all that came
-// before it is over by then; a kernel that needs nothing of the one before it can
-// do its work at once, and waits before it ends.
+// before it in the stream ends. A kernel that needs nothing of the one before it
+// can do its work at once, and waits before it ends; the one before it then lets
+// it begin (launch_dependents) only once it has waited itself, so that all that
+// came earlier is over.
 template <class... Args>
 cudaError_t launch_early(void (*kernel)(Args...), unsigned grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t stream,
                          Args... args)

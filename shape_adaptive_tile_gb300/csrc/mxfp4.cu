@@ -118,8 +118,8 @@ __device__ __forceinline__ uint32_t largest_field(const Pack<T>& p)  // 16-bit t
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) sat_mxfp4_quantize_kernel(const __grid_constant__ Args a)
 {
-    wait_for_earlier();
     launch_dependents();
+    wait_for_earlier();
     const Place p = place(a);
     const long long j = p.unit * 8ll;
     Pack<T> in[4];
@@ -210,8 +210,8 @@ __device__ __forceinline__ void store_shifted(T* row, long long j, long long wid
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) sat_mxfp4_dequantize_kernel(const __grid_constant__ Args a)
 {
-    wait_for_earlier();
     launch_dependents();
+    wait_for_earlier();
     const Place p = place(a);
     const bool in = p.in && (p.unit >> 2) < a.blocks;
     if (kVec && !in)
