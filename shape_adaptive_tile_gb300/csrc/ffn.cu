@@ -93,7 +93,7 @@ struct Product {
     int64_t rows, cols;  // of one output
     void* out[3];
     int64_t ld[3];
-    bool beside, next_beside;  // needs nothing of the kernel before it; nor does the next one of this
+    bool beside;  // needs nothing of the kernel before it
     bool padded;  // the outputs' rows go on to a whole number of 16 bytes that nobody reads
     const void* dh;
     int64_t lddh;
@@ -243,7 +243,6 @@ int launch_product(const Product& p, int sms, cudaStream_t stream)
     a.add = p.add;
     a.keep = p.keep;
     a.beside = p.beside;
-    a.next_beside = p.next_beside;
     a.rows = static_cast<int>(p.rows);
     a.cols = static_cast<int>(p.cols);
     const int outs = p.epi == kStore ? p.batch : p.epi == kGrad ? 2 : p.keep ? 3 : 1;
@@ -752,10 +751,8 @@ int ffn_gated_backward(const ffn_gated_args* args, const ffn_gated_grads* grads,
         p.cols = a.width;
         p.out[0] = g.dx;
         p.ld[0] = g.lddx;
-        p.next_beside = g.dw != nullptr;
         rc = launch_product(p, sms, s);
         p.segments = 1;
-        p.next_beside = false;
     }
     if (!rc && g.dw) {
         // A product for each half of dw, over the rows of x and of [dg du].

@@ -72,8 +72,9 @@ struct TileTraits {
     static_assert(SWAP || OUT_COLS % 64 == 0, "whole 64-column chunks");
     static_assert(STAGES >= 2 && NEED_COLS <= 512, "ring or tensor memory");
     static_assert((SWAP && BN <= 32 ? 2 : 1) * (SMEM_BYTES + 1024) <= 228 * 1024, "shared memory of an SM");
-    // CTAs of two launches may meet on an SM, and the later one's wait for the earlier one's end: whatever fits there
-    // together has to find its tensor memory together. Kernels of more than 151 KB meet none of 75.5 KB or more (with 1 KB of the system's each).
+    // CTAs of a kernel and of one beside it may meet on an SM, and the later ones wait for the earlier ones' end: whatever
+    // fits there together has to find its tensor memory together. One of more than 151 KB meets none of 75.5 KB or more
+    // (with 1 KB of the system's each).
     static_assert(SMEM_BYTES > 151 * 1024 || (SMEM_BYTES >= 75 * 1024 + 512 && TMEM_COLS <= 128), "tensor memory of an SM");
 };
 
@@ -461,6 +462,10 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
     __syncthreads();
     if constexpr (T::CG == 2)
         cluster_sync();
+    // Tensor memory is taken only now: a CTA that held it while it waited could keep it from one that it waits for. With
+    // that done, the next kernel of the stream may start its set-up, or, where it needs nothing of this one, its work.
+    if (!args.beside)
+        wait_for_earlier();
     uint32_t tmem_base = 0;
     if (warp >= 1) {
         if (warp == 1) {
@@ -474,13 +479,7 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
         if (T::CG == 2 && !leader && warp == 1 && lane == 0)
             mbar_arrive_cluster(map_to_cta(tmem_ready_bar, 0));
     }
-    // The next kernel may start its set-up once this one's CTAs all have their tensor memory, or, where it will not wait
-    // itself (next_beside), once all that came before this one is over.
-    if (!args.next_beside && warp == 1)
-        launch_dependents();
-    if (!args.beside)
-        wait_for_earlier();
-    if (args.next_beside)
+    if (warp == 1)
         launch_dependents();
     const Waiter wc{abort_at, T::CG == 2 ? map_to_cta(abort_at, rank ^ 1u) : abort_at};
     constexpr bool kClu = T::CG == 2;
@@ -693,8 +692,8 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
     const int ew = warp - 2, sub = warp & 3, half = ew >> 2;
     bool ok = true;  // false: a wait gave up, and the outputs are NaN from then on
     uint32_t acc_cols = 0;  // this tile's accumulator, at this warp's lanes
-    // GC accumulator columns from `col` on, of row sub * 32 + lane; in a split tile with the other CTAs' sums added,
-    // in rank order after this CTA's own. part: their place in the partial sums (in groups of GC columns).
+    // Adds the other CTAs' sums of a split tile, in rank order, to this one's: 4 n4 columns of row sub * 32 + lane, which
+    // are group `colgroup` of the `groups` of a chunk.
     auto add_parts = [&](uint32_t* r, int n4, int chunk, int colgroup, int groups) {
         if constexpr (T::SPLIT) {
             const int per = (T::NCHUNK + split - 1) / split;  // chunks a CTA may own

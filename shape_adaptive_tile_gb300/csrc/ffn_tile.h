@@ -33,7 +33,6 @@ struct TileArgs {
     int keep;      // kGated: the pre-activations are wanted
     int rows, cols;  // of one output matrix
     int beside;      // this kernel needs nothing of the one before it in the stream, and may run beside it
-    int next_beside; // so may the next one beside this
     void* out[3];    // kStore: batch 0 and 1; kGated: h, gate, up; kGrad: dg, du
     long long ld[3];
     int tma_out;     // bit i: out[i] is written by bulk tensor stores through o[i],

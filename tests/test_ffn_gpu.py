@@ -274,3 +274,75 @@ def test_offsets_past_32_bits():
     assert sat.ffn_gated(a, stream()) == 0, sat.gemm_last_error()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_a_training_step_of_the_block():
+    # Gated product, down projection, its gradients and the gated product's, with the library's own products between; each
+    # step against the definition on what the step before it gave.
+    rows, width, hidden = 384, 256, 640
+    c = Case(3, rows, width, hidden, "bf16", "silu")
+    down = ref.rows(c.g, hidden, width, "bf16", scale=hidden**-0.5)
+    dy = ref.rows(c.g, rows, width, "bf16")
+    h, pre = c.forward(keep=True)
+    ref.assert_within(h, *ref.Gated(c.x, c.w, True, hidden).h("bf16", "silu"), "h")
+    y, dh, ddown = (torch.empty(*s, device="cuda", dtype=torch.bfloat16) for s in ((rows, width), (rows, hidden), (hidden, width)))
+    products = ((h, down, y, rows, width, hidden, False, False), (dy, down, dh, rows, hidden, width, False, True),
+                (h, dy, ddown, hidden, width, rows, True, False))
+    for a, b, to, m, n, k, ta, tb in products:
+        with sat.Plan(m, n, k, "bf16", trans_a=ta, trans_b=tb, c_type="bf16") as plan:
+            plan.run(a, b, to, 1.0, 0.0, stream())
+            torch.cuda.synchronize()
+        u, v = (a.double().t() if ta else a.double()), (b.double().t() if tb else b.double())
+        want, off = u @ v, ref.sum_error(k, u.abs() @ v.abs())
+        ref.assert_within(to, want, off + ref.half_step(want.abs() + off, "bf16"), "product")
+    c.dh = dh
+    gx, gw = c.backward(pre, "fp32")
+    dx, off_dx, dw, off_dw = ref.gradients(c.x, c.w, True, hidden, "bf16", "silu", dh, pre)
+    ref.assert_within(gx, dx, off_dx + ref.half_step(dx.abs() + off_dx, "bf16"), "dx")
+    ref.assert_within(gw, dw, off_dw + ref.half_step(dw.abs() + off_dw, "fp32"), "dw")
+
+
+def test_two_streams_at_once():
+    cases = [Case(s, 515, 264, 1001, "fp16", "gelu", pad=3) for s in (1, 2)]
+    want = [(c.forward()[0].clone(), *(t.clone() for t in c.backward())) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    runs = []
+    for c in cases:  # buffers of each call's own
+        h, gx, gw = c.out(515, 1001, "fp16"), c.out(515, 264, "fp16"), c.out(2002, 264, "fp16")
+        a = c.args(h=h, ldh=h.stride(0))
+        size = sat.ffn_gated_workspace(a)
+        a.workspace, a.workspace_bytes = scratch(size), size
+        b = c.args()
+        g = sat.FfnGrads(dh=c.dh, lddh=c.dh.stride(0), dx=gx, lddx=gx.stride(0), dw=gw, lddw=gw.stride(0), dw_type="fp16")
+        size = sat.ffn_gated_backward_workspace(b, g)
+        g.workspace, g.workspace_bytes = scratch(size), size
+        runs.append((a, b, g, (h, gx, gw)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (a, b, g, _) in zip(streams, runs):
+            assert sat.ffn_gated(a, s.cuda_stream) == 0 and sat.ffn_gated_backward(b, g, s.cuda_stream) == 0
+    torch.cuda.synchronize()
+    for w, r in zip(want, runs):
+        assert all(torch.equal(x, y) for x, y in zip(w, r[3]))
+
+
+def test_the_first_call_of_a_process_may_be_a_captured_one():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(sat.__file__)))
+    code = """
+import torch, shape_adaptive_tile_gb300 as sat
+x, w = torch.randn(300, 256, device="cuda").bfloat16(), torch.randn(1024, 256, device="cuda").bfloat16() / 16
+h = torch.zeros(300, 512, device="cuda", dtype=torch.bfloat16)
+a = sat.FfnArgs(rows=300, width=256, hidden=512, type="bf16", activation="none", w_by_output=1, x=x, ldx=256, w=w, ldw=256, h=h, ldh=512)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    sat.check(sat.ffn_gated(a, torch.cuda.current_stream().cuda_stream))
+g.replay()
+torch.cuda.synchronize()
+z = x.double() @ w.double().t()
+assert float((h.double() - z[:, :512] * z[:, 512:]).abs().max()) < 0.1
+"""
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True, timeout=300)

@@ -288,3 +288,26 @@ def test_offsets_past_32_bits():
     a.copy_(p.a[0])
     p.a = (a, *p.a[1:])
     assert torch.equal(p.run(), want)
+
+
+def test_scales_of_every_size():
+    # Scales at both ends: powers that cancel are exact, whatever they are, as long as the products are normal numbers.
+    for ea, eb in ((254, 0), (0, 254), (127, 127), (200, 54), (10, 240), (3, 250), (190, 100)):
+        p = Product(3, 70, 136, 256)
+        for m, n, e in ((p.a, 70, ea), (p.b, 136, eb)):
+            code = ref.quantized(torch.randn(n, 256, generator=torch.Generator().manual_seed(n)))[0]
+            byte = torch.full((n, 8), e, dtype=torch.uint8)
+            m[0].copy_(ref.pack(code, m[0].shape[1]))
+            m[1].copy_(ref.tile_scales(byte, 256))
+            m[2].copy_(ref.values(code, byte))
+        p.check()
+
+
+def test_weights_quantised_as_two_halves_of_a_buffer():
+    # Strides of the gate's and the other weights may differ, and rows may lie inside a larger buffer.
+    p = Product(5, 90, 200, 160, "bf16", "silu")
+    wide = torch.zeros(200, 160, device="cuda", dtype=torch.uint8)
+    wide[:, :80] = p.up[0]
+    want = p.run().clone()
+    p.up = (wide[:, :80], *p.up[1:])
+    assert torch.equal(p.run(), want)
