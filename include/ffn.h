@@ -37,7 +37,7 @@ typedef enum {
     FFN_SILU = 1,      /* g / (1 + exp(-g)) */
     FFN_GELU = 2,      /* g (1 + erf(g / sqrt 2)) / 2 */
     FFN_GELU_TANH = 3, /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
-    FFN_RELU = 4       /* max(g, 0); its derivative at 0 is 0 */
+    FFN_RELU = 4       /* max(g, 0), NaN of NaN; its derivative at 0 is 0 */
 } ffn_activation_t;
 
 /* ---- gated product -----------------------------------------------------------
@@ -86,7 +86,7 @@ int ffn_gated(const ffn_gated_args* args, void* stream);
  * from x and w (one product more, nothing kept). dg and du are rounded to the
  * type in the workspace: they are operands of the products, as x and w are. dw
  * lies as w does; accumulate != 0 adds to what dw holds (fp32 only, so that
- * what is added is not rounded to fewer bits). Either of dx and dw may be NULL
+ * what is added is not rounded to fewer bits; sums below 2^-126 may become 0). Either of dx and dw may be NULL
  * and is then not computed. With rows == 0 dw is set to 0 (or left, with
  * accumulate). args->h and args->workspace are not used. */
 typedef struct {

@@ -223,7 +223,8 @@ int launch_product(const Product& p, int sms, cudaStream_t stream)
     const Variant* v = c.v;
     const int cluster = c.cluster;
     const int64_t tp = c.tp, tq = c.tq, tiles = tp * tq * p.batch;
-    if (tiles * 16 >= kMost)
+    // (The kernels count tiles, and a CTA's k-blocks, in 32 bits; at a quarter of a microsecond each that is minutes.)
+    if (tiles * 16 >= kMost || ceil_div(tiles, sms / 2) * num_kb >= kMost)
         return fail_with(GEMM_ERR_ARG, "too many tiles");
     const int grid = static_cast<int>(v->persistent ? std::min<int64_t>(tiles, sms / v->cg) * v->cg : tiles * cluster);
     TileArgs a{};
@@ -309,11 +310,11 @@ struct Copies {
     int64_t at_x, at_w, at_w2, at_dh, end;
 };
 
-Copies copies_of(const ffn_gated_args& a, const void* dh, int64_t lddh, bool uses_x, int64_t at)
+Copies copies_of(const ffn_gated_args& a, const void* dh, int64_t lddh, bool uses_x, bool uses_w, int64_t at)
 {
     Copies k{};
     k.x = uses_x && !rows16(a.x, a.ldx);
-    k.w = !rows16(a.w, a.ldw) || (!a.w_by_output && a.hidden % 8 != 0);
+    k.w = uses_w && (!rows16(a.w, a.ldw) || (!a.w_by_output && a.hidden % 8 != 0));
     k.dh = dh && !rows16(dh, lddh);
     if (k.x) {
         k.ldx = packed_ld(a.width);
@@ -583,7 +584,8 @@ int64_t dz_ld(const ffn_gated_args& a) { return 2 * round_up(a.hidden, 8); }
 
 Copies backward_copies(const ffn_gated_args& a, const ffn_gated_grads& g)
 {
-    return copies_of(a, a.preact ? nullptr : g.dh, g.lddh, !a.preact || g.dw, round_up(a.rows * dz_ld(a) * 2, 128));
+    return copies_of(a, a.preact ? nullptr : g.dh, g.lddh, !a.preact || g.dw, !a.preact || g.dx,
+                     round_up(a.rows * dz_ld(a) * 2, 128));
 }
 
 bool backward_empty(const ffn_gated_args& a, const ffn_gated_grads& g)
@@ -603,7 +605,7 @@ int64_t ffn_gated_workspace(const ffn_gated_args* args)
         return rc;
     if (args->rows == 0 || args->width == 0 || args->hidden == 0)
         return 0;
-    return copies_of(*args, nullptr, 0, true, 0).end;
+    return copies_of(*args, nullptr, 0, true, true, 0).end;
 }
 
 int ffn_gated(const ffn_gated_args* args, void* stream)
@@ -626,7 +628,7 @@ int ffn_gated(const ffn_gated_args* args, void* stream)
             e = cudaMemset2DAsync(a.preact, a.ldp * 2, 0, a.hidden * 4, a.rows, s);
         return cuda_rc(e, "clearing h");
     }
-    const Copies k = copies_of(a, nullptr, 0, true, 0);
+    const Copies k = copies_of(a, nullptr, 0, true, true, 0);
     rc = check_workspace(a.workspace, a.workspace_bytes, k.end, "ffn_gated_workspace");
     int sms = 0;
     if (!rc)
