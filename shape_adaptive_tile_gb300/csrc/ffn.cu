@@ -142,32 +142,34 @@ struct Choice {
     int64_t tp, tq;
     int cluster;
     double us;
+    cudaError_t error;
 };
 
 // How long a kind of tile takes, in us: a launch with its first loads and last
-// stores, a tile's own overhead, a k-block, and adding up a shared tile's sums.
-// Measured on a GB300 over 65 to 2048 rows and 64 to 16384 of k, of which these
-// give the times to 10% or so, 20% at worst. What they decide: of 515 x 1008 by
-// 4016 of k, 13 us as 40 tiles of 128 x 128 shared by 3 CTAs against 25 as 12
-// pairs' tiles; of 2048 x 2048 by 4096, 24 us as 64 pairs' tiles against 37; gated,
-// 1024 x 1024 of 1024 outputs, 9.2 us as 128 single tiles against 10.5.
+// stores, a tile's own overhead, a k-block, and adding up the sums of a tile that
+// CTAs share, once and for each of them. Measured on a GB300 over 65 to 2048 rows
+// and 64 to 16384 of k, of which these give the times to 10% or so, 20% at worst.
+// What they decide: of 256 x 1024 by 8192 of k, 17 us as 16 tiles of 128 x 128
+// shared by 4 CTAs against 36 unshared and 41 as 4 pairs' tiles; of 2048 x 2048 by
+// 4096, 24 us as 64 pairs' tiles against 37; gated, 1024 x 1024 of 1024 outputs, 8.6
+// us as 128 single tiles against 10.0.
 struct Cost {
-    double launch, tile, block, join;
+    double launch, tile, block, join, share;
 };
 
 Cost cost_of(int mx, bool gated, int cg)
 {
     if (cg == 2)
-        return mx ? Cost{5.0, 2.2, 0.28, 0.0} : Cost{6.5, 1.1, 0.26, 0.0};
+        return mx ? Cost{5.0, 2.2, 0.28, 0.0, 0.0} : Cost{4.5, 1.1, 0.27, 0.0, 0.0};
     if (mx)
-        return gated ? Cost{1.0, 2.3, 0.69, 6.0} : Cost{1.4, 3.8, 0.32, 2.0};
-    return Cost{2.0, 4.0, 0.20, 2.5};
+        return gated ? Cost{1.0, 6.0, 0.455, 2.4, 0.35} : Cost{1.4, 3.8, 0.32, 1.2, 0.45};
+    return Cost{2.0, 2.5, 0.225, 0.8, 0.65};
 }
 
 Choice tiles_of(const Product& p, const Variant* v, int sms)
 {
     const bool gated = p.epi != kStore;
-    Choice c{v, 0, 0, v->cg, 0.0};
+    Choice c{v, 0, 0, v->cg, 0.0, cudaSuccess};
     if (v->swap) {
         c.tp = ceil_div(p.cols, 128);
         c.tq = ceil_div(p.rows, v->bn);
@@ -182,9 +184,15 @@ Choice tiles_of(const Product& p, const Variant* v, int sms)
         // k-blocks a CTA, and the sums have to fit in the ring.
         const int64_t ctas = p.mx && v->bn <= 32 ? 2 * sms : sms;
         int64_t s = 1;
-        while (s < 8 && tiles * (s + 1) <= ctas && num_kb / (s + 1) >= 4 &&
-               s * ceil_div(v->chunks, s + 1) * v->part_bytes <= v->ring_bytes)
-            ++s;
+        for (int64_t n = 2; n <= 8 && tiles * n <= ctas && num_kb / n >= 4; ++n) {
+            if ((n - 1) * ceil_div(v->chunks, n) * v->part_bytes > v->ring_bytes)
+                continue;
+            int fit = 0;
+            if ((c.error = v->fit(static_cast<int>(n), &fit)) != cudaSuccess)
+                return c;
+            if (tiles <= fit)
+                s = n;
+        }
         c.cluster = static_cast<int>(s);
         return c;
     }
@@ -195,8 +203,13 @@ Choice tiles_of(const Product& p, const Variant* v, int sms)
     }
     for (int64_t s = 1; s <= 8 && s <= std::max<int64_t>(1, num_kb / 4); ++s) {
         if ((s - 1) * ceil_div(v->chunks, s) * v->part_bytes > v->ring_bytes)
-            break;
-        const double us = t.launch + ceil_div(tiles * s, sms) * (t.tile + t.block * ceil_div(num_kb, s) + (s > 1 ? t.join : 0.0));
+            continue;
+        int fit = sms;
+        if (s > 1 && (c.error = v->fit(static_cast<int>(s), &fit)) != cudaSuccess)
+            return c;
+        if (fit < 1)
+            continue;
+        const double us = t.launch + ceil_div(tiles, fit) * (t.tile + t.block * ceil_div(num_kb, s) + (s > 1 ? t.join + t.share * s : 0.0));
         if (s == 1 || us < c.us) {
             c.cluster = static_cast<int>(s);
             c.us = us;
@@ -217,9 +230,11 @@ int launch_product(const Product& p, int sms, cudaStream_t stream)
     } else {
         c = tiles_of(p, find_variant(p.mx, p.epi, 2, 256, p.x.mn, p.w.mn, 0), sms);
         const Choice one = tiles_of(p, find_variant(p.mx, p.epi, 1, p.mx && gated ? 256 : 128, p.x.mn, p.w.mn, 0), sms);
-        if (one.us < c.us)
+        if (one.error != cudaSuccess || one.us < c.us)
             c = one;
     }
+    if (c.error != cudaSuccess)
+        return fail_with(GEMM_ERR_LAUNCH, "asking for a tile kernel's clusters: %s", cudaGetErrorString(c.error));
     const Variant* v = c.v;
     const int cluster = c.cluster;
     const int64_t tp = c.tp, tq = c.tq, tiles = tp * tq * p.batch;

@@ -58,7 +58,7 @@ struct TileTraits {
     static constexpr int NEED_COLS = ACCS * ACC_COLS + STAGES * SF_COLS;
     static constexpr int TMEM_COLS = NEED_COLS <= 32 ? 32 : NEED_COLS <= 64 ? 64 : NEED_COLS <= 128 ? 128 : NEED_COLS <= 256 ? 256 : 512;
     // Columns of one epilogue step, counted in output columns.
-    static constexpr int CHUNK = SWAP ? 16 : 64;
+    static constexpr int CHUNK = SWAP ? 16 : SPLIT ? 32 : 64;
     static constexpr int OUT_COLS = GATED && !SWAP ? BN / 2 : BN;  // output columns of a tile (swapped: tokens)
     static constexpr int NCHUNK = OUT_COLS / CHUNK;
     static constexpr int CHUNK_ACC = GATED ? 2 * CHUNK : CHUNK;    // accumulator columns of a chunk
@@ -69,7 +69,7 @@ struct TileTraits {
     static_assert(!SPLIT || CG == 1, "split tiles are 1-SM");
     static_assert(!DRAIN || BN == 256, "half the tile's columns a warp");
     static_assert(EPI != kGrad || !SWAP, "no swapped gradient");
-    static_assert(SWAP || OUT_COLS % 64 == 0, "whole 64-column chunks");
+    static_assert(OUT_COLS % CHUNK == 0, "whole chunks");
     static_assert(STAGES >= 2 && NEED_COLS <= 512, "ring or tensor memory");
     static_assert((SWAP && BN <= 32 ? 2 : 1) * (SMEM_BYTES + 1024) <= 228 * 1024, "shared memory of an SM");
     // CTAs of a kernel and of one beside it may meet on an SM, and the later ones wait for the earlier ones' end: whatever
@@ -147,6 +147,27 @@ __device__ __forceinline__ void gate(float (&g)[N], const float (&u)[N], int kin
             float a, d;
             act_grad<decltype(k)::value>(g[j], a, d);
             g[j] = a * u[j];
+        }
+    });
+}
+
+__device__ __forceinline__ void unpack2(uint32_t v, int kind, float& lo, float& hi);
+
+// From gate g, other factor u and dh (pairs of 16-bit elements): g = dg, u = du.
+__device__ __forceinline__ void slope(float (&g)[32], float (&u)[32], const uint32_t (&dh)[16], int kind, int activation)
+{
+    with_act(activation, [&](auto k) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            float d[2];
+            unpack2(dh[j], kind, d[0], d[1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float a, s;
+                act_grad<decltype(k)::value>(g[2 * j + e], a, s);
+                g[2 * j + e] = d[e] * u[2 * j + e] * s;
+                u[2 * j + e] = d[e] * a;
+            }
         }
     });
 }
@@ -840,6 +861,12 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                 }
             };
 
+            auto stage16 = [&](const float (&x)[32], int at) {  // 32 values of this row as 16-bit columns from `at` on
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    st_shared_v4u(piece(at / 8 + q), pack2(x[8 * q], x[8 * q + 1], kind), pack2(x[8 * q + 2], x[8 * q + 3], kind),
+                                  pack2(x[8 * q + 4], x[8 * q + 5], kind), pack2(x[8 * q + 6], x[8 * q + 7], kind));
+            };
             if (!ok)
                 break;
             if constexpr (T::DRAIN) {
@@ -859,12 +886,6 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         v[g][j] = alpha * v[g][j];
-                auto stage16 = [&](const float (&x)[32], int at) {  // 32 values of this row as 16-bit columns from `at` on
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        st_shared_v4u(piece(at / 8 + q), pack2(x[8 * q], x[8 * q + 1], kind), pack2(x[8 * q + 2], x[8 * q + 3], kind),
-                                      pack2(x[8 * q + 4], x[8 * q + 5], kind), pack2(x[8 * q + 6], x[8 * q + 7], kind));
-                };
                 constexpr int GROUPS = T::GATED ? 2 : 4;
                 const int first = col0 + half * GROUPS * 32;
                 if constexpr (T::GATED) {
@@ -929,11 +950,89 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                     }
                     store_column(args.out[0], kind, tok0 * args.ld[0] + f, args.ld[0], n, g);
                 }
-            } else if constexpr (T::EPI == kStore) {
+            } else if constexpr (T::SPLIT) {
+                // 32 output columns at a time, dealt to the CTAs and to both halves of the warps: with 64, half of the warps
+                // of half of the CTAs added up a gated tile's sums. Rows on 16 bytes go straight out of the registers.
+                auto out32 = [&](int i, const float (&x)[32], int cc) {
+                    if (kind == 0) {
+                        take();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            st_shared_v4(piece(q), x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+                        put(i, row0, cc);
+                        return;
+                    }
+                    uint32_t p[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        p[q] = pack2(x[2 * q], x[2 * q + 1], kind);
+                    if (((args.tma_out >> i) & 1) && cc + 32 <= args.cols) {
+                        if (row0 + lane < args.rows) {
+                            uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.out[i]) +
+                                                                static_cast<long long>(row0 + lane) * args.ld[i] + cc);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                o[q] = make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
+                        }
+                        return;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        st_shared_v4u(piece(q), p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
+                    __syncwarp();
+                    store_rows(sb, args.out[i], static_cast<long long>(row0) * args.ld[i] + cc, args.ld[i], kind,
+                               min(32, args.rows - row0), min(32, args.cols - cc), false);
+                    __syncwarp();
+                };
 #pragma unroll 1
                 for (int c = half; c < T::NCHUNK; c += 2) {
                     if (!own(c))
                         continue;
+                    const int cc = col0 + c * 32;
+                    if constexpr (T::EPI == kGrad) {
+                        fence_proxy_async_smem();
+                        take();
+                        if (row0 < args.rows && cc < args.cols) {
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(load_bar(ew), 4096);
+                                tma_load_2d(sb, &maps.o[2], load_bar(ew), cc, row0);
+                            }
+                            ok = wait_for<false>(load_bar(ew), load_phase, wc);
+                            load_phase ^= 1u;
+                        }
+                        if (!ok)
+                            break;
+                    }
+                    float v[32];
+                    fetch32(v, c * 32, c, 0);
+                    if constexpr (!T::GATED) {
+                        out32(w.z, v, cc);
+                    } else {
+                        float u[32];
+                        fetch32(u, T::BN / 2 + c * 32, c, 1);
+                        if constexpr (T::EPI == kGated) {
+                            if (args.keep) {
+                                out32(1, v, cc);
+                                out32(2, u, cc);
+                            }
+                            gate(v, u, activation);
+                            out32(0, v, cc);
+                        } else {
+                            uint32_t hw[16];  // this row's 32 values of dh (of the 64 that a box brings)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                ld_shared_v4u(piece(q), hw[4 * q], hw[4 * q + 1], hw[4 * q + 2], hw[4 * q + 3]);
+                            slope(v, u, hw, kind, activation);
+                            out32(0, v, cc);
+                            out32(1, u, cc);
+                        }
+                    }
+                }
+                if (!ok)
+                    break;
+            } else if constexpr (T::EPI == kStore) {
+#pragma unroll 1
+                for (int c = half; c < T::NCHUNK; c += 2) {
                     if (kind == 0) {
 #pragma unroll 1
                         for (int g = 0; g < 2; ++g) {
@@ -955,110 +1054,48 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                             fetch32(v, c * 64 + g * 32, c, g);
                             if (c + 2 >= T::NCHUNK && g == 1)
                                 release();
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                st_shared_v4u(piece(g * 4 + q), pack2(v[8 * q], v[8 * q + 1], kind),
-                                              pack2(v[8 * q + 2], v[8 * q + 3], kind), pack2(v[8 * q + 4], v[8 * q + 5], kind),
-                                              pack2(v[8 * q + 6], v[8 * q + 7], kind));
+                            stage16(v, g * 32);
                         }
                         put(w.z, row0, col0 + c * 64);
                     }
                 }
-                if constexpr (T::NCHUNK < 2) {
-                    if (half >= T::NCHUNK)
-                        release();
-                }
             } else {
-                // Gated tiles: 64 output columns a warp (128-column tiles) or, of 64-column tiles, the first four warps.
-                static_assert(T::NCHUNK <= 2, "a chunk a warp");
-                if (half >= T::NCHUNK || !own(half)) {
-                    release();
-                } else {
-                    const int c = half, cc = col0 + c * 64;
-                    uint32_t hw[32];  // kGrad: this row's 64 values of dh
-                    if constexpr (T::EPI == kGrad) {
-                        if (T::SPLIT) {
-                            take();
-                            if (lane == 0 && row0 < args.rows && cc < args.cols) {
-                                mbar_arrive_expect_tx(load_bar(ew), 4096);
-                                tma_load_2d(sb, &maps.o[2], load_bar(ew), cc, row0);
-                            }
-                        }
-                        if (row0 < args.rows && cc < args.cols) {
-                            ok = wait_for<false>(load_bar(ew), load_phase, wc);
-                            load_phase ^= 1u;
-                        }
-                        if (!ok)
-                            break;
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            ld_shared_v4u(piece(q), hw[4 * q], hw[4 * q + 1], hw[4 * q + 2], hw[4 * q + 3]);
-                        __syncwarp();
-                    }
-                    // kGated: first (and, with the pre-activations wanted, second) h, then gate and up; kGrad: dg in the
-                    // buffer, du kept in hw until dg has been read.
-                    const int outs = T::EPI == kGated && args.keep ? 3 : 1;
-#pragma unroll 1
-                    for (int o = 0; o < outs; ++o) {
-                        if (!(T::EPI == kGrad))
-                            take();
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            float gv[32], uv[32];
-                            if (T::EPI == kGrad || o != 2)
-                                fetch32(gv, c * 64 + g * 32, c, g);
-                            if (T::EPI == kGrad || o != 1)
-                                fetch32(uv, T::BN / 2 + c * 64 + g * 32, c, 2 + g);
-                            if (g == 1 && o == outs - 1)
-                                release();
-                            if constexpr (T::EPI == kGrad) {
-                                with_act(activation, [&](auto k) {
-#pragma unroll
-                                    for (int j = 0; j < 16; ++j) {
-                                        float d0, d1, a0, a1, s0, s1;
-                                        unpack2(hw[g * 16 + j], kind, d0, d1);
-                                        act_grad<decltype(k)::value>(gv[2 * j], a0, s0);
-                                        act_grad<decltype(k)::value>(gv[2 * j + 1], a1, s1);
-                                        hw[g * 16 + j] = pack2(d0 * a0, d1 * a1, kind);
-                                        gv[2 * j] = d0 * uv[2 * j] * s0;
-                                        gv[2 * j + 1] = d1 * uv[2 * j + 1] * s1;
-                                    }
-                                });
-                            } else if (o == 0) {
-                                gate(gv, uv, activation);
-                            } else if (o == 2) {
-#pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    gv[j] = uv[j];
-                            }
-                            if constexpr (T::MX) {
-                                if (kind == 0) {  // (fp32 outputs: of products of 4-bit operands only)
-                                    if (g == 1)
-                                        take();
-#pragma unroll
-                                    for (int q = 0; q < 8; ++q)
-                                        st_shared_v4(piece(q), gv[4 * q], gv[4 * q + 1], gv[4 * q + 2], gv[4 * q + 3]);
-                                    put(0, row0, cc + g * 32);
-                                    continue;
-                                }
-                            }
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                st_shared_v4u(piece(g * 4 + q), pack2(gv[8 * q], gv[8 * q + 1], kind),
-                                              pack2(gv[8 * q + 2], gv[8 * q + 3], kind), pack2(gv[8 * q + 4], gv[8 * q + 5], kind),
-                                              pack2(gv[8 * q + 6], gv[8 * q + 7], kind));
-                        }
-                        if (!T::MX || kind != 0)
-                            put(o, row0, cc);
-                    }
-                    if constexpr (T::EPI == kGrad) {
-                        take();
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            st_shared_v4u(piece(q), hw[4 * q], hw[4 * q + 1], hw[4 * q + 2], hw[4 * q + 3]);
-                        put(1, row0, cc);
-                    }
+                static_assert(T::EPI == kGrad && T::NCHUNK == 2, "a chunk a warp");
+                const int c = half, cc = col0 + c * 64;
+                uint32_t hw[32];  // this row's 64 values of dh, then of du
+                if (row0 < args.rows && cc < args.cols) {
+                    ok = wait_for<false>(load_bar(ew), load_phase, wc);
+                    load_phase ^= 1u;
                 }
+                if (!ok)
+                    break;
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    ld_shared_v4u(piece(q), hw[4 * q], hw[4 * q + 1], hw[4 * q + 2], hw[4 * q + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    float v[32], u[32];
+                    fetch32(v, c * 64 + g * 32, c, g);
+                    fetch32(u, T::BN / 2 + c * 64 + g * 32, c, 2 + g);
+                    if (g == 1)
+                        release();
+                    uint32_t d[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        d[j] = hw[g * 16 + j];
+                    slope(v, u, d, kind, activation);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        hw[g * 16 + j] = pack2(u[2 * j], u[2 * j + 1], kind);
+                    stage16(v, g * 32);
+                }
+                put(0, row0, cc);
+                take();
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    st_shared_v4u(piece(q), hw[4 * q], hw[4 * q + 1], hw[4 * q + 2], hw[4 * q + 3]);
+                put(1, row0, cc);
             }
             if (++acc == T::ACCS) {
                 acc = 0;
@@ -1117,20 +1154,25 @@ __global__ void __launch_bounds__(T::THREADS, T::SWAP && T::BN <= 32 ? 2 : 1)
 }
 
 template <class T>
-cudaError_t launch_tiles(const TileMaps& maps, const ScaleMaps* scales, const TileArgs& args, int grid, int cluster,
-                         cudaStream_t stream)
+const void* tile_function()
 {
-    const void* fn;
     if constexpr (T::MX)
-        fn = reinterpret_cast<const void*>(sat_ffn_scaled_tile_kernel<T>);
+        return reinterpret_cast<const void*>(sat_ffn_scaled_tile_kernel<T>);
     else
-        fn = reinterpret_cast<const void*>(sat_ffn_tile_kernel<T>);
-    // Once for each device.
+        return reinterpret_cast<const void*>(sat_ffn_tile_kernel<T>);
+}
+
+// The kernel's shared memory is allowed on the current device (asked for once for each).
+template <class T>
+cudaError_t allow_memory(int* device)
+{
+    const void* fn = tile_function<T>();
     static std::atomic<uint64_t> ready{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
+    *device = dev;
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
         if (e != cudaSuccess)
@@ -1138,6 +1180,46 @@ cudaError_t launch_tiles(const TileMaps& maps, const ScaleMaps* scales, const Ti
         if (dev < 64)
             ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     }
+    return cudaSuccess;
+}
+
+// The CTAs of a cluster are of one GPC, and the GPCs' sizes differ from chip to chip: 152 SMs held 76, 46, 36, 28, 23, 15 and
+// 15 clusters of 2 to 8 CTAs of an SM each. A cluster too many runs after the others: 20.8 us instead of 14.0 (96 x 4096 x 1024).
+template <class T>
+cudaError_t clusters_at_once(int cluster, int* clusters)
+{
+    static std::atomic<int> known[64][9];
+    int dev = 0;
+    cudaError_t e = allow_memory<T>(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 64 && (*clusters = known[dev][cluster].load(std::memory_order_relaxed)) > 0)
+        return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+    cfg.blockDim = dim3(T::THREADS);
+    cfg.dynamicSmemBytes = T::SMEM_BYTES;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(clusters, tile_function<T>(), &cfg);
+    if (e == cudaSuccess && dev < 64)
+        known[dev][cluster].store(*clusters, std::memory_order_relaxed);
+    return e;
+}
+
+template <class T>
+cudaError_t launch_tiles(const TileMaps& maps, const ScaleMaps* scales, const TileArgs& args, int grid, int cluster,
+                         cudaStream_t stream)
+{
+    int dev = 0;
+    const cudaError_t e = allow_memory<T>(&dev);
+    if (e != cudaSuccess)
+        return e;
     if constexpr (T::MX)
         return launch_early(sat_ffn_scaled_tile_kernel<T>, static_cast<unsigned>(grid), T::THREADS, T::SMEM_BYTES,
                             static_cast<unsigned>(cluster), stream, maps, *scales, args);
@@ -1150,7 +1232,7 @@ template <class T>
 constexpr Variant variant()
 {
     return Variant{T::MX, T::EPI, T::CG, T::BN, T::P_MN, T::Q_MN, T::SWAP, !T::SPLIT,
-                   T::STAGES * T::STAGE_BYTES, T::NCHUNK, T::PART_BYTES, &launch_tiles<T>};
+                   T::STAGES * T::STAGE_BYTES, T::NCHUNK, T::PART_BYTES, &launch_tiles<T>, &clusters_at_once<T>};
 }
 
 }  // namespace ffn

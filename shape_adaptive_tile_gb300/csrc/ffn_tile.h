@@ -56,6 +56,8 @@ struct Variant {
     int ring_bytes, chunks, part_bytes;
     cudaError_t (*launch)(const TileMaps& maps, const ScaleMaps* scales, const TileArgs& args, int grid, int cluster,
                           cudaStream_t stream);
+    // How many clusters of this many CTAs (up to 8) the current device holds at once.
+    cudaError_t (*fit)(int cluster, int* clusters);
 };
 
 // A launch that may begin its set-up (up to wait_for_earlier) while the kernel

@@ -148,6 +148,28 @@ def test_strides_and_alignment(i):
     c.check_backward(bool(rng.integers(2)))
 
 
+@pytest.mark.parametrize("out_pad,out_offset", [(0, 0), (8, 8), (3, 1)])
+@pytest.mark.parametrize("by_output", [True, False])
+@pytest.mark.parametrize("rows,width,hidden", [(66, 1030, 33), (70, 2056, 200), (129, 4096, 104), (96, 16400, 72), (200, 9000, 1)])
+def test_long_sums_of_few_outputs(rows, width, hidden, by_output, out_pad, out_offset):
+    """Tiles that several CTAs share: whole and ragged chunks of columns, rows on and off 16 bytes."""
+    c = Case(rows + hidden, rows, width, hidden, "bf16", "silu", by_output, out_pad=out_pad, out_offset=out_offset)
+    c.check_forward(keep=True)
+    c.check_forward()
+    c.check_backward(True)
+    c.check_backward(False)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("by_output", [True, False])
+@pytest.mark.parametrize("rows,width,hidden,out_pad", [(4100, 130, 50, 0), (9000, 72, 36, 1), (2050, 200, 130, 4)])
+def test_weight_gradients_of_many_rows(rows, width, hidden, out_pad, by_output, accumulate):
+    c = Case(rows + hidden, rows, width, hidden, "fp16", "gelu_tanh", by_output, out_pad=out_pad)
+    c.check_backward(True, "fp32", accumulate)
+    if not accumulate:
+        c.check_backward(False, "fp16")
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 def test_many_tiles(kind):
     # More tiles than SMs: several rounds of the persistent kernels, in both directions along k.

@@ -181,6 +181,15 @@ def test_gated_product_sizes(rows, cols, width, activation):
     Product(rows + cols, rows, cols, width, "bf16" if rows % 2 else "fp32", activation, 0.125).check()
 
 
+@pytest.mark.parametrize("pad", [0, 8, 3])
+@pytest.mark.parametrize("activation", [None, "silu"])
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,cols,width", [(66, 40, 4100), (129, 104, 16000), (70, 300, 2080), (300, 130, 30000), (4, 300, 16000)])
+def test_long_sums_of_few_outputs(rows, cols, width, out, activation, pad):
+    """Tiles that several CTAs share."""
+    Product(rows + cols, rows, cols, width, out, activation, 0.125, pad).check()
+
+
 @pytest.mark.parametrize("activation", [None, "silu"])
 def test_product_of_many_tiles(activation):
     Product(1, 2700, 4104, 1312, "bf16", activation).check()
