@@ -368,3 +368,28 @@ z = x.double() @ w.double().t()
 assert float((h.double() - z[:, :512] * z[:, 512:]).abs().max()) < 0.1
 """
     subprocess.run([sys.executable, "-c", code], cwd=root, check=True, timeout=300)
+
+
+def test_the_first_call_of_a_process_may_be_a_captured_one_of_shared_tiles():
+    """How many clusters the device holds is asked for by the first call, here while a graph is captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(sat.__file__)))
+    code = """
+import torch, shape_adaptive_tile_gb300 as sat
+x, w = torch.randn(96, 4096, device="cuda").bfloat16(), torch.randn(512, 4096, device="cuda").bfloat16() / 64
+h, one = (torch.zeros(n, 256, device="cuda", dtype=torch.bfloat16) for n in (96, 1))
+f = dict(width=4096, hidden=256, type="bf16", activation="none", w_by_output=1, x=x, ldx=4096, w=w, ldw=4096, ldh=256)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    for n, out in ((96, h), (1, one)):
+        sat.check(sat.ffn_gated(sat.FfnArgs(rows=n, h=out, **f), torch.cuda.current_stream().cuda_stream))
+g.replay()
+torch.cuda.synchronize()
+z = x.double() @ w.double().t()
+want = z[:, :256] * z[:, 256:]
+assert float((h.double() - want).abs().max()) < 0.1 and float((one.double() - want[:1]).abs().max()) < 0.1
+"""
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True, timeout=300)
