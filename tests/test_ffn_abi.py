@@ -172,3 +172,17 @@ def test_no_device_is_an_error_and_not_a_crash():
         pytest.skip("a GPU is present")
     assert sat.ffn_gated(_ffn()) in (-2, -4) and sat.ffn_gated_backward(_ffn(), _grads()) in (-2, -4)
     assert sat.mxfp4_gemm(_gemm()) in (-2, -4) and sat.mxfp4_quantize(_quant()) == -4
+
+
+@pytest.mark.parametrize("big", [("rows", "width"), ("rows", "hidden"), ("width", "hidden")])
+def test_bytes_that_64_bits_cannot_count_are_refused(big):
+    most = (1 << 30) - 9  # (2 hidden columns in one row)
+    sizes = {**dict(rows=3, width=5, hidden=7), **{n: most for n in big}}
+    f = dict(ldx=2 * most + 1, ldw=2 * most + 1, ldh=2 * most + 1, x=AT + 2, w=AT + 2, w_by_output=0)
+    for preact in (None, AT):
+        a = _ffn(**{**f, **sizes, "preact": preact, "ldp": 2 * most + 1})
+        g = _grads(lddh=2 * most + 1, lddx=2 * most + 1, lddw=2 * most + 1)
+        for call in (lambda: sat.ffn_gated_workspace(a), lambda: sat.ffn_gated_backward_workspace(a, g)):
+            with pytest.raises(sat.GemmError, match="2\\^56"):
+                call()
+        assert sat.ffn_gated(a) == sat.ffn_gated_backward(a, g) == -1
