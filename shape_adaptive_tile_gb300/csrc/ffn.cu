@@ -183,14 +183,18 @@ Choice tiles_of(const Product& p, const Variant* v, int sms)
         // (8192 x 8192 gated by one token: 16.4 us as 256 CTAs, 23.1 as 128; 16-bit weights lose 1 to 3%). At least four
         // k-blocks a CTA, and the sums have to fit in the ring.
         const int64_t ctas = p.mx && v->bn <= 32 ? 2 * sms : sms;
+        // Two CTAs an SM for up to 32 tokens, where the runtime counts one all the same: twice what it says of the tiles of 64
+        // tokens, which fill an SM (8192 x 8192 by one token: 9.6 us in clusters of four, 10.2 in clusters of two).
+        const int per_sm = v->bn <= 32 ? 2 : 1;
+        const Variant* full = per_sm == 1 ? v : find_variant(v->mx, v->epi, 1, 64, v->p_mn, v->q_mn, 1);
         int64_t s = 1;
         for (int64_t n = 2; n <= 8 && tiles * n <= ctas && num_kb / n >= 4; ++n) {
             if ((n - 1) * ceil_div(v->chunks, n) * v->part_bytes > v->ring_bytes)
                 continue;
             int fit = 0;
-            if ((c.error = v->fit(static_cast<int>(n), &fit)) != cudaSuccess)
+            if ((c.error = full->fit(static_cast<int>(n), &fit)) != cudaSuccess)
                 return c;
-            if (tiles <= fit)
+            if (tiles <= per_sm * fit)
                 s = n;
         }
         c.cluster = static_cast<int>(s);
