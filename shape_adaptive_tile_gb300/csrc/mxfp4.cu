@@ -1,5 +1,9 @@
 // Microscaled 4-bit matrices: quantisation and its inverse (include/ffn.h).
 #include "ffn.h"
+
+#include <climits>
+#include <type_traits>
+
 #include "ffn_ptx.cuh"
 #include "ffn_tile.h"
 #include "rows.cuh"
@@ -48,48 +52,74 @@ __device__ __forceinline__ unsigned long long scales_of(const Args& a, unsigned 
     return (static_cast<unsigned long long>(set >> 5) * a.groups + (unit >> 4)) * 32 + (set & 31);
 }
 
-// Eight elements of row[j ..]; past the width 0. Rows that start off 16 bytes:
-// by the 16-byte pieces around them where these lie in the row, shifted into
-// place (the shift is the same in all of a row's threads).
-template <typename T, bool kVec>
-__device__ __forceinline__ Pack<T> load8(const T* row, long long j, long long width)
+// Eight elements of row[j ..], one by one; past the width 0.
+template <typename T>
+__device__ __forceinline__ Pack<T> load_singly(const T* row, long long j, long long width)
 {
-    if (kVec && j + 8 <= width)
-        return load_pack(row + j);
     Pack<T> v{};
-    if constexpr (!kVec) {
-        constexpr int P = 16 / sizeof(T), N = sizeof(T) == 4 ? 3 : 2;
-        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row + j)) & 15u;
-        const int back = static_cast<int>(off / sizeof(T));
-        if (j >= back && j - back + N * P <= width) {
-            const uint4* from = reinterpret_cast<const uint4*>(row + j - back);
-            uint32_t w[4 * N + 3] = {};
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint4 q = __ldg(from + i);
-                w[4 * i] = q.x;
-                w[4 * i + 1] = q.y;
-                w[4 * i + 2] = q.z;
-                w[4 * i + 3] = q.w;
-            }
-#pragma unroll
-            for (int i = 0; i < 4 * N; ++i)
-                w[i] = off & 8 ? w[i + 2] : w[i];
-#pragma unroll
-            for (int i = 0; i < 4 * N; ++i)
-                w[i] = off & 4 ? w[i + 1] : w[i];
-#pragma unroll
-            for (int i = 0; i < static_cast<int>(2 * sizeof(T)); ++i)
-                v.w[i] = sizeof(T) == 2 && (off & 2) ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
-            return v;
-        }
-    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (j + i < width)
             reinterpret_cast<T*>(v.w)[i] = row[j + i];
     return v;
 }
+
+// The 16-byte pieces around eight elements of a row that may start off 16 bytes.
+// All rows' pieces are on their way before the first is shifted: with each row's
+// loads behind a test of its own, 8192 x 8191 bf16 took 58 us instead of 47, and
+// 55049 x 427 fp16, with the elements at the rows' ends one by one, 28 instead of
+// 21. (fp32 in pairs of rows: 8000 x 4097 43 us; 41 one after the other.)
+template <typename T>
+struct Around {
+    static constexpr int P = 16 / sizeof(T), N = sizeof(T) == 4 ? 3 : 2;
+    uint4 q[N];
+
+    // Those that hold an element of the row, whole: what else is in them has to be the matrix's or between its rows.
+    __device__ __forceinline__ void load(const T* row, long long j, long long width)
+    {
+        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row + j)) & 15u;
+        const int back = static_cast<int>(off / sizeof(T));
+        const uint4* from = reinterpret_cast<const uint4*>(row + j - back);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            q[i] = j - back + i * P < width && (i < N - 1 || off) ? __ldg(from + i) : make_uint4(0, 0, 0, 0);
+    }
+
+    // The eight elements, shifted into place; past the width 0.
+    __device__ __forceinline__ Pack<T> elements(const T* row, long long j, long long width) const
+    {
+        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row + j)) & 15u;
+        uint32_t w[4 * N + 3] = {};
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            w[4 * i] = q[i].x;
+            w[4 * i + 1] = q[i].y;
+            w[4 * i + 2] = q[i].z;
+            w[4 * i + 3] = q[i].w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4 * N; ++i)
+            w[i] = off & 8 ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < 4 * N; ++i)
+            w[i] = off & 4 ? w[i + 1] : w[i];
+        Pack<T> v;
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(2 * sizeof(T)); ++i)
+            v.w[i] = sizeof(T) == 2 && (off & 2) ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+        if (j + 8 > width) {
+            const int left = static_cast<int>(width - j);
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(2 * sizeof(T)); ++i) {
+                if constexpr (sizeof(T) == 4)
+                    v.w[i] = i < left ? v.w[i] : 0u;
+                else
+                    v.w[i] = 2 * i + 1 < left ? v.w[i] : 2 * i < left ? v.w[i] & 0xFFFFu : 0u;
+            }
+        }
+        return v;
+    }
+};
 
 // The exponent field, as an fp32 number's, of the largest magnitude: 255 with an infinity or a NaN among the values.
 __device__ __forceinline__ uint32_t largest_field(const Pack<float>& p)
@@ -134,7 +164,7 @@ __device__ __forceinline__ uint32_t codes_of(const float (&v)[8])
 // its place is worked out once. 8192 x 8192 bf16 30.8 us, 81% of the copy rate,
 // with some 3 of 4 instructions a cycle; fp32 45 us, 98%.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads, 4) sat_mxfp4_quantize_kernel(const __grid_constant__ Args a)
+__global__ void __launch_bounds__(kThreads, !kVec && sizeof(T) == 4 ? 3 : 4) sat_mxfp4_quantize_kernel(const __grid_constant__ Args a)
 {
     launch_dependents();
     wait_for_earlier();
@@ -148,13 +178,35 @@ __global__ void __launch_bounds__(kThreads, 4) sat_mxfp4_quantize_kernel(const _
         const bool in = p.in && set < a.sets;
         const unsigned row = row_of(set);
         const T* from = static_cast<const T*>(a.values) + static_cast<unsigned long long>(row) * a.ldv;
+        auto row_at = [&](int u) { return from + static_cast<unsigned long long>(32 * u) * a.ldv; };
         Pack<T> v[4];
+        if constexpr (kVec) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (in && row + 32 * u < a.rows)
-                v[u] = load8<T, kVec>(from + static_cast<unsigned long long>(32 * u) * a.ldv, j, a.width);
-            else
-                v[u] = Pack<T>{};
+            for (int u = 0; u < 4; ++u)
+                if (in && row + 32 * u < a.rows)
+                    v[u] = j + 8 <= a.width ? load_pack(row_at(u) + j) : load_singly(row_at(u), j, a.width);
+                else
+                    v[u] = Pack<T>{};
+        } else {
+            // Pieces of the first and the last row may reach out of the matrix, and so may those of rows closer than 16 bytes.
+            auto inside = [&](int u) {
+                return row + 32 * u > 0 && row + 32 * u + 1 < a.rows && a.ldv >= static_cast<unsigned>(Around<T>::P);
+            };
+            constexpr int AT_ONCE = sizeof(T) == 4 ? 2 : 4;  // (registers)
+#pragma unroll
+            for (int u0 = 0; u0 < 4; u0 += AT_ONCE) {
+                Around<T> pieces[AT_ONCE];
+#pragma unroll
+                for (int u = 0; u < AT_ONCE; ++u)
+                    pieces[u].load(row_at(u0 + u), j, in && inside(u0 + u) ? static_cast<long long>(a.width) : LLONG_MIN);
+#pragma unroll
+                for (int u = 0; u < AT_ONCE; ++u)
+                    if (inside(u0 + u) || !in || row + 32 * (u0 + u) >= a.rows)
+                        v[u0 + u] = pieces[u].elements(row_at(u0 + u), j, a.width);
+                    else
+                        v[u0 + u] = load_singly(row_at(u0 + u), j, a.width);
+            }
+        }
         uint32_t fields = 0;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -186,120 +238,124 @@ __global__ void __launch_bounds__(kThreads, 4) sat_mxfp4_quantize_kernel(const _
     }
 }
 
-// Eight elements a thread to row[j ..], of rows that start off 16 bytes (all of a
-// warp's threads; `in`: this one has elements). A thread writes the 16-byte
-// pieces that begin among its elements, the last of them with the next lane's;
-// elements at the row's or the warp's ends, in no such piece, go one by one.
-// (All one by one, 8192 x 8191 bf16 took 174 us instead of 36.)
-template <typename T>
-__device__ __forceinline__ void store_shifted(T* row, long long j, long long width, const Pack<T>& v, bool in, bool same_as_next,
-                                              bool same_as_last)
+// The fp16 numbers of eight codes, the first in the lowest four bits.
+__device__ __forceinline__ void numbers_of(uint32_t codes, uint32_t (&two)[4])
 {
-    constexpr int P = 16 / sizeof(T), W = 2 * sizeof(T), PIECES = W / 4;
-    uint32_t w[W + 4 + 3] = {};
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(two[0]), "=r"(two[1]), "=r"(two[2]), "=r"(two[3])
+        : "r"(codes));
+}
+
+// 2^(byte - 127), of byte 0 below the normal numbers; NaN of 255.
+__device__ __forceinline__ float power_of(uint32_t byte)
+{
+    return __uint_as_float(byte == 255 ? 0x7FFFFFFFu : byte ? byte << 23 : 0x00400000u);
+}
+
+// Eight elements from their codes, the first `n` by one scale, the others by the next block's.
+template <typename T>
+__device__ __forceinline__ Pack<T> elements_of(uint32_t codes, float by, float by_next, int n)
+{
+    uint32_t two[4];
+    numbers_of(codes, two);
+    Pack<T> out;
 #pragma unroll
-    for (int i = 0; i < W; ++i)
-        w[i] = v.w[i];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[W + i] = __shfl_down_sync(0xffffffffu, v.w[i], 1);
-    if (!in)
-        return;
-    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row + j)) & 15u, skip = (16u - off) & 15u;
-    const int first = static_cast<int>(skip / sizeof(T));  // element that the first piece begins with
-#pragma unroll
-    for (int i = 0; i < W + 4; ++i)
-        w[i] = skip & 8 ? w[i + 2] : w[i];
-#pragma unroll
-    for (int i = 0; i < W + 4; ++i)
-        w[i] = skip & 4 ? w[i + 1] : w[i];
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-        w[i] = sizeof(T) == 2 && (skip & 2) ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
-    int done = first;  // elements from `first` on that pieces take
-#pragma unroll
-    for (int k = 0; k < PIECES; ++k) {
-        const bool mine = first + (k + 1) * P <= 8;
-        if (j + first + (k + 1) * P <= width && (mine || same_as_next)) {
-            *reinterpret_cast<uint4*>(row + j + first + k * P) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-            done = first + (k + 1) * P;
+    for (int k = 0; k < 4; ++k) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two[k]));
+        const float x = f.x * (2 * k < n ? by : by_next), y = f.y * (2 * k + 1 < n ? by : by_next);
+        if constexpr (sizeof(T) == 4) {
+            reinterpret_cast<float*>(out.w)[2 * k] = x;
+            reinterpret_cast<float*>(out.w)[2 * k + 1] = y;
+        } else if constexpr (std::is_same_v<T, __half>) {
+            reinterpret_cast<__half2*>(out.w)[k] = __floats2half2_rn(x, y);
+        } else {
+            reinterpret_cast<__nv_bfloat162*>(out.w)[k] = __floats2bfloat162_rn(x, y);
         }
     }
-    const bool head = first > 0 && !(same_as_last && j + first <= width);  // no piece of the last lane's reaches in here
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if ((i < first ? head : i >= done) && j + i < width)
-            row[j + i] = reinterpret_cast<const T*>(v.w)[i];
+    return out;
 }
 
-// Two values of the type from two codes' fp16 numbers and the block's scale.
-template <typename T>
-__device__ __forceinline__ void scaled(uint32_t two, float by, T* out)
-{
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
-    if constexpr (sizeof(T) == 4) {
-        out[0] = f.x * by;
-        out[1] = f.y * by;
-    } else if constexpr (std::is_same_v<T, __half>) {
-        *reinterpret_cast<__half2*>(out) = __floats2half2_rn(f.x * by, f.y * by);
-    } else {
-        *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(f.x * by, f.y * by);
-    }
-}
-
+// Rows that start off 16 bytes: a thread takes the eight elements that begin at
+// the first whole 16 bytes among its own, so that it stores whole ones: their
+// codes are its own and the next thread's word, shifted (codes are a quarter of
+// the elements' bits, and nothing is exchanged), and the last of a block's four
+// threads has the next block's scale for the rest. What is before the row's first
+// whole 16 bytes, its first thread stores too. 8192 x 8191 bf16 39 us; 61 with
+// finished elements exchanged between lanes and shifted, 174 one by one.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads, 4) sat_mxfp4_dequantize_kernel(const __grid_constant__ Args a)
 {
     launch_dependents();
     wait_for_earlier();
     const Place p = place(a);
-    const bool coded = p.in && (p.unit >> 2) < a.blocks;
+    const bool coded = p.in && (p.unit >> 2) < a.blocks, more = ((p.unit + 1) >> 2) < a.blocks;
     const long long j = p.unit * 8ll;
     const unsigned sub = threadIdx.x / a.per_row;
-    // Whether the neighbouring lanes have the row's next and last eight columns.
-    const int lane = threadIdx.x & 31;
-    const unsigned in_row = threadIdx.x - sub * a.per_row;
-    const bool same_as_next = lane < 31 && in_row + 1 < a.per_row, same_as_last = lane > 0 && in_row > 0;
 #pragma unroll 1
     for (unsigned set = p.first; set - sub < a.sets; set += a.stride) {
         const bool in = coded && set < a.sets;
         const unsigned row = row_of(set);
         const uint4 s4 = in ? a.scales[scales_of(a, set, p.unit)] : make_uint4(0, 0, 0, 0);
         const uint32_t words[4] = {s4.x, s4.y, s4.z, s4.w};
+        uint4 n4 = make_uint4(0, 0, 0, 0);  // of the next four blocks, where the next thread's block is one of them
+        if (!kVec && in && more && (p.unit & 15) == 15)
+            n4 = a.scales[scales_of(a, set, p.unit + 1)];
+        const uint32_t next_words[4] = {n4.x, n4.y, n4.z, n4.w};
         const uint8_t* from = a.codes + static_cast<unsigned long long>(row) * a.ldc + p.unit * 4;
-        uint32_t codes[4];
+        uint32_t codes[4], next[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            codes[u] = in && row + 32 * u < a.rows
-                           ? *reinterpret_cast<const uint32_t*>(from + static_cast<unsigned long long>(32 * u) * a.ldc)
-                           : 0u;
+        for (int u = 0; u < 4; ++u) {
+            const bool here = in && row + 32 * u < a.rows;
+            const uint32_t* at = reinterpret_cast<const uint32_t*>(from + static_cast<unsigned long long>(32 * u) * a.ldc);
+            codes[u] = here ? at[0] : 0u;
+            next[u] = !kVec && here && more ? at[1] : 0u;
+        }
         T* to = static_cast<T*>(a.values) + static_cast<unsigned long long>(row) * a.ldv;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const bool here = in && row + 32 * u < a.rows;
-            const uint32_t byte = words[u] >> (8 * (p.unit / 4 % 4)) & 255u;
-            // 2^(byte - 127): of byte 0 it is below the normal numbers.
-            const float by = __uint_as_float(byte == 255 ? 0x7FFFFFFFu : byte ? byte << 23 : 0x00400000u);
+            if (!kVec && !here)
+                break;
+            const float by = power_of(words[u] >> (8 * (p.unit / 4 % 4)) & 255u);
             T* at = to + static_cast<unsigned long long>(32 * u) * a.ldv;
-            uint32_t two[4];
-            asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-                "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-                "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-                : "=r"(two[0]), "=r"(two[1]), "=r"(two[2]), "=r"(two[3])
-                : "r"(codes[u]));
-            Pack<T> out;
+            if constexpr (kVec) {
+                const Pack<T> out = elements_of<T>(codes[u], by, by, 8);
+                if (here && j + 8 <= a.width) {
+                    store_pack(at + j, out);
+                } else if (here) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                scaled(two[k], by, reinterpret_cast<T*>(out.w) + 2 * k);
-            if constexpr (!kVec) {
-                store_shifted(at, j, a.width, out, here, same_as_next, same_as_last);
-            } else if (here && j + 8 <= a.width) {
-                store_pack(at + j, out);
-            } else if (here) {
+                    for (int k = 0; k < 8; ++k)
+                        if (j + k < a.width)
+                            at[j + k] = reinterpret_cast<const T*>(out.w)[k];
+                }
+            } else {
+                constexpr int P = 16 / sizeof(T);
+                const int skip = -static_cast<int>(reinterpret_cast<uintptr_t>(at) / sizeof(T)) & (P - 1);
+                const uint32_t next_byte =
+                    ((p.unit & 15) == 15 ? next_words[u] : words[u] >> (8 * ((p.unit + 1) / 4 % 4))) & 255u;
+                const Pack<T> out = elements_of<T>(__funnelshift_r(codes[u], next[u], 4 * skip), by, power_of(next_byte),
+                                                   (p.unit & 3) == 3 ? 8 - skip : 8);
+                const long long first = j + skip;
+                if (first + 8 <= a.width) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (j + k < a.width)
-                        at[j + k] = reinterpret_cast<const T*>(out.w)[k];
+                    for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k)
+                        *reinterpret_cast<uint4*>(at + first + k * P) =
+                            make_uint4(out.w[4 * k], out.w[4 * k + 1], out.w[4 * k + 2], out.w[4 * k + 3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (first + k < a.width)
+                            at[first + k] = reinterpret_cast<const T*>(out.w)[k];
+                }
+                if (p.unit == 0 && skip > 0) {
+                    const Pack<T> head = elements_of<T>(codes[u], by, by, 8);
+#pragma unroll
+                    for (int k = 0; k < P - 1; ++k)
+                        if (k < skip && k < a.width)
+                            at[k] = reinterpret_cast<const T*>(head.w)[k];
+                }
             }
         }
     }

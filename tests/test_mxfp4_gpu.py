@@ -77,6 +77,17 @@ def test_quantize_strides(i):
     check_quantized(ref.rows(g, n, width, kind, pad, offset), kind, int(rng.choice([0, 16, 48])), pad, offset)
 
 
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+def test_rows_off_16_bytes_among_not_a_number(kind):
+    """Whole 16-byte pieces are read and written around rows that start anywhere: neighbours are neither taken nor overwritten."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    for rows, width, gap, offset in [(r, w, e, o) for r in (1, 2, 3, 131) for w in (1, 2, 5, 7, 9, 33, 129, 200)
+                                     for e, o in ((0, 0), (0, 3), (1, 1), (2, 6), (3, 5), (8, 7), (5, 4))]:
+        x = ref.rows(g, rows, width, kind, gap, offset)
+        check_quantized(x, kind, pad=gap, offset=offset)
+
+
 def test_every_bf16_value_in_a_block_with_each_power():
     # All finite bf16 values, each against block maxima that put it anywhere on the grid; ties included.
     v = torch.arange(1 << 16, device="cuda", dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
