@@ -18,8 +18,8 @@
  * that a ..._workspace function gives; concurrent calls need scratch of their
  * own. Waits inside the kernels are bounded: where a copy or a product has not
  * come after two seconds, which no launch takes, the outputs that hang on it
- * are NaN. Sizes are below 2^31, matrices of fewer than 2^56 elements, and no
- * output may overlap an input or another output.
+ * are NaN. Sizes (and twice `hidden`) are below 2^31, matrices of fewer than 2^56
+ * elements, and no output may overlap an input or another output.
  */
 #ifndef SAT_FFN_H
 #define SAT_FFN_H

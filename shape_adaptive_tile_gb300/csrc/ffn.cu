@@ -359,8 +359,8 @@ int check(const ffn_gated_args* a)
 {
     if (!a)
         return fail_with(GEMM_ERR_ARG, "args is NULL");
-    if (a->rows < 0 || a->width < 0 || a->hidden < 0 || a->rows >= kMost || a->width >= kMost || 2 * a->hidden >= kMost)
-        return fail_with(GEMM_ERR_ARG, "sizes must be in [0, 2^31)");
+    if (a->rows < 0 || a->width < 0 || a->hidden < 0 || a->rows >= kMost || a->width >= kMost || a->hidden >= kMost / 2)
+        return fail_with(GEMM_ERR_ARG, "sizes must be in [0, 2^31), and so must 2 hidden");
     // (Bytes and offsets are counted in 64 bits.)
     if (std::max({a->rows * a->width, a->rows * a->hidden, a->width * a->hidden}) >= INT64_C(1) << 56)
         return fail_with(GEMM_ERR_ARG, "a matrix of 2^56 elements or more");
