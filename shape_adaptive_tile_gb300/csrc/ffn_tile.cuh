@@ -74,6 +74,8 @@ struct TileTraits {
     static constexpr int NCHUNK = OUT_COLS / CHUNK;
     static constexpr int CHUNK_ACC = GATED ? 2 * CHUNK : CHUNK;    // accumulator columns of a chunk
     static constexpr int PART_BYTES = CHUNK_ACC * 128 * 4;         // a chunk's partial sums of one CTA
+    // The output columns of a tile that each half of the epilogue warps has: whole chunks in turn, or, drained, one half of them.
+    static constexpr int RUN = DRAIN ? OUT_COLS / 2 : CHUNK, RUNS = OUT_COLS / RUN;
 
     static_assert(!MX || (!P_MN && !Q_MN), "4-bit operands are K-major");
     static_assert(!SWAP || (SPLIT && CG == 1 && !Q_MN), "few tokens: split, K-major tokens");
@@ -241,7 +243,9 @@ __device__ __forceinline__ void unpack2(uint32_t v, int kind, float& lo, float& 
 #define SAT_FFN_WAIT_NS 2000000000ull
 #endif
 constexpr unsigned long long kWaitNs = SAT_FFN_WAIT_NS;
-constexpr int kWaitTries = kWaitNs > 0 ? 64 : 0, kWaitRound = kWaitNs > 0 ? 32 : 1;
+// (try_wait may suspend a thread for longer than a limit below this, which only tests have.)
+constexpr bool kSuspend = kWaitNs >= 1000000;
+constexpr int kWaitTries = kSuspend ? 64 : 0, kWaitRound = kSuspend ? 32 : 1;
 
 struct Waiter {
     uint32_t abort;       // shared address of the flag
@@ -258,7 +262,7 @@ static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, con
     for (;;) {
         bool there = false;
         for (int i = 0; i < kWaitRound && !there; ++i)
-            there = kWaitNs > 0 ? mbar_try_wait<kCluster>(bar, parity) : mbar_test_wait<kCluster>(bar, parity);
+            there = kSuspend ? mbar_try_wait<kCluster>(bar, parity) : mbar_test_wait<kCluster>(bar, parity);
         if (__all_sync(0xffffffffu, there))
             return true;
         if (__any_sync(0xffffffffu, w.aborted()))
@@ -898,7 +902,8 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                     for (int j = 0; j < 32; ++j)
                         v[g][j] = alpha * v[g][j];
                 constexpr int GROUPS = T::GATED ? 2 : 4;
-                const int first = col0 + half * GROUPS * 32;
+                static_assert(GROUPS * 32 == T::RUN, "the columns that are NaN where a wait gives up");
+                const int first = col0 + half * T::RUN;
                 if constexpr (T::GATED) {
                     if (!T::MX && args.keep) {
                         take();
@@ -1118,14 +1123,14 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
             const int row0 = w.tp * (128 * T::CG) + (T::CG == 2 ? static_cast<int>(rank) * 128 : 0) + sub * 32;
             const int outs = T::EPI == kGrad ? 2 : T::EPI == kGated && args.keep ? 3 : 1;
             for (int o = 0; o < outs; ++o)
-                for (int c = half; c < T::NCHUNK; c += 2) {
+                for (int c = half; c < T::RUNS; c += 2) {
                     if (!own(c))
                         continue;
-                    const int col = w.tq * T::OUT_COLS + c * T::CHUNK;
+                    const int col = w.tq * T::OUT_COLS + c * T::RUN;
                     if (T::SWAP)
-                        store_nan(args, o, col, T::CHUNK, row0, 32);
+                        store_nan(args, o, col, T::RUN, row0, 32);
                     else
-                        store_nan(args, T::EPI == kStore ? w.z : o, row0, 32, col, T::CHUNK);
+                        store_nan(args, T::EPI == kStore ? w.z : o, row0, 32, col, T::RUN);
                 }
         }
         if (!T::SWAP && lane == 0) {
