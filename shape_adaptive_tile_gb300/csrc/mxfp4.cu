@@ -66,15 +66,16 @@ __device__ __forceinline__ Pack<T> load_singly(const T* row, long long j, long l
 
 // The 16-byte pieces around eight elements of a row that may start off 16 bytes.
 // All rows' pieces are on their way before the first is shifted: with each row's
-// loads behind a test of its own, 8192 x 8191 bf16 took 58 us instead of 47, and
+// loads behind a test of its own, 8192 x 8191 bf16 took 58 us instead of 48, and
 // 55049 x 427 fp16, with the elements at the rows' ends one by one, 28 instead of
-// 21. (fp32 in pairs of rows: 8000 x 4097 43 us; 41 one after the other.)
+// 22. (fp32 in pairs of rows: 8000 x 4097 44 us; 41 one after the other.)
 template <typename T>
 struct Around {
     static constexpr int P = 16 / sizeof(T), N = sizeof(T) == 4 ? 3 : 2;
     uint4 q[N];
 
-    // Those that hold an element of the row, whole: what else is in them has to be the matrix's or between its rows.
+    // Those that hold an element of the row, whole: what else is in them has to be the matrix's or between its rows. (By
+    // coherent loads: the kernel before this one may still write the matrix when this one starts.)
     __device__ __forceinline__ void load(const T* row, long long j, long long width)
     {
         const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row + j)) & 15u;
@@ -82,7 +83,7 @@ struct Around {
         const uint4* from = reinterpret_cast<const uint4*>(row + j - back);
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            q[i] = j - back + i * P < width && (i < N - 1 || off) ? __ldg(from + i) : make_uint4(0, 0, 0, 0);
+            q[i] = j - back + i * P < width && (i < N - 1 || off) ? from[i] : make_uint4(0, 0, 0, 0);
     }
 
     // The eight elements, shifted into place; past the width 0.
