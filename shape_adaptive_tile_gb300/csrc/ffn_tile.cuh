@@ -159,7 +159,8 @@ __device__ __forceinline__ void act_grad(float g, float& a, float& d)
     } else if constexpr (KIND == 3) {  // (1 + tanh y) / 2 = 1 / (1 + exp(-2 y))
         const float s = sigmoid(1.5957691216057308f * fmaf(0.044715f * g * g, g, g));
         a = g * s;
-        d = fmaf(a * (1.0f - s), 1.5957691216057308f * fmaf(0.134145f * g, g, 1.0f), s);
+        // (g^2 is held to what no s (1 - s) but 0 meets, or it would overflow to 0 times infinity.)
+        d = fmaf(a * (1.0f - s), 1.5957691216057308f * fmaf(0.134145f, fminf(g * g, 1e6f), 1.0f), s);
     } else if constexpr (KIND == 4) {
         a = g > 0.0f ? g : (g != g ? g : 0.0f);
         d = g > 0.0f ? 1.0f : (g != g ? g : 0.0f);
