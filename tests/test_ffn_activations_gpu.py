@@ -5,7 +5,11 @@ Roundings are counted in 2^-24 of a value (fp32's half step):
 - GELU: the fit of the tail 0.4, t 3 (its reciprocal 2, its sum one), which the Mills ratio passes on at most once, eight
   steps of the polynomial 3 (each counts by its share of the sum; evaluated in fp32 against 64 bits), the density 12 (two
   powers of two 4 each, the constant and three products), three more products and that with u: 23.
-So 2^-19 (32 of them). Below fp32's normal numbers a rounding is up to 2^-149.
+- SiLU, g e / (1 + e) with e = exp(-|g|): exp 10 (two powers of two 4 each, two products), 1 + e one, its reciprocal 2, three
+  products: 16.
+- GELU by tanh: as SiLU, and 6 of the argument of exp (constants, squares, products), which exp takes to 6 times the
+  argument's size.
+So 2^-19 (32 of them) and, by tanh, 2^-21 times the argument. Below fp32's normal numbers a rounding is up to 2^-149.
 """
 import math
 
@@ -18,7 +22,7 @@ from tests.gpu_util import stream
 
 pytestmark = pytest.mark.gpu
 
-KINDS = ["none", "gelu", "relu"]
+KINDS = ["none", "silu", "gelu", "gelu_tanh", "relu"]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -28,11 +32,16 @@ def _device():
     sat.lib()
 
 
+def argument(g):
+    """What exp gets in GELU by tanh."""
+    return 2 * math.sqrt(2 / math.pi) * (g + 0.044715 * g**3).abs()
+
+
 def tolerance(g, kind):
     """Relative, of the activation."""
     if kind in ("none", "relu"):
         return torch.full_like(g, 2.0**-24)
-    return torch.full_like(g, 2.0**-19)
+    return 2.0**-19 + (2.0**-21 * argument(g).clamp(max=200.0) if kind == "gelu_tanh" else 0.0)
 
 
 def tiny(g):
@@ -115,9 +124,17 @@ def test_every_gate(kind, activation):
 def slope_terms(g, kind):
     """The derivative and the magnitude of what it is the sum of."""
     d = ref.act(g, kind)[1]
+    if kind == "silu":
+        s = torch.sigmoid(g)
+        return d, s + (g * s * torch.sigmoid(-g)).abs()
     if kind == "gelu":
         c = 0.5 * torch.special.erfc(-g / math.sqrt(2))
         return d, c + (g * torch.exp(-g * g / 2)).abs() / math.sqrt(2 * math.pi)
+    if kind == "gelu_tanh":
+        y = math.sqrt(2 / math.pi) * (g + 0.044715 * g**3)
+        s, r = torch.sigmoid(2 * y), torch.sigmoid(-2 * y)
+        return s + g * s * r * 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * g * g), s + (
+            g * s * r * 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * g * g)).abs()
     return d, d.abs()
 
 
