@@ -442,9 +442,9 @@ static __device__ __noinline__ void store_rows(uint32_t sb, void* at, long long 
 // NaN in `rows` rows and `cols` columns of out[i] from (row0, col0) on, where they are in the output.
 static __device__ __noinline__ void store_nan(const TileArgs& a, int i, int row0, int rows, int col0, int cols)
 {
-    for (int r = row0; r < min(row0 + rows, a.rows); ++r)
-        for (int c = col0 + (threadIdx.x & 31); c < min(col0 + cols, a.cols); c += 32) {
-            const long long at = static_cast<long long>(r) * a.ld[i] + c;
+    for (int r = 0; r < min(rows, a.rows - row0); ++r)  // (row0 + rows may be 2^31)
+        for (int c = threadIdx.x & 31; c < min(cols, a.cols - col0); c += 32) {
+            const long long at = static_cast<long long>(row0 + r) * a.ld[i] + col0 + c;
             if (a.out_kind == 0)
                 static_cast<uint32_t*>(a.out[i])[at] = 0x7FFFFFFFu;
             else
@@ -864,7 +864,7 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
             fence_proxy_async_smem();
             __syncwarp();
             // (A box that reaches past the last column overwrites the rest of that 16-byte piece with zeros.)
-            if (((args.tma_out >> i) & 1) && (col0 + (kind == 0 ? 32 : 64) <= args.cols || ((args.tma_edge >> i) & 1))) {
+            if (((args.tma_out >> i) & 1) && (args.cols - col0 >= (kind == 0 ? 32 : 64) || ((args.tma_edge >> i) & 1))) {
                 if (lane == 0 && row0 < args.rows && col0 < args.cols) {
                     if (T::EPI == kStore && args.add)
                         tma_add_2d(&maps.o[i], sb, col0, row0);
@@ -1035,7 +1035,7 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
                         p[q] = pack2(x[2 * q], x[2 * q + 1], kind);
-                    if (((args.tma_out >> i) & 1) && cc + 32 <= args.cols) {
+                    if (((args.tma_out >> i) & 1) && args.cols - cc >= 32) {
                         if (row0 + lane < args.rows) {
                             uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.out[i]) +
                                                                 static_cast<long long>(row0 + lane) * args.ld[i] + cc);
