@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "ffn_device.h"
 #include "ffn_tile.cuh"
 #include "rows.cuh"
 
@@ -41,34 +42,6 @@ constexpr int64_t kMost = INT64_C(1) << 31;
 
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 int64_t ceil_div(int64_t n, int64_t by) { return (n + by - 1) / by; }
-
-// The current device's SMs, or a status.
-int device_sms(int* sms)
-{
-    static std::atomic<int> known[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess)
-        return fail_with(GEMM_ERR_LAUNCH, "querying the device: %s", cudaGetErrorString(e));
-    int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
-    if (n == 0) {
-        int major = 0, minor = 0;
-        e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-        if (e == cudaSuccess)
-            e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-        if (e == cudaSuccess)
-            e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess)
-            return fail_with(GEMM_ERR_LAUNCH, "querying the device: %s", cudaGetErrorString(e));
-        if (major != 10 || minor != 3)
-            return fail_with(GEMM_ERR_ARCH, "device %d is compute capability %d.%d; this library is built for sm_103a only",
-                             dev, major, minor);
-        if (dev < 64)
-            known[dev].store(n, std::memory_order_relaxed);
-    }
-    *sms = n;
-    return GEMM_OK;
-}
 
 // One factor of a product: `extent` rows (or columns) of the output by k. mn:
 // extent is the contiguous one, else k is. Two pointers: two segments of k, two

@@ -4,6 +4,7 @@
 #include <climits>
 #include <type_traits>
 
+#include "ffn_device.h"
 #include "ffn_ptx.cuh"
 #include "ffn_tile.h"
 #include "rows.cuh"
@@ -382,7 +383,7 @@ int check(const mxfp4_args* a)
 }
 
 template <typename T, bool kQuantize>
-cudaError_t launch(const mxfp4_args& a, cudaStream_t s)
+cudaError_t launch(const mxfp4_args& a, int sms, cudaStream_t s)
 {
     Args k{};
     k.rows = static_cast<unsigned>(a.rows);
@@ -399,9 +400,9 @@ cudaError_t launch(const mxfp4_args& a, cudaStream_t s)
     k.scales = static_cast<uint4*>(a.scales);
     // CTAs with several sets of rows each, or, of many columns, one. Quantising, eight an SM (8192 x 8192 bf16 30.8 us; 32.2
     // with 32), and 32 the other way, whose stores want more of them under way (fp32 45.5 us; 51.0 with eight).
-    constexpr unsigned kCtas = (kQuantize ? 8 : 32) * 152;
+    const unsigned ctas = (kQuantize ? 8u : 32u) * static_cast<unsigned>(sms);
     const unsigned rows = kThreads / k.per_row, goes = (k.sets + rows - 1) / rows;
-    const unsigned most = k.chunks >= kCtas ? 1 : kCtas / k.chunks;
+    const unsigned most = k.chunks >= ctas ? 1 : ctas / k.chunks;
     const unsigned per_chunk = goes < most ? goes : most;
     k.stride = per_chunk * rows;
     const long long grid = static_cast<long long>(per_chunk) * k.chunks;
@@ -415,12 +416,17 @@ cudaError_t launch(const mxfp4_args& a, cudaStream_t s)
 }
 
 template <bool kQuantize>
-cudaError_t launch_as(const mxfp4_args& a, void* stream)
+int launch_as(const mxfp4_args& a, void* stream, const char* what)
 {
+    int sms = 0;
+    const int rc = ffn::device_sms(&sms);
+    if (rc)
+        return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return a.type == GEMM_C_F32    ? launch<float, kQuantize>(a, s)
-           : a.type == GEMM_C_BF16 ? launch<__nv_bfloat16, kQuantize>(a, s)
-                                   : launch<__half, kQuantize>(a, s);
+    const cudaError_t e = a.type == GEMM_C_F32    ? launch<float, kQuantize>(a, sms, s)
+                          : a.type == GEMM_C_BF16 ? launch<__nv_bfloat16, kQuantize>(a, sms, s)
+                                                  : launch<__half, kQuantize>(a, sms, s);
+    return e == cudaSuccess ? GEMM_OK : fail_with(GEMM_ERR_LAUNCH, "launching the %s: %s", what, cudaGetErrorString(e));
 }
 
 }  // namespace
@@ -441,8 +447,7 @@ int mxfp4_quantize(const mxfp4_args* args, void* stream)
     const int rc = check(args);
     if (rc || args->rows == 0 || args->width == 0)
         return rc;
-    const cudaError_t e = launch_as<true>(*args, stream);
-    return e == cudaSuccess ? GEMM_OK : fail_with(GEMM_ERR_LAUNCH, "launching the quantisation: %s", cudaGetErrorString(e));
+    return launch_as<true>(*args, stream, "quantisation");
 }
 
 int mxfp4_dequantize(const mxfp4_args* args, void* stream)
@@ -451,8 +456,7 @@ int mxfp4_dequantize(const mxfp4_args* args, void* stream)
     const int rc = check(args);
     if (rc || args->rows == 0 || args->width == 0)
         return rc;
-    const cudaError_t e = launch_as<false>(*args, stream);
-    return e == cudaSuccess ? GEMM_OK : fail_with(GEMM_ERR_LAUNCH, "launching the dequantisation: %s", cudaGetErrorString(e));
+    return launch_as<false>(*args, stream, "dequantisation");
 }
 
 }  // extern "C"
