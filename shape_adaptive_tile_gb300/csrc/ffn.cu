@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(256) sat_ffn_slope_kernel(const SlopeArgs a, c
         for (int i = 0; i < 8; ++i) {
             const float dv = to_f32(reinterpret_cast<const T*>(d.w)[i]);
             float v, slope;
-            act_grad<decltype(k)::value>(to_f32(reinterpret_cast<const T*>(g.w)[i]), v, slope);
+            act_grad<decltype(k)::value, false>(to_f32(reinterpret_cast<const T*>(g.w)[i]), v, slope);
             reinterpret_cast<T*>(dg.w)[i] = from_f32<T>(dv * to_f32(reinterpret_cast<const T*>(u.w)[i]) * slope);
             reinterpret_cast<T*>(du.w)[i] = from_f32<T>(dv * v);
         }

@@ -107,29 +107,31 @@ __device__ __forceinline__ float power_of_two(float x)
     return r;
 }
 
-// exp(by (x + low)), of by (x + low) from -150 to 0 with a `low` below x's last place: the square of a power of two with half
-// the exponent, which is no number below the normal ones where the result is, and what the exponent's roundings (its own and
-// the constant's) left out as a factor 1 + ... .
-template <bool kLow>
+// exp(by x), of by x from -150 to 0: the square of a power of two with half the exponent, which is no number below the normal
+// ones where the result is. kFine: by (x + low), and what the exponent's roundings (its own and the constant's) left out comes
+// in as a factor 1 + ... . Without it the result is off by up to 2^-23.7 of itself times by x (and 2^-24 times by x where x
+// was rounded): 1.2e-5 at most where an fp32 result ends, which an output rounded to 16 bits (2^-9 or 2^-12) does not show. It
+// is for fp32 outputs: 4-bit gated 2049 x 4096 x 8200 to fp16 took 68.7 us with it and 66.6 without, gradients recomputed 2048
+// x 1024 x 4096 96.1 and 94.0.
+template <bool kFine>
 __device__ __forceinline__ float exp_product(float x, float low, double by)
 {
     const double factor = 0.72134752044448170 * by;  // log2(e) / 2
     const float c = static_cast<float>(factor), rest = static_cast<float>(factor - c);
     const float y = c * x;
-    float off = fmaf(rest, x, fmaf(c, x, -y));
-    if constexpr (kLow)
-        off = fmaf(c, low, off);
     const float e = power_of_two(y);
+    if constexpr (!kFine)
+        return e * e;
+    const float off = fmaf(rest, x, fmaf(c, low, fmaf(c, x, -y)));
     return fmaf(1.3862943611198906f * off, e, e) * e;
 }
 
-// s = 1 / (1 + exp(-x)) and o = 1 - s, each to some 16 of fp32's half steps of itself: from exp(-|x|), which does not overflow.
-// (Left of -87 a quotient by 1 + exp(-x) is 0 or lost where s is a number yet. By __expf and __fdividef, which are off by 5e-6
-// at -80 besides, the epilogue has two or three instructions less: 4-bit gated 2049 x 4096 x 8200 66.4 us, 68.0 with this;
-// gradients recomputed 2048 x 1024 x 4096 90 and 94; 2047 x 1000 to 2 x 2501 with the pre-activations 34 either way.)
+// s = 1 / (1 + exp(-x)) and o = 1 - s, each with a small error relative to itself: from exp(-|x|), which does not overflow.
+// (Left of -87 a quotient by 1 + exp(-x) is 0 or lost where s is a number yet.)
+template <bool kFine>
 __device__ __forceinline__ void logistic(float x, float& s, float& o)
 {
-    const float e = exp_product<false>(fminf(fabsf(x), 150.0f), 0.0f, -1.0);
+    const float e = exp_product<kFine>(fminf(fabsf(x), 150.0f), 0.0f, -1.0);
     const float r = reciprocal(1.0f + e);
     s = x < 0.0f ? e * r : r;
     o = x < 0.0f ? r : e * r;
@@ -137,13 +139,13 @@ __device__ __forceinline__ void logistic(float x, float& s, float& o)
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi, int kind);
 
-// a(g) and a'(g) of the activation KIND (ffn_activation_t).
-template <int KIND>
+// a(g) and a'(g) of the activation KIND (ffn_activation_t), for outputs in fp32 (kFine) or of 16 bits.
+template <int KIND, bool kFine>
 __device__ __forceinline__ void act_grad(float g, float& a, float& d)
 {
     if constexpr (KIND == 1) {
         float s, o;
-        logistic(g, s, o);
+        logistic<kFine>(g, s, o);
         a = g * s;
         d = s * fmaf(g, o, 1.0f);
     } else if constexpr (KIND == 2) {
@@ -151,13 +153,11 @@ __device__ __forceinline__ void act_grad(float g, float& a, float& d)
         // with t = 1 / (1 + 0.27 x), the form of Hastings, Approximations for Digital Computers, with coefficients of this
         // file's own, fitted by least squares reweighted to the smallest relative error, 2.5e-8 for x from 0 to 16. Below 0 the
         // activation is that tail itself, so its error has to be relative too, some 20 of fp32's half steps. (From 14.5 on phi
-        // is 0 in fp32; infinities stay out of the products.) The derivative wants phi too. A form with a small absolute error,
-        // 26.2.17 of Abramowitz and Stegun, is as fast (2047 x 1000 to 2 x 2501 with the pre-activations 37 us either way;
-        // 4-bit 2048 x 512 to 2 x 4096 22.5 us, 23.2 with this) and off by 0.4% at -6; with expf the latter takes 25 us.
+        // is 0 in fp32; infinities stay out of the products.) The derivative wants phi too.
         const float x = fminf(fabsf(g), 16.0f);
         const float t = reciprocal(fmaf(0.27f, x, 1.0f));
         const float h = x * x;
-        const float phi = 0.39894228040143268f * exp_product<true>(h, fmaf(x, x, -h), -0.5);
+        const float phi = 0.39894228040143268f * exp_product<kFine>(h, fmaf(x, x, -h), -0.5);
         float q = fmaf(0.0727893636f, t, -0.318029493f);
         q = fmaf(q, t, 0.427678317f);
         q = fmaf(q, t, -0.175963894f);
@@ -172,7 +172,7 @@ __device__ __forceinline__ void act_grad(float g, float& a, float& d)
         d = fmaf(g, phi, c);
     } else if constexpr (KIND == 3) {  // (1 + tanh y) / 2 = 1 / (1 + exp(-2 y))
         float s, o;
-        logistic(1.5957691216057308f * fmaf(0.044715f * g * g, g, g), s, o);
+        logistic<kFine>(1.5957691216057308f * fmaf(0.044715f * g * g, g, g), s, o);
         a = g * s;
         // (g^2 is held to what no s (1 - s) but 0 meets, or it would overflow to 0 times infinity.)
         d = fmaf(a * o, 1.5957691216057308f * fmaf(0.134145f, fminf(g * g, 1e6f), 1.0f), s);
@@ -204,17 +204,27 @@ __device__ __forceinline__ void with_act(int kind, F f)
 }
 
 // g = a(g) u
-template <int N>
-__device__ __forceinline__ void gate(float (&g)[N], const float (&u)[N], int kind)
+template <bool kFine, int N>
+__device__ __forceinline__ void gate_as(float (&g)[N], const float (&u)[N], int kind)
 {
     with_act(kind, [&](auto k) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             float a, d;
-            act_grad<decltype(k)::value>(g[j], a, d);
+            act_grad<decltype(k)::value, kFine>(g[j], a, d);
             g[j] = a * u[j];
         }
     });
+}
+
+// (fp32 outputs: of 4-bit operands only)
+template <class T, int N>
+__device__ __forceinline__ void gate(float (&g)[N], const float (&u)[N], int kind, int out_kind)
+{
+    if (T::MX && out_kind == 0)
+        gate_as<true>(g, u, kind);
+    else
+        gate_as<false>(g, u, kind);
 }
 
 __device__ __forceinline__ void unpack2(uint32_t v, int kind, float& lo, float& hi);
@@ -230,7 +240,7 @@ __device__ __forceinline__ void slope(float (&g)[32], float (&u)[32], const uint
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float a, s;
-                act_grad<decltype(k)::value>(g[2 * j + e], a, s);
+                act_grad<decltype(k)::value, false>(g[2 * j + e], a, s);
                 g[2 * j + e] = d[e] * u[2 * j + e] * s;
                 u[2 * j + e] = d[e] * a;
             }
@@ -968,8 +978,8 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                         stage16(v[3], 32);
                         put(2, row0, first);
                     }
-                    gate(v[0], v[2], activation);
-                    gate(v[1], v[3], activation);
+                    gate<T>(v[0], v[2], activation, kind);
+                    gate<T>(v[1], v[3], activation, kind);
                 }
                 if (T::MX && kind == 0) {  // (fp32 outputs: of 4-bit operands only)
 #pragma unroll
@@ -1015,7 +1025,7 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                             store_column(args.out[1], kind, tok0 * args.ld[1] + f, args.ld[1], n, g);
                             store_column(args.out[2], kind, tok0 * args.ld[2] + f, args.ld[2], n, u);
                         }
-                        gate(g, u, activation);
+                        gate<T>(g, u, activation, kind);
                     }
                     store_column(args.out[0], kind, tok0 * args.ld[0] + f, args.ld[0], n, g);
                 }
@@ -1084,7 +1094,7 @@ __device__ __forceinline__ void tile_kernel(const TileMaps& maps, const ScaleMap
                                 out32(1, v, cc);
                                 out32(2, u, cc);
                             }
-                            gate(v, u, activation);
+                            gate<T>(v, u, activation, kind);
                             out32(0, v, cc);
                         } else {
                             uint32_t hw[16];  // this row's 32 values of dh (of the 64 that a box brings)
