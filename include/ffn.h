@@ -8,10 +8,11 @@
  * consecutive columns and a row stride in elements (of codes: in bytes).
  * Products are taken on the tensor cores with fp32 accumulators; activations
  * are computed in fp32 from these, off by at most 2^-19 of themselves for fp32
- * outputs and 2^-16 for others (GELU by tanh: by 2^-21 times the argument of its
- * exponential besides), and each output is rounded once, to nearest even. Every sum is taken in a fixed order, so results are identical from run
- * to run. Calls enqueue on `stream` without synchronising, may be captured
- * into a graph, and return 0 or a negative gemm_status_t with a message in
+ * outputs and 2^-16 for others (GELU by tanh: by 2^-21 times the argument of
+ * its exponential besides), and each output is rounded once, to nearest even.
+ * Every sum is taken in a fixed order, so results are identical from run to
+ * run. Calls enqueue on `stream` without synchronising, may be captured into a
+ * graph, and return 0 or a negative gemm_status_t with a message in
  * gemm_last_error(): GEMM_ERR_ARG for a bad size, stride, type or a missing
  * pointer, GEMM_ERR_ALIGN, GEMM_ERR_ARCH for a current device that is not of
  * compute capability 10.3 (all pointers belong to the current device),
@@ -19,8 +20,8 @@
  * that a ..._workspace function gives; concurrent calls need scratch of their
  * own. Waits inside the kernels are bounded: where a copy or a product has not
  * come after two seconds, which no launch takes, the outputs that hang on it
- * are NaN. Sizes (and twice `hidden`) are below 2^31, matrices of fewer than 2^56
- * elements, and no output may overlap an input or another output.
+ * are NaN. Sizes (and twice `hidden`) are below 2^31, matrices of fewer than
+ * 2^56 elements, and no output may overlap an input or another output.
  */
 #ifndef SAT_FFN_H
 #define SAT_FFN_H

@@ -17,11 +17,13 @@
 // columns (in a pair, each CTA loads one half), or, swapped, as two accumulators.
 //
 // What bounds them, and what they take:
-//   - 16-bit pairs' tiles: the tensor pipe, 86% busy (2048 x 4096 to 2 x 8192, 147 us), and, back to back, the power: 8192 x
-//     4096 to 2 x 16384 in 1240 us, 1.77 PFLOP/s. Of outputs off 16 bytes the epilogue: 2047 x 1000 to 2 x 2501 with the
-//     pre-activations 36 us, the tensor pipe 25% busy.
-//   - 4-bit pairs' tiles: the operands' way from L2 to shared memory, some 600 cycles for a stage of 512 cycles of products,
-//     and the drain of the one accumulator: 8192 x 8192 x 8192 in 185 us, 5.9 PFLOP/s.
+//   - 16-bit pairs' tiles: the tensor pipe, 87% busy (2048 x 4096 to 2 x 8192, 144 us), and, back to back, the power: 8192 x
+//     4096 to 2 x 16384 in 1230 us, 1.79 PFLOP/s. Of outputs off 16 bytes the epilogue: 2047 x 1000 to 2 x 2501 with the
+//     pre-activations 34 us, the tensor pipe 26% busy.
+//   - 4-bit pairs' tiles: 600 cycles a stage, of which the products are 512 at four times the rate of 16 bits and the loads
+//     from L2 436 when nothing else runs (8192 of k); what keeps both from running side by side has not been measured, the
+//     products of a stage waiting for the next stage's scales is one candidate. Then the drain of the one accumulator:
+//     8192 x 8192 x 8192 in 185 us, 5.9 PFLOP/s.
 //   - a few tokens: memory. One token, 4096 to 2 x 16384, in 45 us, 6.0 TB/s; 48 tokens, 2048 to 2 x 8192, in 17 us, of which 5
 //     are the launch, the first loads and the last stores.
 //   - shared 128 x 128 tiles: loads, 0.22 us for a stage of 32 KB a CTA, then the sums' way between the CTAs, 0.8 us and 0.65
