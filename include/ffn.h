@@ -8,8 +8,9 @@
  * consecutive columns and a row stride in elements (of codes: in bytes).
  * Products are taken on the tensor cores with fp32 accumulators; activations
  * are computed in fp32 from these, off by at most 2^-19 of themselves for fp32
- * outputs and 2^-16 for others (GELU by tanh: by 2^-21 times the argument of
- * its exponential besides), and each output is rounded once, to nearest even.
+ * outputs and 2^-16 for others, as far as they are normal numbers of fp32 (GELU
+ * by tanh: by 2^-21 times the argument of its exponential besides), and each
+ * output is rounded once, to nearest even.
  * Every sum is taken in a fixed order, so results are identical from run to
  * run. Calls enqueue on `stream` without synchronising, may be captured into a
  * graph, and return 0 or a negative gemm_status_t with a message in
